@@ -458,6 +458,79 @@ int moe_mx_route_ffn_combine(const uint16_t *x, int T, int H, int I, const float
                              float *topk_w, uint16_t *out, void *workspace, size_t workspace_bytes,
                              const void *prefetch, size_t prefetch_bytes, void *stream);
 
+/* ------------------------------------------------------------------ dense MXFP4 operators
+ * What stands around the routed experts in a layer: making MXFP4 rows, products
+ * with MXFP4 weights (projections, dense layers, logits) and the norms between
+ * blocks.  Element and scale encodings per the OCP Microscaling Formats v1.0
+ * spec, rows as in the MXFP4 section above, so a quantised matrix is a slab's
+ * matrix and a slab's matrix is an operand of the product.
+ * Strides are bytes between rows; a stride of one row is not read.  Every pointer
+ * belongs to the current device, which is the stream's.  Calls share nothing: any
+ * number may be in flight, and all can be captured into graphs. */
+enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2, MOE_MXFP4 = 3 };       /* element types */
+enum { MOE_MX_SCALE_FLOOR = 0, MOE_MX_SCALE_FIT = 1 };                   /* block scale rules */
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_ROW = 2, MOE_GATE_ELEMENT = 3 };
+
+/* Bytes of an MXFP4 row of K columns: K/2 code bytes, K/32 scale bytes, zero
+   padding to a multiple of 16; 0 unless K is a positive multiple of 32. */
+size_t moe_mx_row_bytes(int K);
+/* Rows of bf16, fp16 or fp32 values -> MXFP4 rows.  Per block of 32 columns, with
+ * 2^e <= max|x| < 2^(e+1):
+ *   scale byte v = e + 125 (MOE_MX_SCALE_FLOOR, the OCP spec's conversion: the
+ *     largest value lands in [4, 8) and saturates at 6), one more where max|x| >
+ *     6 * 2^(e-2) (MOE_MX_SCALE_FIT: no value saturates), at least 0;
+ *   code = x / 2^(v-127) to the nearest E2M1 value, ties to the even code, beyond
+ *     6 to 6; the sign is kept for zeros too.
+ * A block with an infinity or a NaN becomes v = 255 (NaN) with codes 0.
+ * x [rows, K] of x_type (MOE_BF16, MOE_FP16 or MOE_FP32), out [rows] MXFP4 rows
+ * (the padding is written too; a slab's gate rows lie 2 * moe_mx_row_bytes(H)
+ * apart), values [rows, K] bf16 contiguous or NULL: what the codes stand for
+ * (exact, infinite beyond bf16's range).  MOE_E_SHAPE unless K % 32 == 0 and the
+ * strides hold a row; MOE_E_ARG for rows < 0, an unknown type or rule, a NULL
+ * pointer, or pointers or strides that are not multiples of 16 bytes; rows = 0
+ * is a no-op.  x, out and values must not overlap. */
+int moe_mx_quant(const void *x, int x_type, int64_t x_stride, int rows, int K, int scale_rule, uint8_t *out,
+                 int64_t out_stride, uint16_t *values, void *stream);
+/* y[m,n] = sum_k A[m,k] * W[n,k] + bias[n], sums in fp32, rounded once.
+ * a [M, K]: bf16 (a_type MOE_BF16; the weights are then formed in bf16, exact for
+ * scale bytes up to 252) or MXFP4 rows (MOE_MXFP4); w [N] MXFP4 rows; bias [N]
+ * fp32 or NULL; y [M, N] bf16 or fp32 (y_type).  Any M, N >= 0 (0: a no-op), K %
+ * 32 == 0.  A scale byte of 255 makes every output it enters NaN.  A row of y
+ * does not depend on the other rows of a, but its last bits may depend on M
+ * (which kernel runs).  workspace: moe_mx_matmul_workspace_bytes(M, N, K,
+ * a_type) bytes (contents don't care, 16-byte aligned; calls sharing it must not
+ * overlap in time; NULL when 0).  MOE_E_SHAPE for a bad K or a stride below its
+ * row; MOE_E_ARG for negative sizes, unknown types, NULL pointers, a or w
+ * pointers or strides that are not multiples of 16 bytes, or y and bias not
+ * aligned to their types; MOE_E_NOMEM for a small workspace.  y must not overlap
+ * the inputs. */
+size_t moe_mx_matmul_workspace_bytes(int M, int N, int K, int a_type);
+int moe_mx_matmul(const void *a, int a_type, int64_t a_stride, const uint8_t *w, int64_t w_stride, int M, int N, int K,
+                  const float *bias, void *y, int y_type, int64_t y_stride, void *workspace, size_t workspace_bytes,
+                  void *stream);
+/* The norms before and after a block, its gate and its residual scale, per token
+ * row t (moe_residual_norm with learned weights and a block's other half):
+ *   d = float(add[t,:])                                    (the block's output)
+ *   d = d / sqrt(mean(d^2) + eps) * w_post                 (post_norm != 0; w_post NULL = ones)
+ *   d = d * gate                                           (by gate_kind)
+ *   resid_out[t,:] = resid[t,:] + scale * d                (rounded once to resid_type)
+ *   x_next[t,:] = bf16( resid_out / sqrt(mean(resid_out^2) + eps) * w_pre )   (w_pre NULL = ones)
+ * add [T,H] bf16, or NULL: only the last line, of resid, and resid_out is not
+ * written; gate: fp32 [H] (MOE_GATE_CHANNEL), fp32 [T] (MOE_GATE_ROW) or bf16
+ * [T,H] (MOE_GATE_ELEMENT); resid, resid_out [T,H] of resid_type (MOE_FP32 or
+ * MOE_BF16; the same buffer or two that do not overlap); w_post, w_pre [H] fp32;
+ * x_next [T,H] bf16 or NULL; x_rows [T] contiguous MXFP4 rows of x_next's values
+ * (as moe_mx_quant makes them from x_next, floor rule) or NULL; both may be NULL
+ * after the last block.  Sums are fp32 in a fixed order.  x_next and x_rows must
+ * not overlap the inputs.  A row of zeros with eps = 0 gives NaN.
+ * MOE_E_ARG for T < 0, H <= 0, eps outside [0, 1], an unknown type or gate kind,
+ * w_post without post_norm, NULL pointers, or a pointer not aligned to its type;
+ * with x_rows MOE_E_SHAPE unless H % 32 == 0 and MOE_E_ARG unless every pointer is
+ * 16-byte aligned; MOE_E_SHAPE for H above 2^28; T = 0 is a no-op. */
+int moe_block_norm(const uint16_t *add, int post_norm, const float *w_post, const void *gate, int gate_kind,
+                   float scale, const void *resid, void *resid_out, int resid_type, const float *w_pre, int T, int H,
+                   float eps, uint16_t *x_next, uint8_t *x_rows, void *stream);
+
 /* ------------------------------------------------------------------ super-block weights
  * A k-quant-style format (the pages' own weights are a 4-bit k-quant GGUF
  * variant: LayerStoRm README, "TL;DR" and "Serve"; this layout is this

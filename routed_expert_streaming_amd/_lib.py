@@ -17,6 +17,9 @@ LIB_PATH = os.environ.get("MOE_LIB_PATH") or os.path.join(_HERE, "libmoe.so")
 
 MOE_OK, MOE_E_ARG, MOE_E_SHAPE, MOE_E_NOT_PINNED, MOE_E_NOMEM, MOE_E_CAPACITY, MOE_E_HIP, MOE_E_STATE = \
     0, -1, -2, -3, -4, -5, -6, -7
+MOE_BF16, MOE_FP16, MOE_FP32, MOE_MXFP4 = 0, 1, 2, 3
+MOE_MX_SCALE_FLOOR, MOE_MX_SCALE_FIT = 0, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_ROW, MOE_GATE_ELEMENT = 0, 1, 2, 3
 MOE_FFN_AUTO, MOE_FFN_PAIRS, MOE_FFN_GROUPED, MOE_FFN_MFMA, MOE_FFN_SPLIT = 0, 1, 2, 3, 4
 
 _lib = None
@@ -47,6 +50,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         _check_single_hip_runtime()
         vp, i, sz, u64p = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.POINTER(ctypes.c_uint64)
+        i64 = ctypes.c_int64
         sig = {
             "moe_status_str": ([i], ctypes.c_char_p),
             "moe_last_hip_error": ([], i),
@@ -98,6 +102,11 @@ def lib():
             "moe_sb_route_ffn_combine": ([vp, i, i, i, vp, vp, i, i, vp, vp, vp, vp, vp, vp, sz, vp, sz, vp], i),
             "moe_mx_expert_ffn_combine": ([vp, i, i, i, i, vp, vp, i, vp, vp, vp, vp, sz, vp], i),
             "moe_mx_route_ffn_combine": ([vp, i, i, i, vp, vp, i, i, vp, vp, vp, vp, vp, vp, sz, vp, sz, vp], i),
+            "moe_mx_row_bytes": ([i], sz),
+            "moe_mx_quant": ([vp, i, i64, i, i, i, vp, i64, vp, vp], i),
+            "moe_mx_matmul_workspace_bytes": ([i, i, i, i], sz),
+            "moe_mx_matmul": ([vp, i, i64, vp, i64, i, i, i, vp, vp, i, i64, vp, sz, vp], i),
+            "moe_block_norm": ([vp, i, vp, vp, i, ctypes.c_float, vp, vp, i, vp, i, i, ctypes.c_float, vp, vp, vp], i),
             "moe_cpu_lane_create": ([i, ctypes.POINTER(vp)], i),
             "moe_cpu_lane_submit": ([vp, vp, i, i, i, vp, vp, u64p], i),
             "moe_cpu_lane_wait": ([vp, ctypes.c_uint64], i),
@@ -491,6 +500,33 @@ def moe_mx_route_ffn_combine(x, T, H, I, w_router, bias, E, k, expert_table, sha
                                           _ptr(shared_slab), _ptr(topk_idx), _ptr(topk_w), _ptr(out), _ptr(workspace),
                                           workspace_bytes, _ptr(prefetch), prefetch_bytes, _stream(stream)),
            "moe_mx_route_ffn_combine")
+
+
+# ----------------------------------------------------------------------- dense MXFP4 operators
+def moe_mx_row_bytes(K: int) -> int:
+    return lib().moe_mx_row_bytes(K)
+
+
+def moe_mx_quant(x, x_type, x_stride, rows, K, scale_rule, out, out_stride, values=None, stream=None):
+    _check(lib().moe_mx_quant(_ptr(x), x_type, x_stride, rows, K, scale_rule, _ptr(out), out_stride, _ptr(values),
+                              _stream(stream)), "moe_mx_quant")
+
+
+def moe_mx_matmul_workspace_bytes(M: int, N: int, K: int, a_type: int) -> int:
+    return lib().moe_mx_matmul_workspace_bytes(M, N, K, a_type)
+
+
+def moe_mx_matmul(a, a_type, a_stride, w, w_stride, M, N, K, bias, y, y_type, y_stride, workspace=None,
+                  workspace_bytes=0, stream=None):
+    _check(lib().moe_mx_matmul(_ptr(a), a_type, a_stride, _ptr(w), w_stride, M, N, K, _ptr(bias), _ptr(y), y_type,
+                               y_stride, _ptr(workspace), workspace_bytes, _stream(stream)), "moe_mx_matmul")
+
+
+def moe_block_norm(add, post_norm, w_post, gate, gate_kind, scale, resid, resid_out, resid_type, w_pre, T, H, eps,
+                   x_next, x_rows=None, stream=None):
+    _check(lib().moe_block_norm(_ptr(add), int(bool(post_norm)), _ptr(w_post), _ptr(gate), gate_kind, scale,
+                                _ptr(resid), _ptr(resid_out), resid_type, _ptr(w_pre), T, H, eps, _ptr(x_next),
+                                _ptr(x_rows), _stream(stream)), "moe_block_norm")
 
 
 # ----------------------------------------------------------------------- super-block weights

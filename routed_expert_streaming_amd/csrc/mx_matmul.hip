@@ -45,10 +45,12 @@ __device__ __forceinline__ float scale_f32(uint32_t v) {
     return v == 255u ? __builtin_nanf("") : __uint_as_float(v ? v << 23 : 0x00400000u);
 }
 
+// One product of 16 x 16 x 128; byte B of ws / as is the lane's block's scale.
+template <int B>
 __device__ __forceinline__ f32x4_t mfma_mx(const uint4 w, const uint4 a, f32x4_t c, int ws, int as) {
     const i32x8_t wv{(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
     const i32x8_t av{(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, c, 4, 4, 0, ws, 0, as);  // 4: FP4 E2M1
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, c, 4, 4, B, ws, B, as);  // 4: FP4 E2M1
 }
 
 // Four outputs n .. n+3 of row m (those below N), bias added, rounded once.
@@ -118,7 +120,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_matmul_direct_kernel(Mat
                 uint32_t xs = load_stream_u8(ap[u] + half + b);
                 if (!in) x = make_uint4(0u, 0u, 0u, 0u), xs = 127u;
 #pragma unroll
-                for (int t = 0; t < NT; ++t) acc[t][u] = mfma_mx(w[t], x, acc[t][u], (int)ws[t], (int)xs);
+                for (int t = 0; t < NT; ++t) acc[t][u] = mfma_mx<0>(w[t], x, acc[t][u], (int)ws[t], (int)xs);
             }
         } else {
 #pragma unroll
@@ -163,18 +165,279 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_matmul_direct_kernel(Mat
         for (int u = 0; u < MT; ++u) store4(p, m0 + 16 * u + r, n0 + 16 * t + 4 * q, acc[t][u]);
 }
 
+// ---------------------------------------------------------------- many rows: tiles through LDS
+// A workgroup owns BM x BN outputs (WM x WN waves of MT x NT tiles of 16 x 16) and
+// walks K in groups of 128 columns through a ring of STAGES LDS stages, filled by
+// direct global -> LDS loads STAGES - 1 groups ahead.
+//  * MXFP4 rows: one load instruction brings a tile's 16 rows x 64 code bytes in
+//    lane order (lane 16q + r: block q of row r), which is the order the products
+//    read them in: 16 consecutive bytes per lane, no bank conflicts.
+//  * bf16 rows: one instruction brings 4 rows x 256 bytes; the 16-byte piece p of
+//    row m lies at place p ^ (m % 16), so that the 16 rows a product reads at one
+//    piece number lie in different banks.
+//  * scales: every fourth group, the 16 scale bytes of each row for the next four
+//    groups come in raw (4 bytes per group, one per quarter) and one thread per
+//    row turns them into one dword per quarter whose byte b belongs to group b:
+//    the products select it by its number (MXFP4) or shift it out (bf16).
+// The last group may end inside (K % 128 != 0): lanes past K load the last block
+// again, their operands become zeros and their scales 1.
+constexpr int kG = 128;          // columns of a group
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+__device__ __forceinline__ uint32_t lds_addr(const void *lds) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_u8 *)lds);
+}
+// Direct global -> LDS load of 16 bytes per lane: base (uniform) + off (this lane's
+// byte offset) -> LDS byte lds + 16 * lane.  Inline asm, because the compiler would
+// make every LDS read wait for all of these; the waits below count them instead
+// (a wave's loads complete in order).  s_nop 4: the wait states a vector memory
+// instruction needs after a VALU write of an SGPR it reads and after the M0 write.
+__device__ __forceinline__ void dma16(const void *base, uint32_t off, uint32_t lds) {
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
+// Waits until at most N of the wave's vector memory operations are in flight.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Workgroup barrier that leaves vector memory in flight; this wave's LDS accesses
+// are done when it arrives.
+__device__ __forceinline__ void ring_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int N>
+struct IntC {
+    static constexpr int value = N;
+};
+template <int B, int E, class F>
+__device__ __forceinline__ void static_for(F &&f) {
+    if constexpr (B < E) {
+        f(IntC<B>{});
+        static_for<B + 1, E>(f);
+    }
+}
+
+__device__ __forceinline__ uint4 zero_unless(bool keep, uint4 v) {
+    return make_uint4(keep ? v.x : 0u, keep ? v.y : 0u, keep ? v.z : 0u, keep ? v.w : 0u);
+}
+
+template <bool MX, int WM, int WN, int MT, int NT>
+struct Tile {
+    static constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, WAVES = WM * WN;
+    static constexpr int W_BYTES = BN * 64, A_BYTES = BM * (MX ? 64 : 256), STAGE = W_BYTES + A_BYTES;
+    static constexpr int SCALE_ROWS = BN + (MX ? BM : 0);  // rows of W, then rows of A
+    static constexpr int SCALE_LOADS = (SCALE_ROWS + 63) / 64;
+    static constexpr int SCALE_BYTES = SCALE_LOADS * 64 * 16;
+    static constexpr int LOADS = STAGE / 1024;                    // load instructions of a group
+    static constexpr int PER_WAVE = (LOADS + WAVES - 1) / WAVES;  // by each wave (some twice, see issue)
+    static constexpr int SCALES_PER_WAVE = (SCALE_LOADS + WAVES - 1) / WAVES;
+    static constexpr int STAGES = (160 * 1024 - 2 * SCALE_BYTES) / STAGE < 4 ? (160 * 1024 - 2 * SCALE_BYTES) / STAGE : 4;
+    static constexpr int LDS = STAGES * STAGE + 2 * SCALE_BYTES;
+    static_assert(STAGES >= 3 && LOADS >= WAVES && SCALE_ROWS <= 64 * WAVES, "tile does not fit its workgroup");
+};
+
+template <bool MX, int WM, int WN, int MT, int NT>
+__global__ __launch_bounds__(64 * WM * WN) void mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles) {
+    using T = Tile<MX, WM, WN, MT, NT>;
+    constexpr int AHEAD = T::STAGES - 1;
+    __shared__ uint4 smem4[T::LDS / 16];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(smem4);
+    uint8_t *raw = smem + T::STAGES * T::STAGE;              // 16 scale bytes per row
+    uint8_t *packed = raw + T::SCALE_BYTES;                  // four dwords per row, one per quarter
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
+    // consecutive workgroups go to the 8 XCDs in turn: each XCD takes a run of
+    // neighbouring tiles, m fastest, so that its L2 holds the W rows they share
+    const int tiles = m_tiles * n_tiles, per = (tiles + 7) / 8;
+    const int tile = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || tile >= tiles) return;
+    const int m0 = tile % m_tiles * T::BM, n0 = tile / m_tiles * T::BN;
+    const int ng = (p.K + kG - 1) / kG;
+    const int nq = (p.K - (ng - 1) * kG) / 32;  // blocks of the last group
+    const int m_last = min(T::BM, p.M - m0) - 1, n_last = min(T::BN, p.N - n0) - 1;
+    const uint8_t *wbase = p.w + (size_t)n0 * p.w_stride, *abase = p.a + (size_t)m0 * p.a_stride;
+    const uint32_t lds0 = lds_addr(smem), raw0 = lds_addr(raw);
+
+    // the wave's load instructions of a group: number c < LOADS fills KB c of the
+    // stage (W tiles first); past the end the wave repeats its previous one
+    uint32_t off[T::PER_WAVE], cut[T::PER_WAVE];  // lane offsets; what the last group's lanes step back by
+#pragma unroll
+    for (int j = 0; j < T::PER_WAVE; ++j) {
+        const int c0 = j * T::WAVES + wave, c = c0 < T::LOADS ? c0 : c0 - T::WAVES;
+        if (c < T::W_BYTES / 1024) {
+            off[j] = (uint32_t)min(16 * c + r, n_last) * (uint32_t)p.w_stride + 16 * q;
+            cut[j] = 16 * (q - min(q, nq - 1));
+        } else if (MX) {
+            off[j] = (uint32_t)min(16 * (c - T::W_BYTES / 1024) + r, m_last) * (uint32_t)p.a_stride + 16 * q;
+            cut[j] = 16 * (q - min(q, nq - 1));
+        } else {
+            const int m = 4 * (c - T::W_BYTES / 1024) + q, piece = r ^ (m & 15);
+            off[j] = (uint32_t)min(m, m_last) * (uint32_t)p.a_stride + 16 * piece;
+            cut[j] = 16 * (piece - min(piece, 4 * nq - 1));
+        }
+    }
+    auto issue = [&](int g) {
+        const uint32_t st = lds0 + (uint32_t)(g % T::STAGES) * T::STAGE;
+        const bool last = g == ng - 1;
+#pragma unroll
+        for (int j = 0; j < T::PER_WAVE; ++j) {
+            const int c0 = j * T::WAVES + wave, c = c0 < T::LOADS ? c0 : c0 - T::WAVES;
+            const bool w = c < T::W_BYTES / 1024;
+            const uint8_t *base = w ? wbase + 64 * (size_t)g : abase + (MX ? 64 : 256) * (size_t)g;
+            dma16(base, last ? off[j] - cut[j] : off[j], st + 1024u * c);
+        }
+    };
+    uint32_t soff[T::SCALES_PER_WAVE];
+#pragma unroll
+    for (int j = 0; j < T::SCALES_PER_WAVE; ++j) {
+        const int c0 = j * T::WAVES + wave, c = c0 < T::SCALE_LOADS ? c0 : c0 % T::SCALE_LOADS;
+        const int row = min(64 * c + lane, T::SCALE_ROWS - 1);
+        soff[j] = row < T::BN ? (uint32_t)min(row, n_last) * (uint32_t)p.w_stride
+                              : (uint32_t)min(row - T::BN, m_last) * (uint32_t)p.a_stride;
+    }
+    auto issue_scales = [&](int h) {  // of groups 4h .. 4h+3
+#pragma unroll
+        for (int j = 0; j < T::SCALES_PER_WAVE; ++j) {
+            const int c0 = j * T::WAVES + wave, c = c0 < T::SCALE_LOADS ? c0 : c0 % T::SCALE_LOADS;
+            const uint8_t *base = (64 * c < T::BN ? wbase : abase) + (size_t)p.K / 2 + 16 * (size_t)h;
+            dma16(base, soff[j], raw0 + 1024u * c);
+        }
+    };
+    static_assert(!MX || T::BN % 64 == 0, "a scale load is all W rows or all A rows");
+    auto pack_scales = [&](int h) {
+        if (tid >= T::SCALE_ROWS) return;
+        const uint4 v = reinterpret_cast<const uint4 *>(raw)[tid];
+        uint32_t d[4] = {v.x, v.y, v.z, v.w};  // d[b] byte q: group 4h + b, quarter q
+        const int in = p.K / 32 - 16 * h;      // blocks that exist
+        if (in < 16)
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (4 * b + k >= in) d[b] = (d[b] & ~(255u << 8 * k)) | 127u << 8 * k;
+        // 4 x 4 byte transposition
+        const uint32_t a0 = __builtin_amdgcn_perm(d[1], d[0], 0x05010400u), a1 = __builtin_amdgcn_perm(d[1], d[0], 0x07030602u);
+        const uint32_t b0 = __builtin_amdgcn_perm(d[3], d[2], 0x05010400u), b1 = __builtin_amdgcn_perm(d[3], d[2], 0x07030602u);
+        reinterpret_cast<uint4 *>(packed)[tid] =
+            make_uint4(__builtin_amdgcn_perm(b0, a0, 0x05040100u), __builtin_amdgcn_perm(b0, a0, 0x07060302u),
+                       __builtin_amdgcn_perm(b1, a1, 0x05040100u), __builtin_amdgcn_perm(b1, a1, 0x07060302u));
+    };
+
+    f32x4_t acc[NT][MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < MT; ++u) acc[t][u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    uint32_t sw[NT], sa[MT];
+
+    // issue order: scales 0, groups 0 .. AHEAD-1; then in group g: [scales of the
+    // next four when g % 4 == 0], group g + AHEAD
+    issue_scales(0);
+    wait_vm<0>();
+    for (int g = 0; g < AHEAD && g < ng; ++g) issue(g);
+    ring_barrier();
+    pack_scales(0);
+
+    auto group = [&](int g, auto b_const) {
+        constexpr int b = decltype(b_const)::value;  // g % 4
+        // group g has landed once only the loads issued after it are in flight
+        if (g + AHEAD - 1 < ng)
+            wait_vm<(AHEAD - 1) * T::PER_WAVE>();
+        else
+            wait_vm<0>();
+        ring_barrier();  // every wave's part of group g is there, and group g - 1 has been read
+        if (b == 0 && g + 4 < ng) issue_scales(g / 4 + 1);
+        if (g + AHEAD < ng) issue(g + AHEAD);
+        if (b == 0) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sw[t] = reinterpret_cast<const uint32_t *>(packed)[(wn * NT + t) * 64 + 4 * r + q];
+            if (MX)
+#pragma unroll
+                for (int u = 0; u < MT; ++u)
+                    sa[u] = reinterpret_cast<const uint32_t *>(packed)[4 * T::BN + (wm * MT + u) * 64 + 4 * r + q];
+        }
+        // the next four groups' scales: issued in this run's first group, so landed
+        // with this one's loads (with AHEAD <= 3 they were issued before those)
+        if (b == 3 && g + 1 < ng) pack_scales(g / 4 + 1);
+        const uint8_t *st = smem + (size_t)(g % T::STAGES) * T::STAGE;
+        const bool keep = g < ng - 1 || q < nq;
+        uint4 w[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            w[t] = zero_unless(keep, reinterpret_cast<const uint4 *>(st)[(wn * NT + t) * 64 + lane]);
+        if constexpr (MX) {
+            const uint4 *as = reinterpret_cast<const uint4 *>(st + T::W_BYTES) + wm * MT * 64 + lane;
+#pragma unroll
+            for (int u = 0; u < MT; ++u) {
+                const uint4 x = as[u * 64];  // past K: finite codes times W's zeros
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[t][u] = mfma_mx<b>(w[t], x, acc[t][u], (int)sw[t], (int)sa[u]);
+            }
+        } else {
+            const uint8_t *as = st + T::W_BYTES + (wm * MT * 16 + r) * 256;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                bf16x8_t wv[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint32_t c = s == 0 ? w[t].x : s == 1 ? w[t].y : s == 2 ? w[t].z : w[t].w;
+                    wv[t] = codes_bf16(c, scale_f32(sw[t] >> 8 * b & 255u));
+                }
+#pragma unroll
+                for (int u = 0; u < MT; ++u) {
+                    const uint4 x = zero_unless(
+                        keep, *reinterpret_cast<const uint4 *>(as + u * 16 * 256 + 16 * ((4 * q + s) ^ r)));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            wv[t], __builtin_bit_cast(bf16x8_t, x), acc[t][u], 0, 0, 0);
+                }
+            }
+        }
+    };
+    for (int g0 = 0; g0 < ng; g0 += 4)
+        static_for<0, 4>([&](auto b) {
+            if (g0 + decltype(b)::value < ng) group(g0 + decltype(b)::value, b);
+        });
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+            store4(p, m0 + (wm * MT + u) * 16 + r, n0 + (wn * NT + t) * 16 + 4 * q, acc[t][u]);
+}
+
 template <bool MX, int MT, int NT, int WM, int WN, int WK>
 void launch_direct(const MatArgs &p, hipStream_t s) {
     const dim3 grid((p.N + 16 * NT * WN - 1) / (16 * NT * WN), (p.M + 16 * MT * WM - 1) / (16 * MT * WM));
     hipLaunchKernelGGL((mx_matmul_direct_kernel<MX, MT, NT, WM, WN, WK>), grid, dim3(64 * WM * WN * WK), 0, s, p);
 }
 
+template <bool MX, int WM, int WN, int MT, int NT>
+void launch_tile(const MatArgs &p, hipStream_t s) {
+    using T = Tile<MX, WM, WN, MT, NT>;
+    const int m_tiles = (p.M + T::BM - 1) / T::BM, n_tiles = (p.N + T::BN - 1) / T::BN;
+    const unsigned grid = (unsigned)(((int64_t)m_tiles * n_tiles + 7) / 8 * 8);
+    hipLaunchKernelGGL((mx_matmul_tile_kernel<MX, WM, WN, MT, NT>), dim3(grid), dim3(64 * T::WAVES), 0, s, p,
+                       m_tiles, n_tiles);
+}
+
 template <bool MX>
 void launch(const MatArgs &p, hipStream_t s) {
+    // a tile's lane offsets are 32 bits: rows further apart take the direct kernel
+    const bool near = p.w_stride < (8u << 20) && p.a_stride < (8u << 20);
     if (p.M <= 16)
         launch_direct<MX, 1, 1, 1, 1, 4>(p, s);
-    else
+    else if (p.M <= 64 || !near)
         launch_direct<MX, 4, 4, 2, 2, 1>(p, s);
+    else if constexpr (MX)
+        launch_tile<MX, 2, 4, 8, 3>(p, s);
+    else
+        launch_tile<MX, 2, 4, 4, 4>(p, s);
 }
 
 }  // namespace

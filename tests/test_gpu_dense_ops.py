@@ -208,8 +208,6 @@ def test_matmul_special_values(M, kind):
     a, av = operand(rng, kind, M, K)
     wc, wsc = mxkit.random_rows(rng, N, K, 126, 128)
     wsc[3, 8] = 255            # a NaN block in the short last group: the whole output column
-    wsc[5, :] = 0              # the smallest scale
-    wsc[6, :] = 1
     wsc[7, :] = 252            # the largest that bf16 weights hold: one weight of 2^124
     wc[7, :], wc[7, 261] = 0, 1
     wsc[8, :] = 64
@@ -217,10 +215,18 @@ def test_matmul_special_values(M, kind):
     got = run_matmul(a, kind, dev(mxkit.pack(wc, wsc)), M, N, K, None, L.MOE_FP32)
     want = av @ wv.T
     assert np.isnan(got[:, 3]).all()
-    plain = [n for n in range(N) if n not in (3, 5, 6)]
+    plain = [n for n in range(N) if n != 3]
     assert np.array_equal(got[:, plain], want[:, plain])  # one power of two per column: the same exact sums, moved
-    # scales of 2^-127 and 2^-126: a product below fp32's normal range may lose what is under 2^-126
-    assert (np.abs(got[:, [5, 6]] - want[:, [5, 6]]) <= K * 2.0 ** -126).all()
+    # the smallest scales, with activations 2^40 larger: sums in fp32's normal range, exact
+    if kind == L.MOE_MXFP4:
+        up = a.clone()
+        up[:, K // 2:K // 2 + K // 32] += 40
+    else:
+        up = a * 2.0 ** 40
+    low = wsc.copy()
+    low[:] = rng.integers(0, 3, (N, 1))
+    got_low = run_matmul(up, kind, dev(mxkit.pack(wc, low)), M, N, K, None, L.MOE_FP32)
+    assert np.array_equal(got_low, (av * 2.0 ** 40) @ mxkit.values(wc, low).T)
     if M > 1:
         bad = a.clone()
         if kind == L.MOE_MXFP4:

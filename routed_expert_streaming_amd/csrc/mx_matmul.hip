@@ -22,12 +22,8 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
-#ifndef MOE_TCFG
-#define MOE_TCFG 2, 4, 8, 3
-#endif
-#ifndef MOE_BCFG
-#define MOE_BCFG 2, 4, 4, 4
-#endif
+constexpr int64_t kMaxStride = 1 << 28;  // 16 rows' offsets stay in 32 bits
+
 struct MatArgs {
     const uint8_t *a, *w;
     size_t a_stride, w_stride;  // bytes between rows
@@ -59,6 +55,12 @@ __device__ __forceinline__ f32x4_t mfma_mx(const uint4 w, const uint4 a, f32x4_t
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, c, 4, 4, B, ws, B, as);  // 4: FP4 E2M1
 }
 
+// Two floats -> bf16 pair, rounded to nearest even, lo in bits 0-15 (one instruction).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return __builtin_bit_cast(
+        uint32_t, __builtin_convertvector((float __attribute__((ext_vector_type(2)))){lo, hi}, moe_bf16x2));
+}
+
 // Four outputs n .. n+3 of row m (those below N), bias added, rounded once.
 __device__ __forceinline__ void store4(const MatArgs &p, int m, int n, const f32x4_t v) {
     if (m >= p.M) return;
@@ -78,117 +80,14 @@ __device__ __forceinline__ void store4(const MatArgs &p, int m, int n, const f32
     } else {
         uint16_t *o = (uint16_t *)row + n;
         if (n + 3 < p.N && (uintptr_t)o % 8 == 0) {
-            *reinterpret_cast<uint2 *>(o) = make_uint2(f32_to_bf16_bits(f[0]) | f32_to_bf16_bits(f[1]) << 16,
-                                                       f32_to_bf16_bits(f[2]) | f32_to_bf16_bits(f[3]) << 16);
+            *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (n + j < p.N) o[j] = (uint16_t)f32_to_bf16_bits(f[j]);
+                if (n + j < p.N) o[j] = (uint16_t)pack_bf16(f[j], 0.0f);
         }
     }
 }
-
-// Waves WM x WN x WK; a wave owns MT tiles of A rows, NT tiles of W rows and every
-// WK-th group of K.  Rows past M or N repeat the last row (their results are not
-// stored); columns past K enter as zeros.
-template <bool MX, int MT, int NT, int WM, int WN, int WK>
-__global__ __launch_bounds__(64 * WM * WN * WK) void mx_matmul_direct_kernel(MatArgs p) {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-    const int wk = wave / (WM * WN), wm = wave / WN % WM, wn = wave % WN;
-    const int m0 = (blockIdx.y * WM + wm) * 16 * MT, n0 = (blockIdx.x * WN + wn) * 16 * NT;
-    const uint8_t *wp[NT], *ap[MT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) wp[t] = p.w + (size_t)min(n0 + 16 * t + r, p.N - 1) * p.w_stride;
-#pragma unroll
-    for (int t = 0; t < MT; ++t) ap[t] = p.a + (size_t)min(m0 + 16 * t + r, p.M - 1) * p.a_stride;
-    f32x4_t acc[NT][MT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int u = 0; u < MT; ++u) acc[t][u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    const size_t half = (size_t)p.K / 2;
-    const int ng = (p.K + 127) / 128;
-    for (int g = wk; g < ng; g += WK) {
-        const bool in = 128 * g + 32 * q < p.K;
-        const int b = in ? 4 * g + q : 0;  // block of 32 columns
-        uint4 w[NT];
-        uint32_t ws[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            w[t] = load_global_u4(wp[t] + 16 * (size_t)b);
-            ws[t] = load_stream_u8(wp[t] + half + b);
-            if (!in) w[t] = make_uint4(0u, 0u, 0u, 0u), ws[t] = 127u;
-        }
-        if constexpr (MX) {
-#pragma unroll
-            for (int u = 0; u < MT; ++u) {
-                uint4 x = load_global_u4(ap[u] + 16 * (size_t)b);
-                uint32_t xs = load_stream_u8(ap[u] + half + b);
-                if (!in) x = make_uint4(0u, 0u, 0u, 0u), xs = 127u;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) acc[t][u] = mfma_mx<0>(w[t], x, acc[t][u], (int)ws[t], (int)xs);
-            }
-        } else {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                bf16x8_t wv[NT];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const uint32_t c = s == 0 ? w[t].x : s == 1 ? w[t].y : s == 2 ? w[t].z : w[t].w;
-                    wv[t] = codes_bf16(c, scale_f32(ws[t]));
-                }
-#pragma unroll
-                for (int u = 0; u < MT; ++u) {
-                    uint4 x = load_global_u4(ap[u] + 64 * (size_t)b + 16 * s);
-                    if (!in) x = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            wv[t], __builtin_bit_cast(bf16x8_t, x), acc[t][u], 0, 0, 0);
-                }
-            }
-        }
-    }
-    if constexpr (WK > 1) {
-        // join: wave wk > 0 leaves its sums in LDS, wave 0 of each (wm, wn) adds them in order
-        __shared__ f32x4_t part[(WK - 1) * WM * WN][NT * MT][64];
-        if (wk > 0)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int u = 0; u < MT; ++u) part[wave - WM * WN][t * MT + u][lane] = acc[t][u];
-        __syncthreads();
-        if (wk > 0) return;
-        for (int k = 1; k < WK; ++k)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int u = 0; u < MT; ++u) acc[t][u] += part[(k - 1) * WM * WN + wave][t * MT + u][lane];
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int u = 0; u < MT; ++u) store4(p, m0 + 16 * u + r, n0 + 16 * t + 4 * q, acc[t][u]);
-}
-
-// ---------------------------------------------------------------- many rows: tiles through LDS
-// A workgroup owns BM x BN outputs (WM x WN waves of MT x NT tiles of 16 x 16) and
-// walks K in groups of 128 columns through a ring of STAGES LDS stages, filled by
-// direct global -> LDS loads STAGES - 1 groups ahead.
-//  * MXFP4 rows next to MXFP4 rows: a stage is two groups, one load instruction 8
-//    rows x 128 code bytes; next to bf16 rows a stage is one group, 16 rows x 64
-//    bytes.  Eight neighbouring lanes on one 128-byte run take 37 cycles an
-//    instruction, four on 64 bytes 50 (measured with the products left out), and
-//    these loads are what bounds the kernel.
-//  * bf16 rows: one instruction brings 4 rows x 256 bytes.
-//  In all a row's 16-byte pieces change places by a key of the row (bank_key).
-//  * scales: every fourth group, the 16 scale bytes of each row for the next four
-//    groups come in raw (4 bytes per group, one per quarter) and one thread per
-//    row turns them into one dword per quarter whose byte b belongs to group b:
-//    the products select it by its number (MXFP4) or shift it out (bf16).
-// The last group may end inside (K % 128 != 0): lanes past K load the last block
-// again, their operands become zeros and their scales 1.
-constexpr int kG = 128;          // columns of a group
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
@@ -233,6 +132,274 @@ __device__ __forceinline__ uint4 zero_unless(bool keep, uint4 v) {
     return make_uint4(keep ? v.x : 0u, keep ? v.y : 0u, keep ? v.z : 0u, keep ? v.w : 0u);
 }
 
+// This lane's part of 512 columns (run h) of an MXFP4 row: blocks 16h + 4q .. + 3.
+struct Run {
+    uint4 c[4];
+    uint32_t s;  // byte j: block j's scale
+};
+// Rows row0 .. row0 + 15 of an operand (those past the last repeat it): a uniform base
+// and this lane's offset, row r's codes from column 128q on.
+struct Rows {
+    const uint8_t *base;
+    uint32_t off;
+};
+__device__ __forceinline__ Rows rows_at(const uint8_t *m, size_t stride, int row0, int rows, int r, int q) {
+    const int first = min(row0, rows - 1);
+    return {m + (size_t)first * stride, (uint32_t)min(r, rows - 1 - first) * (uint32_t)stride + 64u * q};
+}
+// (blocks past K repeat the row's last one; the scale dword lies inside the row, whose
+// scales are padded to 16 bytes)
+__device__ __forceinline__ Run load_run(const MatArgs &p, const Rows &m, int h, int q) {
+    Run v;
+    const int n = p.K / 32 - 16 * h;  // blocks of the run
+    const uint8_t *c = m.base + 256 * (size_t)h;
+    if (n >= 16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v.c[j] = load_global_u4(c + m.off + 16 * j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v.c[j] = load_global_u4(c + m.off - 64u * q + 16u * min(4 * q + j, n - 1));
+    }
+    v.s = load_stream_u32(m.base + (size_t)p.K / 2 + 16 * (size_t)h + (m.off - 60u * q));
+    return v;
+}
+// blocks past K: zeros, scale 1
+__device__ __forceinline__ void cut_run(const MatArgs &p, Run &v, int h, int q) {
+    const int n = p.K / 32 - (16 * h + 4 * q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j >= n) {
+            v.c[j] = make_uint4(0u, 0u, 0u, 0u);
+            v.s = (v.s & ~(255u << 8 * j)) | 127u << 8 * j;
+        }
+}
+// The compiler waits for these loads here (and not later, behind loads issued since).
+__device__ __forceinline__ void wait_run(Run &v) {
+    asm volatile("" : "+v"(v.c[0].x), "+v"(v.c[1].x), "+v"(v.c[2].x), "+v"(v.c[3].x), "+v"(v.s));
+}
+// acc += a run of W times the same run of bf16 A, whose rows lie kXRow bytes apart in
+// LDS: 16 more than a run, so that 16 rows' 16-byte pieces lie in different banks.
+// xs: this lane's row and quarter.
+constexpr int kXRow = 1040;
+template <int MT, int NT>
+__device__ __forceinline__ void multiply_run(const Run (&w)[NT], const uint8_t *(&xs)[MT], f32x4_t (&acc)[NT][MT]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float sc[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sc[t] = scale_f32(w[t].s >> 8 * j & 255u);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            bf16x8_t wv[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const uint4 c = w[t].c[j];
+                wv[t] = codes_bf16(s == 0 ? c.x : s == 1 ? c.y : s == 2 ? c.z : c.w, sc[t]);
+            }
+#pragma unroll
+            for (int u = 0; u < MT; ++u) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(xs[u] + 64 * j + 16 * s);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[t], __builtin_bit_cast(bf16x8_t, x),
+                                                                        acc[t][u], 0, 0, 0);
+            }
+        }
+    }
+}
+// Run h of a row of bf16 A into LDS (lane l: its 16-byte piece l; past K the last one).
+__device__ __forceinline__ void dma_run(const MatArgs &p, int m, int h, int lane, uint32_t lds) {
+    const int pieces = p.K / 8 - 64 * h;
+    dma16(p.a + (size_t)m * p.a_stride + 1024 * (size_t)h, 16 * min(lane, pieces - 1), lds);
+}
+// Zeros past K in the last run of `rows` rows at xs, once it is there.
+__device__ __forceinline__ void zero_past_k(const MatArgs &p, uint8_t *xs, int rows, int h, int lane) {
+    if (8 * lane >= p.K - 512 * h)
+        for (int m = 0; m < rows; ++m)
+            *reinterpret_cast<uint4 *>(xs + m * kXRow + 16 * lane) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// ---------------------------------------------------------------- few rows: W straight into registers
+// One workgroup owns 16 * MT rows of A and 16 * NT rows of W; its WK waves split K
+// in runs of 512 columns (wave k takes runs k, k + WK, ...) and their sums are
+// joined through LDS, in wave order.  In a run lane 16q + r holds blocks 4q .. 4q+3
+// of row r: 64 code bytes and one dword of scales, so a row's 256 bytes are read as
+// whole lines, and product j takes block 4q + j from every quarter.  W is read once
+// from memory, the next run's while this one is multiplied; A comes from the caches.
+// Rows past M or N repeat the last row (their results are not stored); blocks past K
+// repeat the row's last block, as zeros.
+//
+// bf16 A: a run of a row is 1 KB, one direct global -> LDS load into the wave's own
+// rows (XR of them, two runs in turn).
+template <bool MX, int MT, int NT, int WK, int XR>
+__global__ __launch_bounds__(64 * WK) void mx_matmul_rows_kernel(MatArgs p) {
+    static_assert(MX || XR <= 16 * MT, "rows of A in LDS");
+    constexpr int XBUF = MX ? 0 : WK * 2 * XR * kXRow, JOIN = WK * NT * MT * 1024;
+    __shared__ uint4 smem4[(XBUF > JOIN ? XBUF : JOIN) / 16];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(smem4);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int m0 = blockIdx.y * 16 * MT, n0 = blockIdx.x * 16 * NT;
+    const int blocks = p.K / 32, runs = (blocks + 15) / 16, xrows = min(XR, p.M - m0);
+    Rows wr[NT], ar[MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) wr[t] = rows_at(p.w, p.w_stride, n0 + 16 * t, p.N, r, q);
+#pragma unroll
+    for (int u = 0; u < MT; ++u) ar[u] = rows_at(p.a, p.a_stride, m0 + 16 * u, p.M, r, q);
+    f32x4_t acc[NT][MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < MT; ++u) acc[t][u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    uint8_t *xw = smem + wave * (2 * XR * kXRow);
+    const uint32_t xbuf = lds_addr(smem) + (uint32_t)wave * (2 * XR * kXRow);
+    auto load_x = [&](int h, int i) __attribute__((always_inline)) {  // run h of A into buffer i of the wave
+        for (int m = 0; m < xrows; ++m) dma_run(p, m0 + m, h, lane, xbuf + (uint32_t)(i * XR + m) * kXRow);
+    };
+    // With one tile the waves themselves are enough in flight (72 registers, three
+    // workgroups a CU: 1 x 65536 x 4096 29.5 us; with the next run too, 85 registers
+    // and two, 35 us).
+    constexpr bool AHEAD = !MX || NT * MT > 1;
+    Run w[NT];
+    if (AHEAD && wave < runs) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) w[t] = load_run(p, wr[t], wave, q);
+        if (!MX) load_x(wave, 0);
+    }
+    int buf = 0;
+    for (int h = wave; h < runs; h += WK, buf ^= 1) {
+        const bool last = h == runs - 1 && blocks % 16 != 0;
+        if (!MX) {
+            wait_vm<0>();
+            if (last) zero_past_k(p, xw + buf * XR * kXRow, xrows, h, lane);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            if (AHEAD)
+                wait_run(w[t]);
+            else
+                w[t] = load_run(p, wr[t], h, q);
+        Run next[NT];
+        if (AHEAD && h + WK < runs) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) next[t] = load_run(p, wr[t], h + WK, q);
+            if (!MX) load_x(h + WK, buf ^ 1);
+        }
+        if (last)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) cut_run(p, w[t], h, q);
+        if constexpr (MX) {
+            Run x[MT];
+#pragma unroll
+            for (int u = 0; u < MT; ++u) x[u] = load_run(p, ar[u], h, q);
+            if (last)
+#pragma unroll
+                for (int u = 0; u < MT; ++u) cut_run(p, x[u], h, q);
+            static_for<0, 4>([&](auto j_const) __attribute__((always_inline)) {
+                constexpr int j = decltype(j_const)::value;
+#pragma unroll
+                for (int u = 0; u < MT; ++u)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        acc[t][u] = mfma_mx<j>(w[t].c[j], x[u].c[j], acc[t][u], (int)w[t].s, (int)x[u].s);
+            });
+        } else {
+            const uint8_t *xs[MT];
+#pragma unroll
+            for (int u = 0; u < MT; ++u) xs[u] = xw + (buf * XR + min(16 * u + r, xrows - 1)) * kXRow + 256 * q;
+            multiply_run<MT, NT>(w, xs, acc);
+        }
+        if (AHEAD)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) w[t] = next[t];
+    }
+    // join: tile i is summed by wave i % WK
+    if (!MX) __syncthreads();  // the rows of A are read
+    f32x4_t(*part)[NT * MT][64] = reinterpret_cast<f32x4_t(*)[NT * MT][64]>(smem);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < MT; ++u) part[wave][t * MT + u][lane] = acc[t][u];
+    __syncthreads();
+#pragma unroll
+    for (int i0 = 0; i0 < NT * MT; i0 += WK) {
+        const int i = i0 + wave;
+        if (i >= NT * MT) break;
+        f32x4_t v = part[0][i][lane];
+#pragma unroll
+        for (int k = 1; k < WK; ++k) v += part[k][i][lane];
+        store4(p, m0 + 16 * (i % MT) + r, n0 + 16 * (i / MT) + 4 * q, v);
+    }
+}
+
+// bf16 A of at most 16 rows that fit LDS (KB of it) whole: the workgroup brings them in
+// once and goes over tiles of 16 rows of W, blockIdx.x, + gridDim.x, ..., its waves
+// sharing each tile's runs as above.
+template <int WK, int KB>
+__global__ __launch_bounds__(64 * WK) void mx_matmul_few_kernel(MatArgs p, int tiles) {
+    __shared__ uint4 xs4[KB * 64];
+    __shared__ f32x4_t part[2][WK][64];
+    uint8_t *xs = reinterpret_cast<uint8_t *>(xs4);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int blocks = p.K / 32, runs = (blocks + 15) / 16;
+    Rows wr = rows_at(p.w, p.w_stride, 16 * blockIdx.x, p.N, r, q);
+    Run w[1];
+    if (wave < runs) w[0] = load_run(p, wr, wave, q);
+    const uint32_t lds0 = lds_addr(xs);
+    for (int h = wave; h < runs; h += WK)
+        for (int m = 0; m < p.M; ++m) dma_run(p, m, h, lane, lds0 + (uint32_t)(h * p.M + m) * kXRow);
+    wait_vm<0>();  // a wave reads only what it loaded itself
+    if (blocks % 16 != 0 && (runs - 1) % WK == wave) zero_past_k(p, xs + (size_t)(runs - 1) * p.M * kXRow, p.M, runs - 1, lane);
+    const uint8_t *xrow = xs + min(r, p.M - 1) * kXRow + 256 * q;
+    int i = 0;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++i) {
+        f32x4_t acc[1][1] = {{f32x4_t{0.f, 0.f, 0.f, 0.f}}};
+        const Rows here = wr;
+        wr = rows_at(p.w, p.w_stride, 16 * min(tile + (int)gridDim.x, tiles - 1), p.N, r, q);
+        for (int h = wave; h < runs; h += WK) {
+            wait_run(w[0]);
+            Run now[1] = {w[0]};
+            const bool more = h + WK < runs;
+            w[0] = load_run(p, more ? here : wr, more ? h + WK : wave, q);  // the next run, or tile
+            const bool last = h == runs - 1 && blocks % 16 != 0;
+            if (last) cut_run(p, now[0], h, q);
+            const uint8_t *x[1] = {xrow + (size_t)h * p.M * kXRow};
+            multiply_run<1, 1>(now, x, acc);
+        }
+        // join, in two buffers in turn, so that one barrier a tile is enough; another
+        // wave each time
+        part[i & 1][wave][lane] = acc[0][0];
+        ring_barrier();
+        if (wave == i % WK) {
+            f32x4_t v = part[i & 1][0][lane];
+#pragma unroll
+            for (int k = 1; k < WK; ++k) v += part[i & 1][k][lane];
+            store4(p, r, tile * 16 + 4 * q, v);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- many rows: tiles through LDS
+// A workgroup owns BM x BN outputs (WM x WN waves of MT x NT tiles of 16 x 16) and
+// walks K in groups of 128 columns through a ring of STAGES LDS stages, filled by
+// direct global -> LDS loads STAGES - 1 groups ahead.
+//  * MXFP4 rows next to MXFP4 rows: a stage is two groups, one load instruction 8
+//    rows x 128 code bytes; next to bf16 rows a stage is one group, 16 rows x 64
+//    bytes.  Eight neighbouring lanes on one 128-byte run take 37 cycles an
+//    instruction, four on 64 bytes 50 (measured with the products left out), and
+//    these loads are what bounds the kernel.
+//  * bf16 rows: one instruction brings 4 rows x 256 bytes.
+//  In all a row's 16-byte pieces change places by a key of the row (bank_key).
+//  * scales: every fourth group, the 16 scale bytes of each row for the next four
+//    groups come in raw (4 bytes per group, one per quarter) and one thread per
+//    row turns them into one dword per quarter whose byte b belongs to group b:
+//    the products select it by its number (MXFP4) or shift it out (bf16).
+// The last group may end inside (K % 128 != 0): lanes past K load the last block
+// again, their operands become zeros and their scales 1.
+constexpr int kG = 128;          // columns of a group
+
 // What the 16-byte pieces of row r of 16 are moved by (xor), for rows of 4, 8 or 16
 // pieces: a wave's 16-byte LDS reads are served in sets of 16 lanes that take rows
 // 0-3 and 12-15 from one quarter and rows 4-11 from the next (or the other way
@@ -259,64 +426,67 @@ struct Tile {
     static constexpr int RAW_PER_WAVE = (RAW_LOADS + WAVES - 1) / WAVES;
     static constexpr int FIT = (160 * 1024 - RAW_BYTES - PACKED_BYTES) / STAGE, STAGES = FIT < 3 ? FIT : 3;
     static constexpr int RING = STAGES * STAGE, LDS = RING + RAW_BYTES + PACKED_BYTES;
-    static_assert(STAGES >= 2 && LOADS >= WAVES && RAW_LOADS >= WAVES, "tile does not fit its workgroup");
+    static_assert(STAGES >= 2 && LOADS >= WAVES, "tile does not fit its workgroup");
 };
 
 // The sums of a workgroup's tile -> y, through the (now free) ring so that the
-// stores are whole rows: the direct order, four n of 16 different m, took 10 us of a
-// 2048 x 6144 output where whole rows take 4.  In as many parts of m as the ring's
-// size asks for.
-template <class T, int WN, int MT, int NT, typename OUT>
+// stores are whole rows: in the registers' order, four n of 16 different m, a 2048 x
+// 6144 output took 10 us, as whole rows 4.  In as many parts of m as the ring's size
+// asks for.  Kept short: it runs once, from a cold instruction cache.
+template <class T, int MT, int NT, typename OUT>
 __device__ __forceinline__ void store_tile(const MatArgs &p, uint8_t *smem, int m0, int n0, int wm, int wn, int lane,
                                            const f32x4_t (&acc)[NT][MT]) {
     constexpr int PITCH = T::BN * (int)sizeof(OUT) + 16;
     constexpr int FULL = T::BM * PITCH, PARTS = FULL <= T::LDS ? 1 : FULL <= 2 * T::LDS ? 2 : 4;
     static_assert(MT % PARTS == 0 && FULL <= PARTS * T::LDS, "a part of the tile fits the LDS");
     constexpr int PM = MT / PARTS, ROWS = T::BM / PARTS;  // row tiles per wave, rows of a part
-    constexpr int PER16 = 16 / (int)sizeof(OUT), UNITS = T::BN / PER16;
+    constexpr int PER16 = 16 / (int)sizeof(OUT), UNITS = T::BN / PER16, THREADS = 64 * T::WAVES;
+    constexpr int AT_ONCE = ROWS * UNITS % (4 * THREADS) == 0 ? 4 : ROWS * UNITS % (2 * THREADS) == 0 ? 2 : 1;
+    static_assert(ROWS * UNITS % (AT_ONCE * THREADS) == 0, "whole rounds of stores");
     const int r = lane & 15, q = lane >> 4;
-    const bool wide = ((uintptr_t)p.y | p.y_stride) % 16 == 0;
+    // 16 bytes at a time where every row begins and ends on such a piece
+    const bool wide = ((uintptr_t)p.y | p.y_stride) % 16 == 0 && p.N % PER16 == 0;
 #pragma unroll
     for (int part = 0; part < PARTS; ++part) {
         if (part) __syncthreads();
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int nl = (wn * NT + t) * 16 + 4 * q;
-            float b[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = p.bias && n0 + nl + j < p.N ? p.bias[n0 + nl + j] : 0.0f;
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int u = 0; u < PM; ++u) {
                 const f32x4_t v = acc[t][part * PM + u];
-                uint8_t *o = smem + ((wm * PM + u) * 16 + r) * PITCH + nl * (int)sizeof(OUT);
+                uint8_t *o = smem + ((wm * PM + u) * 16 + r) * PITCH + ((wn * NT + t) * 16 + 4 * q) * (int)sizeof(OUT);
                 if constexpr (sizeof(OUT) == 4)
-                    *reinterpret_cast<float4 *>(o) = make_float4(v[0] + b[0], v[1] + b[1], v[2] + b[2], v[3] + b[3]);
+                    *reinterpret_cast<f32x4_t *>(o) = v;
                 else
-                    *reinterpret_cast<uint2 *>(o) =
-                        make_uint2(f32_to_bf16_bits(v[0] + b[0]) | f32_to_bf16_bits(v[1] + b[1]) << 16,
-                                   f32_to_bf16_bits(v[2] + b[2]) | f32_to_bf16_bits(v[3] + b[3]) << 16);
+                    *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
             }
-        }
         __syncthreads();
-        for (int i = threadIdx.x; i < ROWS * UNITS; i += 64 * T::WAVES) {
-            const int lr = i / UNITS, c = i - lr * UNITS;
-            // row lr of the part: wave row lr / (16 * PM), its tile part * PM + ...
-            const int m = m0 + lr / (16 * PM) * (16 * MT) + part * 16 * PM + lr % (16 * PM), n = n0 + c * PER16;
-            if (m >= p.M || n >= p.N) continue;
-            const uint4 v = *reinterpret_cast<const uint4 *>(smem + lr * PITCH + 16 * c);
-            OUT *o = reinterpret_cast<OUT *>(p.y + (size_t)m * p.y_stride) + n;
-            if (wide && n + PER16 <= p.N) {
-                *reinterpret_cast<uint4 *>(o) = v;
-            } else {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        // row lr of the part: wave row lr / (16 * PM), its tiles part * PM and up
+        auto row_of = [&](int lr) { return m0 + lr / (16 * PM) * (16 * MT) + part * 16 * PM + lr % (16 * PM); };
+        if (wide) {
+#pragma unroll 1
+            for (int i0 = threadIdx.x; i0 < ROWS * UNITS; i0 += AT_ONCE * THREADS) {
+                uint4 v[AT_ONCE];
 #pragma unroll
-                for (int j = 0; j < PER16; ++j)
-                    if (n + j < p.N) {
-                        if constexpr (sizeof(OUT) == 4)
-                            o[j] = __uint_as_float(w[j]);
-                        else
-                            o[j] = (OUT)(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
-                    }
+                for (int e = 0; e < AT_ONCE; ++e) {
+                    const int i = i0 + e * THREADS;
+                    v[e] = *reinterpret_cast<const uint4 *>(smem + i / UNITS * PITCH + 16 * (i % UNITS));
+                }
+#pragma unroll
+                for (int e = 0; e < AT_ONCE; ++e) {
+                    const int i = i0 + e * THREADS, m = row_of(i / UNITS), n = n0 + i % UNITS * PER16;
+                    if (m < p.M && n < p.N)
+                        *reinterpret_cast<uint4 *>(p.y + (size_t)m * p.y_stride + (size_t)n * sizeof(OUT)) = v[e];
+                }
+            }
+        } else {  // value by value, a wave on neighbouring ones
+            const int cols = min(T::BN, p.N - n0);
+            for (int lr = threadIdx.x / 64; lr < ROWS; lr += T::WAVES) {
+                const int m = row_of(lr);
+                if (m >= p.M) continue;
+                OUT *o = reinterpret_cast<OUT *>(p.y + (size_t)m * p.y_stride) + n0;
+                const OUT *v = reinterpret_cast<const OUT *>(smem + lr * PITCH);
+                for (int n = lane; n < cols; n += 64) o[n] = v[n];
             }
         }
     }
@@ -324,7 +494,7 @@ __device__ __forceinline__ void store_tile(const MatArgs &p, uint8_t *smem, int 
 
 template <bool MX, int WM, int WN, int MT, int NT>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void
-mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles) {
+mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles, int k_part) {
     using T = Tile<MX, WM, WN, MT, NT>;
     constexpr int S = T::STAGES;
     __shared__ uint4 smem4[T::LDS / 16];
@@ -339,12 +509,16 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles) {
     const int tile = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if (tile >= tiles) return;
     const int m0 = tile % m_tiles * T::BM, n0 = tile / m_tiles * T::BN;
-    const int ng = (p.K + kG - 1) / kG, ns = (ng + T::KS - 1) / T::KS;  // groups, stages
-    const int nq = (p.K - (ng - 1) * kG) / 32;              // blocks of the last group
-    const int nb = nq + 4 * (ng - 1 - (ns - 1) * T::KS);    // blocks of the last stage
     const int m_last = min(T::BM, p.M - m0) - 1, n_last = min(T::BN, p.N - n0) - 1;
-    const uint8_t *wbase = p.w + (size_t)n0 * p.w_stride, *abase = p.a + (size_t)m0 * p.a_stride;
+    // this workgroup's columns k0 .. k0 + K - 1 (k_part a multiple of 512: whole runs of scales)
+    const int k0 = blockIdx.y * k_part, K = min(k_part, p.K - k0);
+    const uint8_t *wbase = p.w + (size_t)n0 * p.w_stride + k0 / 2;
+    const uint8_t *abase = p.a + (size_t)m0 * p.a_stride + (MX ? (size_t)k0 / 2 : 2 * (size_t)k0);
+    const size_t scales = (size_t)p.K / 2 - k0 / 2 + k0 / 32;  // from there
     const uint32_t lds0 = lds_addr(smem), raw0 = lds_addr(raw);
+    const int ng = (K + kG - 1) / kG, ns = (ng + T::KS - 1) / T::KS;  // groups, stages
+    const int nq = (K - (ng - 1) * kG) / 32;              // blocks of the last group
+    const int nb = nq + 4 * (ng - 1 - (ns - 1) * T::KS);    // blocks of the last stage
 
     // the wave's load instructions of a stage: number c < LOADS fills KB c of the
     // stage (W rows first); past the end the wave repeats its previous one
@@ -376,20 +550,20 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles) {
     // scales: an instruction brings 64 bytes of each of 16 rows (places past the row's
     // last 16 bytes repeat those)
     const int nr = (ng + 3) / 4;                      // runs of four groups
-    const int last16 = ((p.K / 32 + 15) / 16 - 1);    // last 16 scale bytes of a row
+    const int last16 = nr - 1;                        // last 16 scale bytes of these columns
     auto issue_scales = [&](int h) __attribute__((always_inline)) {  // of runs h .. h + 3 (h % 4 == 0)
 #pragma unroll
         for (int j = 0; j < T::RAW_PER_WAVE; ++j) {
-            const int c0 = j * T::WAVES + wave, c = c0 < T::RAW_LOADS ? c0 : c0 - T::WAVES;
+            const int c0 = j * T::WAVES + wave, c = c0 < T::RAW_LOADS ? c0 : c0 % T::RAW_LOADS;
             const bool isw = 16 * c < T::BN;
             const int row = 16 * c + (lane >> 2) - (isw ? 0 : T::BN);
             const uint32_t at = (uint32_t)min(row, isw ? n_last : m_last) * (uint32_t)(isw ? p.w_stride : p.a_stride);
-            const uint8_t *base = (isw ? wbase : abase) + (size_t)p.K / 2 + 16 * (size_t)h;
+            const uint8_t *base = (isw ? wbase : abase) + scales + 16 * (size_t)h;
             dma16(base, at + 16 * min(lane & 3, last16 - h), raw0 + 1024u * c);
         }
     };
     auto pack_scales = [&](int h) __attribute__((always_inline)) {
-        const int in = p.K / 32 - 16 * h;  // blocks that exist (none past the last run)
+        const int in = K / 32 - 16 * h;  // blocks that exist (none past the last run)
 #pragma unroll
         for (int row0 = 0; row0 < T::SCALE_ROWS; row0 += 64 * T::WAVES) {
             const int row = min(row0 + tid, T::SCALE_ROWS - 1);  // several threads write the last row alike
@@ -454,11 +628,11 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles) {
     // the last stage the last one is loaded again, into the places no one reads any
     // more, so that the loop needs no branch.
     issue_scales(0);
-    wait_vm<0>();
 #pragma unroll
     for (int i = 0; i < S; ++i)
 #pragma unroll
         for (int j = 0; j < T::PER_WAVE; ++j) issue_one(min(i, ns - 1), i, j);
+    wait_vm<S * T::PER_WAVE>();
     ring_barrier();
     pack_scales(0);
     wait_vm<(S - 1) * T::PER_WAVE>();
@@ -498,10 +672,12 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles) {
                     acc[t][u] = mfma_mx<b>(w[cur][t], x[u], acc[t][u], (int)sw[t], (int)sa[u]);
                 pin(u);
                 if (turns && u == 0) turn(g);
-                if (u < NT) {
-                    w[nxt][u] = read_w(g + 1, u);
-                    if (b == 3) sw_next[u] = read_sw(u);
-                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (t % MT == u) {
+                        w[nxt][t] = read_w(g + 1, t);
+                        if (b == 3) sw_next[t] = read_sw(t);
+                    }
                 x[u] = read_x(g + 1, 0, u);
                 if (b == 3) sa[u] = read_sa(u);
                 if (turns)
@@ -567,46 +743,177 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles) {
     });
     wait_vm<0>();     // no load may still write the ring
     __syncthreads();  // the ring becomes the output's staging
+    p.y += (size_t)blockIdx.y * p.M * p.y_stride;  // (parts of K: their sums one after the other)
+    if (p.bias)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float c = p.bias[min(n0 + (wn * NT + t) * 16 + 4 * q + j, p.N - 1)];
+#pragma unroll
+                for (int u = 0; u < MT; ++u) acc[t][u][j] += c;
+            }
     if (p.y_f32)
-        store_tile<T, WN, MT, NT, float>(p, smem, m0, n0, wm, wn, lane, acc);
+        store_tile<T, MT, NT, float>(p, smem, m0, n0, wm, wn, lane, acc);
     else
-        store_tile<T, WN, MT, NT, uint16_t>(p, smem, m0, n0, wm, wn, lane, acc);
+        store_tile<T, MT, NT, uint16_t>(p, smem, m0, n0, wm, wn, lane, acc);
 }
 
-template <bool MX, int MT, int NT, int WM, int WN, int WK>
-void launch_direct(const MatArgs &p, hipStream_t s) {
-    const dim3 grid((p.N + 16 * NT * WN - 1) / (16 * NT * WN), (p.M + 16 * MT * WM - 1) / (16 * MT * WM));
-    hipLaunchKernelGGL((mx_matmul_direct_kernel<MX, MT, NT, WM, WN, WK>), grid, dim3(64 * WM * WN * WK), 0, s, p);
+template <bool MX, int MT, int NT, int WK, int XR>
+void launch_rows(MatArgs p, hipStream_t s) {
+    const int most = 65535 * 16 * MT, all = p.M;  // rows of A a grid holds
+    for (int m = 0;; m += most) {
+        p.M = min(all - m, most);
+        const dim3 grid((p.N + 16 * NT - 1) / (16 * NT), (p.M + 16 * MT - 1) / (16 * MT));
+        hipLaunchKernelGGL((mx_matmul_rows_kernel<MX, MT, NT, WK, XR>), grid, dim3(64 * WK), 0, s, p);
+        if (all - m <= most) return;
+        p.a += (size_t)most * p.a_stride;
+        p.y += (size_t)most * p.y_stride;
+    }
+}
+
+template <int WK, int KB>
+void launch_few(const MatArgs &p, int per_cu, hipStream_t s) {
+    const int tiles = (p.N + 15) / 16;
+    hipLaunchKernelGGL((mx_matmul_few_kernel<WK, KB>), dim3(min(tiles, 256 * per_cu)), dim3(64 * WK), 0, s, p, tiles);
 }
 
 template <bool MX, int WM, int WN, int MT, int NT>
-void launch_tile(const MatArgs &p, hipStream_t s) {
+void launch_tile(const MatArgs &p, int k_part, hipStream_t s) {
     using T = Tile<MX, WM, WN, MT, NT>;
     const int m_tiles = (p.M + T::BM - 1) / T::BM, n_tiles = (p.N + T::BN - 1) / T::BN;
-    const unsigned grid = (unsigned)(((int64_t)m_tiles * n_tiles + 7) / 8 * 8);
-    hipLaunchKernelGGL((mx_matmul_tile_kernel<MX, WM, WN, MT, NT>), dim3(grid), dim3(64 * T::WAVES), 0, s, p,
-                       m_tiles, n_tiles);
+    const dim3 grid((unsigned)(((int64_t)m_tiles * n_tiles + 7) / 8 * 8), (unsigned)((p.K + k_part - 1) / k_part));
+    hipLaunchKernelGGL((mx_matmul_tile_kernel<MX, WM, WN, MT, NT>), grid, dim3(64 * T::WAVES), 0, s, p, m_tiles,
+                       n_tiles, k_part);
+}
+
+// The parts' sums [parts][M][N] added in order, bias, rounding once.
+__global__ __launch_bounds__(256) void mx_matmul_join_kernel(const float *__restrict__ sums, int parts, MatArgs p) {
+    const size_t all = (size_t)p.M * p.N, step = (size_t)gridDim.x * 256;
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
+        float v = sums[i];
+        for (int k = 1; k < parts; ++k) v += sums[k * all + i];
+        const size_t m = i / (uint32_t)p.N, n = i - m * p.N;
+        if (p.bias) v += p.bias[n];
+        uint8_t *row = p.y + m * p.y_stride;
+        if (p.y_f32)
+            reinterpret_cast<float *>(row)[n] = v;
+        else
+            reinterpret_cast<uint16_t *>(row)[n] = (uint16_t)pack_bf16(v, 0.0f);
+    }
+}
+
+// Which kernel a product takes: the least estimated time, in us, over the tile sizes
+// and parts of K.  A round of one workgroup per CU takes a + b per 128 columns; b grows
+// from `few` workgroups to a full round (they share L2 and the power budget).  Measured
+// at K = 2048 and 6144:
+//   MXFP4 A   256 x 192  7 + 0.52 .. 0.78   128 x 128  3 + 0.31 .. 0.41     64 x 64  3 + 0.17 .. 0.18
+//   bf16 A    128 x 256  6 + 1.23 .. 1.60   128 x 128  2.8 + 0.81 .. 1.06   64 x 64  2.5 + 0.47
+// and the rows kernel 2 (bf16 2.2) + 2.1 per turn of its waves' runs.  So 128 x 6144 x
+// 6144 in MXFP4 takes 31 us in 256 x 192 tiles and 12 us in 64 x 64 ones, 2048 rows 44
+// us and 129 us.  Parts cost a second kernel, about 3 us, and their sums written and
+// read: 64 x 6144 x 6144 with bf16 A 25 us in one part, 18 us in two.
+struct Plan {
+    enum Kind { FEW, ROWS1, ROWS2, TILE_L, TILE_M, TILE_S } kind;
+    int k_part, parts;
+};
+constexpr int kCUs = 256;
+
+int64_t few_bytes(int M, int K) { return (int64_t)((K + 511) / 512) * M * kXRow; }  // bf16 A in LDS
+constexpr int64_t kFewMost = 136 << 10;
+
+Plan plan(bool mx, int M, int N, int K, bool near) {
+    Plan best{Plan::ROWS1, K, 1};
+    if (M <= 16) {
+        if (!mx && near && few_bytes(M, K) <= kFewMost) best.kind = Plan::FEW;
+        return best;
+    }
+    auto rounds = [](int64_t wgs) { return (double)((wgs + kCUs - 1) / kCUs); };
+    auto over = [](int a, int b) { return (int64_t)((a + b - 1) / b); };
+    best.kind = Plan::ROWS2;
+    if (!near) return best;
+    const int turns = (int)over((int)over(K, 512), mx ? 8 : 2);
+    double least = rounds(over(M, 32) * over(N, 32)) * (mx ? 2.0 + 2.1 * turns : 2.2 + 2.1 * turns);
+    const struct {
+        Plan::Kind kind;
+        int bm, bn;
+        double a, few, full;
+    } tiles[2][3] = {{{Plan::TILE_L, 128, 256, 6.0, 1.23, 1.60},
+                      {Plan::TILE_M, 128, 128, 2.8, 0.81, 1.06},
+                      {Plan::TILE_S, 64, 64, 2.5, 0.47, 0.47}},
+                     {{Plan::TILE_L, 256, 192, 7.0, 0.52, 0.78},
+                      {Plan::TILE_M, 128, 128, 3.0, 0.31, 0.41},
+                      {Plan::TILE_S, 64, 64, 3.0, 0.17, 0.18}}};
+    for (const auto &t : tiles[mx])
+        for (int parts = 1; parts <= 8; parts *= 2) {
+            const int64_t part = over((int)over(K, 512), parts) * 512;
+            if (parts > 1 && part * (parts - 1) >= K) break;  // a part would be empty
+            const int64_t wgs = over(M, t.bm) * over(N, t.bn) * parts, rest = wgs % kCUs;
+            const double groups = (double)(part < K ? part : K) / 128;
+            const double join = parts > 1 ? 3.0 + (double)M * N * 8.0 * parts / 4e6 : 0.0;
+            const double us = (double)(wgs / kCUs) * (t.a + t.full * groups) +
+                              (rest ? t.a + (t.few + (t.full - t.few) * (double)rest / kCUs) * groups : 0.0) + join;
+            if (us < least) {
+                least = us;
+                best = Plan{t.kind, part < K ? (int)part : K, parts};
+            }
+        }
+    return best;
 }
 
 template <bool MX>
-void launch(const MatArgs &p, hipStream_t s) {
-    // a tile's lane offsets are 32 bits: rows further apart take the direct kernel
-    const bool near = p.w_stride < (8u << 20) && p.a_stride < (8u << 20);
-    if (p.M <= 16)
-        launch_direct<MX, 1, 1, 1, 1, 4>(p, s);
-    else if (p.M <= 64 || !near)
-        launch_direct<MX, 4, 4, 2, 2, 1>(p, s);
-    else if constexpr (MX)
-        launch_tile<MX, MOE_TCFG>(p, s);
-    else
-        launch_tile<MX, MOE_BCFG>(p, s);
+int run(const MatArgs &p, const Plan &how, float *sums, hipStream_t s) {
+    MatArgs t = p;  // what the tile kernels write: y, or the parts' sums
+    if (how.parts > 1) {
+        t.y = (uint8_t *)sums;
+        t.y_stride = (size_t)p.N * 4;
+        t.y_f32 = true;
+        t.bias = nullptr;
+    }
+    switch (how.kind) {
+        case Plan::FEW: {
+            const int64_t bytes = few_bytes(p.M, p.K);  // workgroups a CU: what LDS and registers hold
+            if (bytes <= 16 << 10)
+                launch_few<4, 16>(p, 3, s);
+            else if (bytes <= 36 << 10)
+                launch_few<4, 36>(p, 3, s);
+            else if (bytes <= 64 << 10)
+                launch_few<4, 64>(p, 2, s);
+            else
+                launch_few<8, 136>(p, 1, s);
+            break;
+        }
+        case Plan::ROWS1: launch_rows<MX, 1, 1, MX ? 8 : 4, 16>(p, s); break;
+        case Plan::ROWS2: launch_rows<MX, 2, 2, MX ? 8 : 2, 32>(p, s); break;
+        case Plan::TILE_L:
+            if constexpr (MX)
+                launch_tile<MX, 2, 4, 8, 3>(t, how.k_part, s);
+            else
+                launch_tile<MX, 2, 4, 4, 4>(t, how.k_part, s);
+            break;
+        case Plan::TILE_M: launch_tile<MX, 2, 4, 4, 2>(t, how.k_part, s); break;
+        case Plan::TILE_S: launch_tile<MX, 2, 4, 2, 1>(t, how.k_part, s); break;
+    }
+    MOE_LAUNCH_CHECK("mx_matmul_kernel");
+    if (how.parts > 1) {
+        const size_t blocks = ((size_t)p.M * p.N + 255) / 256;
+        hipLaunchKernelGGL(mx_matmul_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, sums,
+                           how.parts, p);
+        MOE_LAUNCH_CHECK("mx_matmul_join_kernel");
+    }
+    return MOE_OK;
 }
+
+// Rows further apart than this take the rows kernels: a tile's lane offsets are 32 bits.
+constexpr int64_t kTileStride = 8 << 20;
+
+size_t sums_bytes(const Plan &how, int M, int N) { return how.parts > 1 ? (size_t)how.parts * M * N * 4 : 0; }
 
 }  // namespace
 
 extern "C" size_t moe_mx_matmul_workspace_bytes(int M, int N, int K, int a_type) {
-    (void)M, (void)N, (void)K, (void)a_type;
-    return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || K % 32 || (a_type != MOE_BF16 && a_type != MOE_MXFP4)) return 0;
+    return sums_bytes(plan(a_type == MOE_MXFP4, M, N, K, true), M, N);
 }
 
 extern "C" int moe_mx_matmul(const void *a, int a_type, int64_t a_stride, const uint8_t *w, int64_t w_stride, int M,
@@ -627,15 +934,16 @@ extern "C" int moe_mx_matmul(const void *a, int a_type, int64_t a_stride, const 
         return moe::fail(MOE_E_ARG, "mx_matmul: operands' pointers and strides must be multiples of 16 bytes");
     if ((uintptr_t)y % size || (M > 1 && y_stride % size) || (uintptr_t)bias % 4)
         return moe::fail(MOE_E_ARG, "mx_matmul: y, its stride or bias is not aligned to its type");
-    const size_t need = moe_mx_matmul_workspace_bytes(M, N, K, a_type);
+    if ((M > 1 && a_stride > kMaxStride) || (N > 1 && w_stride > kMaxStride))
+        return moe::fail(MOE_E_SHAPE, "mx_matmul: operands' rows more than %lld bytes apart", (long long)kMaxStride);
+    const bool mx = a_type == MOE_MXFP4;
+    const Plan how = plan(mx, M, N, K, (M == 1 || a_stride < kTileStride) && (N == 1 || w_stride < kTileStride));
+    const size_t need = sums_bytes(how, M, N);
     if (workspace_bytes < need || (need && !workspace))
         return moe::fail(MOE_E_NOMEM, "mx_matmul: workspace %zu < %zu bytes", workspace_bytes, need);
-    const MatArgs p{(const uint8_t *)a, w, (size_t)a_stride, (size_t)w_stride, M, N, K, bias, (uint8_t *)y,
-                    (size_t)y_stride, y_type == MOE_FP32};
-    if (a_type == MOE_MXFP4)
-        launch<true>(p, (hipStream_t)stream);
-    else
-        launch<false>(p, (hipStream_t)stream);
-    MOE_LAUNCH_CHECK("mx_matmul_kernel");
-    return MOE_OK;
+    if (need && (uintptr_t)workspace % 16) return moe::fail(MOE_E_ARG, "mx_matmul: workspace is not 16-byte aligned");
+    const MatArgs p{(const uint8_t *)a, w, M > 1 ? (size_t)a_stride : 0, N > 1 ? (size_t)w_stride : 0, M, N, K, bias,
+                    (uint8_t *)y, M > 1 ? (size_t)y_stride : 0, y_type == MOE_FP32};
+    return mx ? run<true>(p, how, (float *)workspace, (hipStream_t)stream)
+              : run<false>(p, how, (float *)workspace, (hipStream_t)stream);
 }

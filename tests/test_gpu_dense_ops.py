@@ -167,6 +167,34 @@ def test_matmul_exact_sums(M, kind):
         assert np.array_equal(got, ref), (M, N, K, kind)
 
 
+@pytest.mark.parametrize("kind", [L.MOE_BF16, L.MOE_MXFP4])
+@pytest.mark.parametrize("M,N,K", [(2040, 6100, 1056), (2040, 4090, 1056), (1000, 2000, 544), (513, 1030, 1024),
+                                   (130, 2100, 1056), (20, 5000, 1056), (64, 257, 1024)])
+def test_matmul_exact_sums_larger(M, N, K, kind):
+    """As above, at sizes where the larger tiles and the parts of K are taken."""
+    rng = np.random.default_rng(M + N)
+    a, av = operand(rng, kind, M, K)
+    c, s = mxkit.random_rows(rng, N, K, 126, 128)
+    w, wv = dev(mxkit.pack(c, s)), mxkit.values(c, s)
+    b = rng.integers(-64, 65, N).astype(np.float32)
+    want = av @ wv.T + b
+    assert np.array_equal(run_matmul(a, kind, w, M, N, K, dev(b), L.MOE_FP32), want)
+    want = torch.from_numpy(want).to(torch.float32).to(torch.bfloat16).double().numpy()
+    assert np.array_equal(run_matmul(a, kind, w, M, N, K, dev(b), L.MOE_BF16), want)
+    # rows of y that 16-byte stores cannot take, and ones that they can
+    y = torch.full((M, (N + 7) // 8 * 8), 5.0, dtype=torch.bfloat16, device="cuda")
+    need = L.moe_mx_matmul_workspace_bytes(M, N, K, kind)
+    ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
+    L.moe_mx_matmul(a, kind, a.stride(0) * a.element_size(), w, mxkit.row_bytes(K), M, N, K, dev(b), y, L.MOE_BF16,
+                    2 * y.shape[1], ws, need, torch.cuda.current_stream())
+    assert np.array_equal(host(y[:, :N]), want) and (y[:, N:] == 5.0).all()
+    if need:
+        with pytest.raises(L.MoEError) as ei:
+            L.moe_mx_matmul(a, kind, a.stride(0) * a.element_size(), w, mxkit.row_bytes(K), M, N, K, None, y,
+                            L.MOE_BF16, 2 * y.shape[1], ws, need - 1, torch.cuda.current_stream())
+        assert ei.value.status == L.MOE_E_NOMEM
+
+
 def check_product(got, av, wv, bias, K, y_type):
     want = av @ wv.T + (0.0 if bias is None else bias)
     terms = np.abs(av) @ np.abs(wv).T

@@ -8,9 +8,10 @@
 //
 // Bound by memory: one read of add, resid (and an element gate), one write of
 // resid and x.  One workgroup owns a row and holds it in registers between the
-// two sums of squares, so nothing is read twice; the sums are fp32 in a fixed
-// order (a lane's values in index order, a butterfly per wave, the waves in
-// order), so results are reproducible.
+// two sums of squares, so nothing is read twice (2048 x 6144, fp32 residual: 151
+// MB in 27.0 us, 5.6 TB/s; one token of 4096: 3.8 us, the latency of a load, two
+// sums and a store).  The sums are fp32 in a fixed order (a lane's values in index
+// order, a butterfly per wave, the waves in order), so results are reproducible.
 #include "common.h"
 #include "dequant.h"
 #include "mx_quant.h"
@@ -18,6 +19,11 @@
 namespace {
 
 constexpr int kMaxThreads = 1024;
+constexpr int kReread = 8;            // items of a row that the registers do not hold
+// Residual streams of this many bytes (an XCD's L2) and more, and their x, are written
+// with non-temporal stores: 256 x 6144 by itself 6.7 us against 7.6, 2048 x 6144 27 us
+// against 39; in a chain with the products between, 2048 rows took the same either way.
+constexpr int64_t kStreamFrom = 4 << 20;
 constexpr int kMaxH = 1 << 28;       // column numbers plus a step stay in 31 bits
 constexpr int kMaxRows = 1 << 20;    // rows of one launch (its threads stay below 2^32)
 
@@ -58,11 +64,19 @@ __device__ __forceinline__ void load_f32(const float *p, size_t i, float (&x)[V]
         x[0] = p[i];
     }
 }
-template <int V>
+// 16 bytes to 16-byte aligned p; STREAM: non-temporal
+template <bool STREAM>
+__device__ __forceinline__ void store16(void *p, uint4 v) {
+    const moe_u32x4 w{v.x, v.y, v.z, v.w};
+    if constexpr (STREAM)
+        __builtin_nontemporal_store(w, (moe_u32x4 *)p);
+    else
+        *(moe_u32x4 *)p = w;
+}
+template <int V, bool STREAM>
 __device__ __forceinline__ void store_bf16(uint16_t *p, size_t i, const uint32_t (&h)[V]) {
     if constexpr (V == 8) {
-        *reinterpret_cast<uint4 *>(p + i) =
-            make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+        store16<STREAM>(p + i, make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16));
     } else {
         p[i] = (uint16_t)h[0];
     }
@@ -117,13 +131,14 @@ __device__ __forceinline__ void load_resid(const void *p, size_t i, float (&r)[V
 }
 
 // Stores r as the residual stream's type; r becomes the value kept.
-template <int V, bool RF32>
+template <int V, bool RF32, bool STREAM>
 __device__ __forceinline__ void store_resid(void *p, size_t i, float (&r)[V]) {
     if constexpr (RF32) {
         if constexpr (V == 8) {
-            float4 *q = reinterpret_cast<float4 *>((float *)p + i);
-            q[0] = make_float4(r[0], r[1], r[2], r[3]);
-            q[1] = make_float4(r[4], r[5], r[6], r[7]);
+#pragma unroll
+            for (int j = 0; j < 8; j += 4)
+                store16<STREAM>((float *)p + i + j, make_uint4(__float_as_uint(r[j]), __float_as_uint(r[j + 1]),
+                                                               __float_as_uint(r[j + 2]), __float_as_uint(r[j + 3])));
         } else {
             ((float *)p)[i] = r[0];
         }
@@ -134,20 +149,20 @@ __device__ __forceinline__ void store_resid(void *p, size_t i, float (&r)[V]) {
             h[j] = f32_to_bf16_bits(r[j]);
             r[j] = bf16_bits_to_f32(h[j]);
         }
-        store_bf16<V>((uint16_t *)p, i, h);
+        store_bf16<V, STREAM>((uint16_t *)p, i, h);
     }
 }
 
 // x of V values from the kept residual, stored as bf16 and / or as MXFP4 codes of
 // those bf16 values (V = 8: four neighbouring lanes hold a block).
-template <int V>
+template <int V, bool STREAM>
 __device__ __forceinline__ void store_next(const NormArgs &a, size_t row, int i, float inv, const float (&r)[V]) {
     uint32_t h[V];
     float w[V];
     if (a.w_pre) load_f32<V>(a.w_pre, (size_t)i, w);
 #pragma unroll
     for (int j = 0; j < V; ++j) h[j] = f32_to_bf16_bits(a.w_pre ? r[j] * inv * w[j] : r[j] * inv);
-    if (a.x_next) store_bf16<V>(a.x_next, row + i, h);
+    if (a.x_next) store_bf16<V, STREAM>(a.x_next, row + i, h);
     if constexpr (V == 8) {
         if (a.x_rows) {
             float x[8];
@@ -164,7 +179,7 @@ __device__ __forceinline__ void store_next(const NormArgs &a, size_t row, int i,
 // ITEMS > 0: thread t holds values V*(t + j*threads) .. + V-1 for j < ITEMS in
 // registers (H <= V * threads * ITEMS).  ITEMS = 0: any H, the row re-read from
 // memory for each of the three steps (the kept residual from resid_out).
-template <int V, int ITEMS, bool RF32>
+template <int V, int ITEMS, bool RF32, bool STREAM>
 __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormArgs a) {
     __shared__ float part[2][kMaxThreads / 64];
     const size_t row = (size_t)blockIdx.x * a.H;
@@ -197,7 +212,7 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormArgs a) {
                 const int i = V * tid + k * step;
                 if (i < a.H) {
                     update<V, RF32>(a, row, i, inv_post, gate_row, d[k], r[k]);
-                    store_resid<V, RF32>(a.resid_out, row + i, r[k]);
+                    store_resid<V, RF32, STREAM>(a.resid_out, row + i, r[k]);
                 }
             }
         }
@@ -211,7 +226,7 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormArgs a) {
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             const int i = V * tid + k * step;
-            if (i < a.H) store_next<V>(a, row, i, inv, r[k]);
+            if (i < a.H) store_next<V, STREAM>(a, row, i, inv, r[k]);
         }
     } else {
         const void *kept = a.resid;
@@ -233,7 +248,7 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormArgs a) {
                 load_bf16<V>(a.add, row + i, d);
                 load_resid<V, RF32>(a.resid, row + i, r);
                 update<V, RF32>(a, row, i, inv_post, gate_row, d, r);
-                store_resid<V, RF32>(a.resid_out, row + i, r);
+                store_resid<V, RF32, STREAM>(a.resid_out, row + i, r);
 #pragma unroll
                 for (int j = 0; j < V; ++j) ss = fmaf(r[j], r[j], ss);
             }
@@ -251,22 +266,22 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormArgs a) {
         for (int i = V * tid; i < a.H; i += step) {
             float r[V];
             load_resid<V, RF32>(kept, row + i, r);
-            store_next<V>(a, row, i, inv, r);
+            store_next<V, STREAM>(a, row, i, inv, r);
         }
     }
 }
 
-template <int V, bool RF32>
+template <int V, bool RF32, bool STREAM>
 void launch(const NormArgs &a, int T, int threads, int items, hipStream_t s) {
     const dim3 grid(T), block(threads);
-    if (items <= 1)
-        hipLaunchKernelGGL((block_norm_kernel<V, 1, RF32>), grid, block, 0, s, a);
-    else if (items <= 2)
-        hipLaunchKernelGGL((block_norm_kernel<V, 2, RF32>), grid, block, 0, s, a);
+    if (items == 1)
+        hipLaunchKernelGGL((block_norm_kernel<V, 1, RF32, STREAM>), grid, block, 0, s, a);
+    else if (items == 2)
+        hipLaunchKernelGGL((block_norm_kernel<V, 2, RF32, STREAM>), grid, block, 0, s, a);
     else if (items <= 4)
-        hipLaunchKernelGGL((block_norm_kernel<V, 4, RF32>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((block_norm_kernel<V, 4, RF32, STREAM>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((block_norm_kernel<V, 0, RF32>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((block_norm_kernel<V, 0, RF32, STREAM>), grid, block, 0, s, a);
 }
 
 }  // namespace
@@ -300,9 +315,14 @@ extern "C" int moe_block_norm(const uint16_t *add, int post_norm, const float *w
     if (x_rows && (!wide || (uintptr_t)x_rows % 16))
         return moe::fail(MOE_E_ARG, "block_norm: MXFP4 rows need every pointer 16-byte aligned");
     const int V = wide ? 8 : 1;
-    int threads = 256;
-    while (threads < kMaxThreads && V * threads < H && (T < 256 || 4 * V * threads < H)) threads *= 2;
-    const int items = (H + V * threads - 1) / (V * threads);
+    const int units = (H + V - 1) / V;
+    const bool stream_out = (int64_t)T * H * (int64_t)size >= kStreamFrom;
+    // Few rows: one item per thread, the most lanes on a row.  A row per CU and more: two
+    // (2048 x 6144: 27.0 us, with one item 28.5, with three 28.0; 301 x 1001: 4.8, 5.4, 5.2).
+    int items = T < 256 ? 1 : 2;
+    while (items < 4 && units > items * kMaxThreads) items *= 2;
+    int threads = ((units + items - 1) / items + 63) / 64 * 64;
+    if (threads > kMaxThreads) threads = kMaxThreads, items = kReread;
     hipStream_t s = (hipStream_t)stream;
     for (int t0 = 0; t0 < T; t0 += kMaxRows) {
         const int n = T - t0 < kMaxRows ? T - t0 : kMaxRows;
@@ -323,10 +343,12 @@ extern "C" int moe_block_norm(const uint16_t *add, int post_norm, const float *w
                    post_norm != 0,
                    scale,
                    eps};
-        if (wide)
-            f32 ? launch<8, true>(a, n, threads, items, s) : launch<8, false>(a, n, threads, items, s);
+        if (!wide)
+            f32 ? launch<1, true, false>(a, n, threads, items, s) : launch<1, false, false>(a, n, threads, items, s);
+        else if (stream_out)
+            f32 ? launch<8, true, true>(a, n, threads, items, s) : launch<8, false, true>(a, n, threads, items, s);
         else
-            f32 ? launch<1, true>(a, n, threads, items, s) : launch<1, false>(a, n, threads, items, s);
+            f32 ? launch<8, true, false>(a, n, threads, items, s) : launch<8, false, false>(a, n, threads, items, s);
         MOE_LAUNCH_CHECK("block_norm_kernel");
         if (T - t0 <= kMaxRows) break;
     }

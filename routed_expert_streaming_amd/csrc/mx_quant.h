@@ -34,40 +34,66 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top, bool fit) {
     return v > 2u ? v - 2u : 0u;
 }
 
+// The scale operand of gfx950's scaled converts: they take its exponent field as an
+// E8M0 byte (0 is 2^-127, 255 NaN).
+__device__ __forceinline__ float mx_scale_operand(uint32_t v) { return __uint_as_float(v << 23); }
+
 // Eight values of this lane -> four code bytes (byte b: value 2b in bits 0-3, 2b+1
-// in bits 4-7); v is the block's E8M0 byte.
+// in bits 4-7); v is the block's E8M0 byte.  x: eight floats, or four words of bf16 or
+// fp16 pairs.
 __device__ __forceinline__ uint32_t mx_codes8(const float (&x)[8], uint32_t v) {
-    if (v == 255u) return 0u;
-    // The convert divides by the scale's exponent field.  Below 2^-63 both sides
-    // are moved up by 2^64 first (exact), so that neither is a subnormal there.
-    const bool low = v < 64u;
-    const float up = low ? 0x1p64f : 1.0f;
-    const float scale = __uint_as_float((v + (low ? 64u : 0u)) << 23);
+    const float scale = mx_scale_operand(v);
     uint32_t c = 0;
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[0] * up, x[1] * up, scale, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2] * up, x[3] * up, scale, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[4] * up, x[5] * up, scale, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[6] * up, x[7] * up, scale, 3);
-    return c;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[0], x[1], scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2], x[3], scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[4], x[5], scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[6], x[7], scale, 3);
+    return v == 255u ? 0u : c;
+}
+typedef _Float16 moe_f16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t mx_codes8_bf16(const uint4 x, uint32_t v) {
+    const float scale = mx_scale_operand(v);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(moe_bf16x2, x.x), scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(moe_bf16x2, x.y), scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(moe_bf16x2, x.z), scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(moe_bf16x2, x.w), scale, 3);
+    return v == 255u ? 0u : c;
+}
+__device__ __forceinline__ uint32_t mx_codes8_f16(const uint4 x, uint32_t v) {
+    const float scale = mx_scale_operand(v);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(moe_f16x2, x.x), scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(moe_f16x2, x.y), scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(moe_f16x2, x.z), scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(moe_f16x2, x.w), scale, 3);
+    return v == 255u ? 0u : c;
 }
 
-// Bits of the largest magnitude of this lane's eight values (a NaN's bits are
-// above every number's).
+// Bits of the largest magnitude of this lane's eight values (a NaN's bits are above
+// every number's): fp32 values, or the 16-bit pattern of bf16 or fp16 pairs.
 __device__ __forceinline__ uint32_t mx_top8(const float (&x)[8]) {
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
     return top;
 }
-
-// 2^(v-127) (v = 255: NaN) and the value of an E2M1 code (bits 0-3), both exact in fp32.
-__device__ __forceinline__ float mx_block_scale(uint32_t v) {
-    return v == 255u ? __builtin_nanf("") : __uint_as_float(v ? v << 23 : 0x00400000u);
+__device__ __forceinline__ uint32_t mx_top8_half(const uint4 x) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    auto mag = [](uint32_t w) { return __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu); };
+    const u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(mag(x.x), mag(x.y)),
+                                              __builtin_elementwise_max(mag(x.z), mag(x.w)));
+    return max((uint32_t)m[0], (uint32_t)m[1]);
 }
-__device__ __forceinline__ float mx_e2m1(uint32_t q) {
-    const uint32_t m = q & 7u;  // 2 * magnitude of codes 0..7, four bits each: 0 1 2 3 4 6 8 12
-    const float a = 0.5f * (float)(0xC8643210u >> (4 * m) & 15u);
-    return q & 8u ? -a : a;
+
+// Eight codes -> their values in bf16 (two significant bits: exact; infinite beyond
+// bf16's range, NaN for v = 255).
+__device__ __forceinline__ uint4 mx_values8(uint32_t c, uint32_t v) {
+    const float scale = mx_scale_operand(v);
+    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3)));
 }
 
 // Scale byte of block `block` of a row whose codes start at row, by the block's

@@ -111,6 +111,109 @@ class ChainStats:
 RMS_EPS = 1e-6  # eps of the residual stream's RMS normalisation between chained layers
 
 
+@dataclass
+class BlockNorms:
+    """The norms around the layers of a chained step (moe_block_norm), all fp32 on the device:
+    pre [L,H], the weight of each layer's input norm; post [L,H], the weight of the norm of each
+    layer's output, or None for no such norm; gate [L,H], a factor per channel of what a layer adds
+    to the residual stream, or None; scale, one factor of it for every layer."""
+    pre: torch.Tensor
+    post: torch.Tensor | None = None
+    gate: torch.Tensor | None = None
+    scale: float = 1.0
+
+
+_ELEMENT = {torch.bfloat16: L.MOE_BF16, torch.float16: L.MOE_FP16, torch.float32: L.MOE_FP32}
+
+
+def quantise_mx(w: torch.Tensor, out: torch.Tensor | None = None, out_stride: int = 0,
+                scale_rule: int = L.MOE_MX_SCALE_FLOOR) -> torch.Tensor:
+    """MXFP4 rows of w [rows, K] (bf16, fp16 or fp32; rows may be strided): a new [rows, row bytes]
+    uint8 tensor, or out, whose rows lie out_stride bytes apart.  Runs on torch's current stream of
+    w's device."""
+    if w.dim() != 2 or w.dtype not in _ELEMENT or (w.shape[1] > 1 and w.stride(1) != 1):
+        raise ValueError("quantise_mx: needs [rows, K] in bf16, fp16 or fp32, each row contiguous")
+    rows, K = w.shape
+    with torch.cuda.device(w.device):
+        if out is None:
+            out_stride = L.moe_mx_row_bytes(K)
+            out = torch.empty((rows, out_stride), dtype=torch.uint8, device=w.device)
+        L.moe_mx_quant(w, _ELEMENT[w.dtype], w.stride(0) * w.element_size(), rows, K, scale_rule, out, out_stride, None,
+                       torch.cuda.current_stream())
+    return out
+
+
+def pack_mx_expert(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, slab: torch.Tensor | None = None,
+                   scale_rule: int = L.MOE_MX_SCALE_FLOOR) -> torch.Tensor:
+    """One expert's MXFP4 slab (weight format 1) from its gate w1 [I,H], up w3 [I,H] and down w2
+    [H,I] matrices: the row pairs (w1 row r, w3 row r), then w2's rows.  slab: where to write it
+    (uint8, moe_expert_bytes_mx(H, I) bytes; a slot of a pool, say), or None for a new tensor."""
+    I, H = w1.shape
+    if tuple(w3.shape) != (I, H) or tuple(w2.shape) != (H, I):
+        raise ValueError(f"pack_mx_expert: shapes {tuple(w1.shape)}, {tuple(w3.shape)}, {tuple(w2.shape)}")
+    nbytes = L.moe_expert_bytes_mx(H, I)
+    if not nbytes:
+        raise ValueError(f"pack_mx_expert: H={H}, I={I} must be multiples of 32")
+    if slab is None:
+        slab = torch.empty(nbytes, dtype=torch.uint8, device=w1.device)
+    if slab.dtype != torch.uint8 or slab.numel() != nbytes or not slab.is_contiguous():
+        raise ValueError(f"pack_mx_expert: the slab must be {nbytes} contiguous bytes")
+    slab = slab.view(-1)
+    gate, down = L.moe_mx_row_bytes(H), L.moe_mx_row_bytes(I)
+    quantise_mx(w1, slab, 2 * gate, scale_rule)
+    quantise_mx(w3, slab[gate:], 2 * gate, scale_rule)
+    quantise_mx(w2, slab[2 * I * gate:], down, scale_rule)
+    return slab
+
+
+class MxLinear:
+    """A dense layer with MXFP4 weights (projections, dense feed-forward layers, logits around the
+    routed experts): y = x W^T + bias.
+
+    weight [N, K]: quantised once, here.  quantise_input: False keeps the activations in bf16, True
+    quantises them per call (MXFP4 x MXFP4 on the scaled matrix cores).  out_dtype: torch.bfloat16
+    or torch.float32."""
+
+    def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None, quantise_input: bool = False,
+                 out_dtype: torch.dtype = torch.bfloat16, scale_rule: int = L.MOE_MX_SCALE_FLOOR):
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"MxLinear: out_dtype {out_dtype}")
+        self.N, self.K = weight.shape
+        self.rows = quantise_mx(weight, scale_rule=scale_rule)
+        self.bias = None if bias is None else bias.to(weight.device, torch.float32).contiguous()
+        if self.bias is not None and tuple(self.bias.shape) != (self.N,):
+            raise ValueError(f"MxLinear: bias {tuple(self.bias.shape)} for {self.N} outputs")
+        self.quantise_input = quantise_input
+        self.out_dtype = out_dtype
+
+    def __call__(self, x: torch.Tensor) -> torch.Tensor:
+        """x [..., K] bf16, or [M, row bytes] uint8 MXFP4 rows (moe_block_norm's x_rows); on torch's
+        current stream of the weights' device."""
+        if x.device != self.rows.device:
+            raise ValueError(f"MxLinear: x on {x.device}, weights on {self.rows.device}")
+        row = self.rows.shape[1]
+        with torch.cuda.device(x.device):
+            if x.dtype == torch.uint8:
+                if x.dim() != 2 or x.shape[1] != row or not x.is_contiguous():
+                    raise ValueError(f"MxLinear: MXFP4 rows must be [M, {row}], contiguous")
+                shape, a, a_type, a_stride = (x.shape[0],), x, L.MOE_MXFP4, row
+            else:
+                if x.dtype != torch.bfloat16 or x.shape[-1] != self.K:
+                    raise ValueError(f"MxLinear: x must be bf16 [..., {self.K}], got {x.dtype} {tuple(x.shape)}")
+                shape, a, a_type, a_stride = x.shape[:-1], x.reshape(-1, self.K), L.MOE_BF16, 2 * self.K
+                a = a if a.is_contiguous() else a.contiguous()
+                if self.quantise_input:
+                    a, a_type, a_stride = quantise_mx(a), L.MOE_MXFP4, row
+            M = a.shape[0]
+            y = torch.empty((M, self.N), dtype=self.out_dtype, device=x.device)
+            # a workspace of the call's own: two calls in flight, or two graphs, share nothing
+            need = L.moe_mx_matmul_workspace_bytes(M, self.N, self.K, a_type)
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+            L.moe_mx_matmul(a, a_type, a_stride, self.rows, row, M, self.N, self.K, self.bias, y, _ELEMENT[y.dtype],
+                            y.element_size() * self.N, ws, need, torch.cuda.current_stream())
+        return y.reshape(*shape, self.N)
+
+
 class MoEStack:
     """L routed-expert MoE layers of one configuration on one GPU.
 
@@ -672,11 +775,34 @@ class MoEStack:
         xs = torch.empty((self.L, self.T, self.H), dtype=torch.bfloat16, device=self.dev)
         return resid, xs
 
+    def _chain_norm(self, add, resid: torch.Tensor, l: int, x_next: torch.Tensor, norms: BlockNorms | None):
+        """Residual update with the output `add` of layer l - 1 (l = 0: the step's input) and the
+        input of layer l."""
+        T, H = self.T, self.H
+        if norms is None:
+            L.moe_residual_norm(add, resid, T, H, RMS_EPS, x_next, self.stream)
+            return
+        first = l == 0  # the step's input enters the stream as it is
+        post = None if first or norms.post is None else norms.post[l - 1]
+        gate = None if first or norms.gate is None else norms.gate[l - 1]
+        L.moe_block_norm(add, post is not None, post, gate, L.MOE_GATE_NONE if gate is None else L.MOE_GATE_CHANNEL,
+                         1.0 if first else norms.scale, resid, resid, L.MOE_FP32, norms.pre[l], T, H, RMS_EPS, x_next,
+                         None, self.stream)
+
+    def _check_norms(self, norms: BlockNorms):
+        for name in ("pre", "post", "gate"):
+            t = getattr(norms, name)
+            if t is not None and (tuple(t.shape) != (self.L, self.H) or t.dtype != torch.float32 or
+                                  t.device != self.dev or not t.is_contiguous()):
+                raise ValueError(f"BlockNorms.{name}: needs contiguous fp32 [{self.L}, {self.H}] on {self.dev}")
+
     def forward_chained(self, h0: torch.Tensor, xs: torch.Tensor, resid: torch.Tensor, out: torch.Tensor,
-                        lookahead: int = 0) -> ChainStats:
+                        lookahead: int = 0, norms: BlockNorms | None = None) -> ChainStats:
         """One step with chained layers: h0 [T,H] bf16 starts the residual stream,
         layer l's input xs[l] is the stream RMS-normalised after every earlier
         layer's output was added (moe_residual_norm), out[l] is layer l's output.
+        With norms, the layers' learned norms, gates and residual scale are applied
+        (moe_block_norm).
 
         Streamed, a layer's routing is known only when the layer before it is
         done, so the copies for its own routing are exposed.  With lookahead = m
@@ -687,8 +813,10 @@ class MoEStack:
         beside the predicted ones."""
         st = ChainStats()
         T, H, k = self.T, self.H, self.k
+        if norms is not None:
+            self._check_norms(norms)
         resid.zero_()
-        L.moe_residual_norm(h0, resid, T, H, RMS_EPS, xs[0], self.stream)
+        self._chain_norm(h0, resid, 0, xs[0], norms)
         m = max(0, min(int(lookahead), k))
         if self.streaming and T * (k + m) > self.C:
             raise ValueError(f"chained streaming needs {T * (k + m)} <= {self.C} slots")
@@ -756,7 +884,7 @@ class MoEStack:
                     self.upload_cpu_rows(l, job[1])
                     self.combine(l, out)
             if l + 1 < self.L:
-                L.moe_residual_norm(out[l], resid, T, H, RMS_EPS, xs[l + 1], self.stream)
+                self._chain_norm(out[l], resid, l + 1, xs[l + 1], norms)
         return st
 
     def last_routing(self) -> np.ndarray:

@@ -131,8 +131,11 @@ def quantise_mx(w: torch.Tensor, out: torch.Tensor | None = None, out_stride: in
     """MXFP4 rows of w [rows, K] (bf16, fp16 or fp32; rows may be strided): a new [rows, row bytes]
     uint8 tensor, or out, whose rows lie out_stride bytes apart.  Runs on torch's current stream of
     w's device."""
-    if w.dim() != 2 or w.dtype not in _ELEMENT or (w.shape[1] > 1 and w.stride(1) != 1):
-        raise ValueError("quantise_mx: needs [rows, K] in bf16, fp16 or fp32, each row contiguous")
+    apart = w.numel() > 0 and w.dim() == 2 and w.shape[1] > 1 and w.stride(1) != 1  # columns
+    if w.dim() != 2 or w.dtype not in _ELEMENT or apart or w.device.type != "cuda":
+        raise ValueError("quantise_mx: needs [rows, K] on the GPU in bf16, fp16 or fp32, each row contiguous")
+    if out is not None and (out.dtype != torch.uint8 or out.device != w.device):
+        raise ValueError(f"quantise_mx: out must be uint8 on {w.device}")
     rows, K = w.shape
     with torch.cuda.device(w.device):
         if out is None:

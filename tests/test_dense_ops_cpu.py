@@ -1,9 +1,11 @@
 """The dense MXFP4 operators without a GPU: their refusals, and the numpy forms the GPU tests compare with."""
 import numpy as np
 import pytest
+import torch
 
 import oracle
 from routed_expert_streaming_amd import _lib as L
+from routed_expert_streaming_amd.runtime import MxLinear, pack_mx_expert, quantise_mx
 from tests import mxkit
 
 FAKE = 0x1000  # never dereferenced: the calls below fail validation or have nothing to do
@@ -97,3 +99,24 @@ def test_numpy_forms_agree_with_the_oracle():
     assert s[0, 0] == 127 and c[0, :9].tolist() == [6, 6, 7, 7, 0, 2, 8, 14, 1]
     c, s = mxkit.quantise(x, "fit")  # halved: 2, 2.5, 2.5005, 3.95, .125, .375, .125, 1.75, .12505
     assert s[0, 0] == 128 and c[0, :9].tolist() == [4, 4, 5, 6, 0, 1, 8, 12, 0]
+
+
+def test_runtime_refusals():
+    w = torch.zeros((64, 96), dtype=torch.bfloat16)
+    for bad in (w, w[0], w.double(), w.t()):  # not on the GPU, not a matrix, a type, columns apart
+        with pytest.raises(ValueError):
+            quantise_mx(bad)
+    with pytest.raises(ValueError):
+        MxLinear(w, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        MxLinear(w)
+    down = torch.zeros((96, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        pack_mx_expert(w, w, w)          # down has the wrong shape
+    with pytest.raises(ValueError):
+        pack_mx_expert(w, w[:32], down)
+    with pytest.raises(ValueError):
+        pack_mx_expert(w, w, down, slab=torch.zeros(16, dtype=torch.uint8))
+    odd = torch.zeros((40, 96), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        pack_mx_expert(odd, odd, odd.t())

@@ -10,7 +10,10 @@ import pytest
 import torch
 
 import oracle
+import synth
 from routed_expert_streaming_amd import _lib as L
+from routed_expert_streaming_amd.runtime import (RMS_EPS, BlockNorms, MoEStack, MxLinear, pack_mx_expert,
+                                                 quantise_mx)
 from tests import mxkit
 
 pytestmark = pytest.mark.gpu
@@ -520,3 +523,96 @@ def test_quantised_experts_in_the_routed_ffn():
     torch.cuda.synchronize()
     wv = mxkit.values(*mxkit.quantise(host(gate), "floor"))
     check_product(host(d), host(x), wv, None, H, L.MOE_FP32)
+
+
+# ------------------------------------------------------------------ through the runtime
+def test_pack_mx_expert():
+    rng = np.random.default_rng(9)
+    H, I = 96, 64
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        mats = [dev(rng.standard_normal(s) * 0.1, dtype) for s in ((I, H), (I, H), (H, I))]
+        pool = torch.full((3, L.moe_expert_bytes_mx(H, I)), 0xA5, dtype=torch.uint8, device="cuda")
+        assert pack_mx_expert(*mats, slab=pool[1]).data_ptr() == pool[1].data_ptr()
+        fresh = pack_mx_expert(*mats)
+        assert torch.equal(fresh, pool[1]) and (pool[0] == 0xA5).all() and (pool[2] == 0xA5).all()
+        for which, m in enumerate(mats):
+            want = mxkit.values(*mxkit.quantise(host(m), "floor"))
+            assert np.array_equal(oracle.dequant(fresh.cpu().numpy(), H, I, which, 1), want)
+
+
+@pytest.mark.parametrize("quantise_input", [False, True])
+def test_mx_linear(quantise_input):
+    rng = np.random.default_rng(4)
+    N, K = 330, 544
+    weight = dev(rng.standard_normal((N, K)) * 0.05, torch.bfloat16)
+    bias = dev(rng.standard_normal(N), torch.bfloat16)
+    wide = torch.zeros((N, K + 32), dtype=torch.bfloat16, device="cuda")
+    wide[:, :K] = weight
+    for out_dtype, y_type in ((torch.bfloat16, L.MOE_BF16), (torch.float32, L.MOE_FP32)):
+        lin = MxLinear(wide[:, :K], bias, quantise_input, out_dtype)  # a view with rows further apart
+        assert torch.equal(lin.rows, quantise_mx(weight))
+        wv = mxkit.values(*mxkit.quantise(host(weight), "floor"))
+        for shape in ((1, K), (3, 5, K), (70, K), (0, K)):
+            x = dev(rng.standard_normal(shape), torch.bfloat16)
+            y = lin(x)
+            assert y.shape == (*shape[:-1], N) and y.dtype == out_dtype
+            if shape[0] == 0:
+                continue
+            xv = host(x).reshape(-1, K)
+            if quantise_input:
+                xv = mxkit.values(*mxkit.quantise(xv, "floor"))
+                assert torch.equal(lin(quantise_mx(x.reshape(-1, K))).reshape(y.shape), y)
+            check_product(host(y).reshape(-1, N), xv, wv, host(bias), K, y_type)
+        every = dev(rng.standard_normal((6, K)), torch.bfloat16)
+        assert torch.equal(lin(every[::2]), lin(every[::2].contiguous()))  # rows apart
+        for bad in (every.float(), every[:, :32], every.cpu()):
+            with pytest.raises(ValueError):
+                lin(bad)
+
+
+@pytest.mark.parametrize("post,gate", [(True, True), (False, True), (True, False), (False, False)])
+def test_chained_layers_with_norms(post, gate):
+    """A chained step with learned norms: every layer's input against the formula in 64 bits on the layers' own
+    outputs; the same step without norms is left as it was."""
+    st = MoEStack(synth.get("tiny", layers=3))
+    try:
+        rng = np.random.default_rng(1)
+        Lyr, T, H = st.L, st.T, st.H
+        norms = BlockNorms(dev(1 + 0.2 * rng.standard_normal((Lyr, H)), torch.float32),
+                           dev(1 + 0.2 * rng.standard_normal((Lyr, H)), torch.float32) if post else None,
+                           dev(rng.random((Lyr, H)), torch.float32) if gate else None, 0.5)
+        resid, xs = st.chain_buffers()
+        out, h0 = st.new_output(), st.make_inputs(0)[0]
+        st.forward_chained(h0, xs, resid, out, norms=norms)
+        torch.cuda.synchronize()
+        r = host(h0)
+        u = roundings(H) * 2.0 ** -24
+        err = np.zeros_like(r)  # how far the stream may be from these 64-bit values
+        for l in range(Lyr):
+            want = mxkit.norm(r, host(norms.pre[l]), RMS_EPS)
+            # an error of the stream moves x by as much as it is of the row's root mean square
+            rms = np.sqrt((r * r).mean(1, keepdims=True))
+            moved = (err + np.abs(r) * err.max(1, keepdims=True) / rms) / rms * np.abs(host(norms.pre[l]))
+            tol = (2.0 ** -8 * (1 + u) + u) * np.abs(want) + 2 * moved
+            assert (np.abs(host(xs[l]) - want) <= tol).all(), l
+            if l + 1 < Lyr:
+                d = host(out[l])
+                nxt = mxkit.block_norm(d, post, host(norms.post[l]) if post else None,
+                                       host(norms.gate[l]) if gate else None, 0.5, r, RMS_EPS)
+                err = err + u * np.abs(nxt - r) + 2.0 ** -24 * (np.abs(nxt) + err)
+                r = nxt
+        assert (np.abs(host(resid) - r) <= err).all()
+        # against the plain chain: unit weights, no gate, scale 1 give the same layers up to the sums' order
+        resid1, xs1 = st.chain_buffers()
+        out1 = st.new_output()
+        st.forward_chained(h0, xs1, resid1, out1)
+        ones = BlockNorms(torch.ones((Lyr, H), device="cuda"))
+        resid2, xs2 = st.chain_buffers()
+        st.forward_chained(h0, xs2, resid2, out, norms=ones)
+        torch.cuda.synchronize()
+        assert (np.abs(host(xs2[0]) - host(xs1[0])) <= 2.0 ** -7 * np.abs(host(xs1[0]))).all()  # one bf16 step
+        for bad in (BlockNorms(norms.pre[:1]), BlockNorms(norms.pre.double()), BlockNorms(norms.pre, norms.pre.t())):
+            with pytest.raises(ValueError):
+                st.forward_chained(h0, xs2, resid2, out, norms=bad)
+    finally:
+        st.close()

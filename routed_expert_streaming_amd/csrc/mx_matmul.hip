@@ -11,8 +11,12 @@
 //    columns 32q + 8s .. 32q + 8s + 7 from lane quarter q of both operands, so W
 //    stays in the same order (a sum over k does not care which lanes hold it).
 // W is the first operand: a lane then holds four consecutive n of one m, which it
-// stores together.  Sums are fp32; waves that split K are joined through LDS in
-// wave order.
+// stores together.  Sums are fp32; waves and parts that split K are joined in a fixed
+// order.
+//
+// Three families, chosen by plan(): up to 16 rows of A (bound by W's bytes), up to
+// about 64 (W's bytes and A's re-reads), more (LDS tiles, bound by the loads into LDS,
+// then by the matrix cores).
 #include "common.h"
 #include "dequant.h"
 
@@ -23,6 +27,8 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int64_t kMaxStride = 1 << 28;  // 16 rows' offsets stay in 32 bits
+constexpr int kMaxRows = 1 << 26;        // M and N: a grid's threads stay below 2^32
+constexpr int kMaxK = 1 << 27;
 
 struct MatArgs {
     const uint8_t *a, *w;
@@ -226,6 +232,10 @@ __device__ __forceinline__ void zero_past_k(const MatArgs &p, uint8_t *xs, int r
 // of row r: 64 code bytes and one dword of scales, so a row's 256 bytes are read as
 // whole lines, and product j takes block 4q + j from every quarter.  W is read once
 // from memory, the next run's while this one is multiplied; A comes from the caches.
+// 1 x 65536 x 4096 in MXFP4 takes 30 us (142 MB, 4.7 TB/s; a large copy reaches 4.9),
+// 32 x 6144 x 6144 8.3 us.  K split over the waves of a workgroup, not whole rows to
+// each, because 16 whole rows at a time keep the memory's pages open: with the same
+// loads alone a workgroup over 16 rows read 5.8 TB/s, one over 64 rows 4.0.
 // Rows past M or N repeat the last row (their results are not stored); blocks past K
 // repeat the row's last block, as zeros.
 //
@@ -335,7 +345,11 @@ __global__ __launch_bounds__(64 * WK) void mx_matmul_rows_kernel(MatArgs p) {
 
 // bf16 A of at most 16 rows that fit LDS (KB of it) whole: the workgroup brings them in
 // once and goes over tiles of 16 rows of W, blockIdx.x, + gridDim.x, ..., its waves
-// sharing each tile's runs as above.
+// sharing each tile's runs as above, the next tile's W in flight while this one is
+// joined.  4 x 65536 x 4096 (fp32 y): 32 us, 4.5 TB/s over W; from global memory, 16
+// scattered loads a run, 42 us, and with A brought in for each tile 40 us.  Four waves
+// and three workgroups a CU: eight waves each took 35 us, four workgroups 42 (the last
+// of 16 tiles a CU then runs alone).
 template <int WK, int KB>
 __global__ __launch_bounds__(64 * WK) void mx_matmul_few_kernel(MatArgs p, int tiles) {
     __shared__ uint4 xs4[KB * 64];
@@ -384,18 +398,24 @@ __global__ __launch_bounds__(64 * WK) void mx_matmul_few_kernel(MatArgs p, int t
 // ---------------------------------------------------------------- many rows: tiles through LDS
 // A workgroup owns BM x BN outputs (WM x WN waves of MT x NT tiles of 16 x 16) and
 // walks K in groups of 128 columns through a ring of STAGES LDS stages, filled by
-// direct global -> LDS loads STAGES - 1 groups ahead.
+// direct global -> LDS loads.
 //  * MXFP4 rows next to MXFP4 rows: a stage is two groups, one load instruction 8
 //    rows x 128 code bytes; next to bf16 rows a stage is one group, 16 rows x 64
 //    bytes.  Eight neighbouring lanes on one 128-byte run take 37 cycles an
-//    instruction, four on 64 bytes 50 (measured with the products left out), and
-//    these loads are what bounds the kernel.
+//    instruction, four on 64 bytes 50 (measured with the products left out).
 //  * bf16 rows: one instruction brings 4 rows x 256 bytes.
 //  In all a row's 16-byte pieces change places by a key of the row (bank_key).
-//  * scales: every fourth group, the 16 scale bytes of each row for the next four
-//    groups come in raw (4 bytes per group, one per quarter) and one thread per
-//    row turns them into one dword per quarter whose byte b belongs to group b:
-//    the products select it by its number (MXFP4) or shift it out (bf16).
+//  * scales: every 16 groups, 64 scale bytes of each row come in raw (16 bytes a row and
+//    load, as every four groups, cost a tenth of the time), and every four groups one
+//    thread per row turns 16 of them into one dword per quarter whose byte b belongs to
+//    group b: the products select it by its number (MXFP4) or shift it out (bf16).
+// Measured, 2048 x 6144 x 6144 in MXFP4, 256 x 192 tiles, one a CU: 44 us, 3.5
+// PFLOP/s.  A 128-column group takes 0.63 us; its products alone 0.45 (the scaled FP4
+// products reach 7.5 PFLOP/s in registers, 20 cycles each), its loads alone 0.35, and
+// the 88 KB of LDS reads and 28 KB of LDS writes 0.39 at 128 bytes a cycle: the three
+// share issue and LDS.  Prologue and epilogue take about 10 us of it.  2048 x 4096 x
+// 6144 with bf16 A, 128 x 256 tiles: 80 us, 1.29 PFLOP/s (bf16 products reach 2.1 in
+// registers; a library product of bf16 matrices of these sizes took 102 us).
 // The last group may end inside (K % 128 != 0): lanes past K load the last block
 // again, their operands become zeros and their scales 1.
 constexpr int kG = 128;          // columns of a group
@@ -493,7 +513,7 @@ __device__ __forceinline__ void store_tile(const MatArgs &p, uint8_t *smem, int 
 }
 
 template <bool MX, int WM, int WN, int MT, int NT>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM * WN / 4))) void
 mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles, int k_part) {
     using T = Tile<MX, WM, WN, MT, NT>;
     constexpr int S = T::STAGES;
@@ -809,6 +829,7 @@ __global__ __launch_bounds__(256) void mx_matmul_join_kernel(const float *__rest
 // at K = 2048 and 6144:
 //   MXFP4 A   256 x 192  7 + 0.52 .. 0.78   128 x 128  3 + 0.31 .. 0.41     64 x 64  3 + 0.17 .. 0.18
 //   bf16 A    128 x 256  6 + 1.23 .. 1.60   128 x 128  2.8 + 0.81 .. 1.06   64 x 64  2.5 + 0.47
+// (of 64 x 64 tiles a CU holds two workgroups: rounds after the first take 0.65 of it)
 // and the rows kernel 2 (bf16 2.2) + 2.1 per turn of its waves' runs.  So 128 x 6144 x
 // 6144 in MXFP4 takes 31 us in 256 x 192 tiles and 12 us in 64 x 64 ones, 2048 rows 44
 // us and 129 us.  Parts cost a second kernel, about 3 us, and their sums written and
@@ -837,13 +858,13 @@ Plan plan(bool mx, int M, int N, int K, bool near) {
     const struct {
         Plan::Kind kind;
         int bm, bn;
-        double a, few, full;
-    } tiles[2][3] = {{{Plan::TILE_L, 128, 256, 6.0, 1.23, 1.60},
-                      {Plan::TILE_M, 128, 128, 2.8, 0.81, 1.06},
-                      {Plan::TILE_S, 64, 64, 2.5, 0.47, 0.47}},
-                     {{Plan::TILE_L, 256, 192, 7.0, 0.52, 0.78},
-                      {Plan::TILE_M, 128, 128, 3.0, 0.31, 0.41},
-                      {Plan::TILE_S, 64, 64, 3.0, 0.17, 0.18}}};
+        double a, few, full, more;
+    } tiles[2][3] = {{{Plan::TILE_L, 128, 256, 6.0, 1.23, 1.60, 1.0},
+                      {Plan::TILE_M, 128, 128, 2.8, 0.81, 1.06, 1.0},
+                      {Plan::TILE_S, 64, 64, 2.5, 0.47, 0.47, 0.65}},
+                     {{Plan::TILE_L, 256, 192, 7.0, 0.52, 0.78, 1.0},
+                      {Plan::TILE_M, 128, 128, 3.0, 0.31, 0.41, 1.0},
+                      {Plan::TILE_S, 64, 64, 3.0, 0.17, 0.18, 0.65}}};
     for (const auto &t : tiles[mx])
         for (int parts = 1; parts <= 8; parts *= 2) {
             const int64_t part = over((int)over(K, 512), parts) * 512;
@@ -851,8 +872,9 @@ Plan plan(bool mx, int M, int N, int K, bool near) {
             const int64_t wgs = over(M, t.bm) * over(N, t.bn) * parts, rest = wgs % kCUs;
             const double groups = (double)(part < K ? part : K) / 128;
             const double join = parts > 1 ? 3.0 + (double)M * N * 8.0 * parts / 4e6 : 0.0;
-            const double us = (double)(wgs / kCUs) * (t.a + t.full * groups) +
-                              (rest ? t.a + (t.few + (t.full - t.few) * (double)rest / kCUs) * groups : 0.0) + join;
+            const double whole = t.a + t.full * groups;
+            const double part_round = rest ? t.a + (t.few + (t.full - t.few) * (double)rest / kCUs) * groups : 0.0;
+            const double us = (wgs < kCUs ? part_round : whole + t.more * ((double)(wgs / kCUs - 1) * whole + part_round)) + join;
             if (us < least) {
                 least = us;
                 best = Plan{t.kind, part < K ? (int)part : K, parts};
@@ -883,7 +905,17 @@ int run(const MatArgs &p, const Plan &how, float *sums, hipStream_t s) {
                 launch_few<8, 136>(p, 1, s);
             break;
         }
-        case Plan::ROWS1: launch_rows<MX, 1, 1, MX ? 8 : 4, 16>(p, s); break;
+        case Plan::ROWS1:
+            // 9 to 16 MXFP4 rows of A are as many bytes as a tile of W: with more tiles than
+            // CUs, two tiles a workgroup read them half as often (16 x 6144 x 6144 6.9 us
+            // against 8.3, 16 x 65536 x 4096 43 against 50; 4 x 65536 x 4096 38 against 35)
+            if constexpr (MX)
+                if (p.M > 8 && p.N > 16 * kCUs) {
+                    launch_rows<MX, 1, 2, 8, 16>(p, s);
+                    break;
+                }
+            launch_rows<MX, 1, 1, MX ? 8 : 4, 16>(p, s);
+            break;
         case Plan::ROWS2: launch_rows<MX, 2, 2, MX ? 8 : 2, 32>(p, s); break;
         case Plan::TILE_L:
             if constexpr (MX)
@@ -912,7 +944,7 @@ size_t sums_bytes(const Plan &how, int M, int N) { return how.parts > 1 ? (size_
 }  // namespace
 
 extern "C" size_t moe_mx_matmul_workspace_bytes(int M, int N, int K, int a_type) {
-    if (M <= 0 || N <= 0 || K <= 0 || K % 32 || (a_type != MOE_BF16 && a_type != MOE_MXFP4)) return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || K % 32 || M > kMaxRows || N > kMaxRows || K > kMaxK || (a_type != MOE_BF16 && a_type != MOE_MXFP4)) return 0;
     return sums_bytes(plan(a_type == MOE_MXFP4, M, N, K, true), M, N);
 }
 
@@ -923,6 +955,8 @@ extern "C" int moe_mx_matmul(const void *a, int a_type, int64_t a_stride, const 
     if (a_type != MOE_BF16 && a_type != MOE_MXFP4) return moe::fail(MOE_E_ARG, "mx_matmul: a_type=%d", a_type);
     if (y_type != MOE_BF16 && y_type != MOE_FP32) return moe::fail(MOE_E_ARG, "mx_matmul: y_type=%d", y_type);
     if (K <= 0 || K % 32) return moe::fail(MOE_E_SHAPE, "mx_matmul: K=%d must be a positive multiple of 32", K);
+    if (M > kMaxRows || N > kMaxRows || K > kMaxK)
+        return moe::fail(MOE_E_SHAPE, "mx_matmul: M=%d, N=%d above %d or K=%d above %d", M, N, kMaxRows, K, kMaxK);
     if (M == 0 || N == 0) return MOE_OK;
     if (!a || !w || !y) return moe::fail(MOE_E_ARG, "mx_matmul: NULL pointer");
     const int64_t row = (int64_t)moe::mx_row_bytes(K), size = y_type == MOE_FP32 ? 4 : 2;

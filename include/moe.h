@@ -494,13 +494,13 @@ int moe_mx_quant(const void *x, int x_type, int64_t x_stride, int rows, int K, i
 /* y[m,n] = sum_k A[m,k] * W[n,k] + bias[n], sums in fp32, rounded once.
  * a [M, K]: bf16 (a_type MOE_BF16; the weights are then formed in bf16, exact for
  * scale bytes up to 252) or MXFP4 rows (MOE_MXFP4); w [N] MXFP4 rows; bias [N]
- * fp32 or NULL; y [M, N] bf16 or fp32 (y_type).  Any M, N >= 0 (0: a no-op), K %
- * 32 == 0.  A scale byte of 255 makes every output it enters NaN.  A row of y
+ * fp32 or NULL; y [M, N] bf16 or fp32 (y_type).  M and N from 0 (a no-op) to 2^26, K
+ * a multiple of 32 up to 2^27, operands' rows at most 2^28 bytes apart.  A scale byte of 255 makes every output it enters NaN.  A row of y
  * does not depend on the other rows of a, but its last bits may depend on M
  * (which kernel runs).  workspace: moe_mx_matmul_workspace_bytes(M, N, K,
  * a_type) bytes (contents don't care, 16-byte aligned; calls sharing it must not
- * overlap in time; NULL when 0).  MOE_E_SHAPE for a bad K or a stride below its
- * row; MOE_E_ARG for negative sizes, unknown types, NULL pointers, a or w
+ * overlap in time; NULL when 0).  MOE_E_SHAPE for sizes or strides beyond these or
+ * a stride below its row; MOE_E_ARG for negative sizes, unknown types, NULL pointers, a or w
  * pointers or strides that are not multiples of 16 bytes, or y and bias not
  * aligned to their types; MOE_E_NOMEM for a small workspace.  y must not overlap
  * the inputs. */

@@ -17,8 +17,14 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Whether the values are written: not, or into the caches, or past them (non-temporal
+// stores; 2048 x 6144 9.0 us against 9.6, 1533 x 2080 fp32 4.7 against 5.0), from an
+// XCD's L2 on.
+enum { kNoValues, kValues, kStreamValues };
+constexpr int64_t kStreamFrom = 4 << 20;
+
 // One lane per eight values, numbered along the rows (units of a row: K / 8).
-template <int TYPE, bool VALUES>
+template <int TYPE, int VALUES>
 __global__ __launch_bounds__(kThreads) void mx_quant_kernel(const uint8_t *__restrict__ x, size_t x_stride,
                                                             uint32_t units, uint32_t per, bool fit,
                                                             uint8_t *__restrict__ out, size_t out_stride,
@@ -48,19 +54,24 @@ __global__ __launch_bounds__(kThreads) void mx_quant_kernel(const uint8_t *__res
     uint8_t *orow = out + row * out_stride;
     *reinterpret_cast<uint32_t *>(orow + 4 * (size_t)c) = codes;
     if ((c & 3) == 0) moe::mx_store_scale(orow, 8 * (int)per, (int)(c >> 2), s);
-    if (VALUES) *reinterpret_cast<uint4 *>(values + 8 * (size_t)u) = moe::mx_values8(codes, s);
+    if constexpr (VALUES != kNoValues) {
+        const uint4 v = moe::mx_values8(codes, s);
+        moe_u32x4 *to = reinterpret_cast<moe_u32x4 *>(values + 8 * (size_t)u);
+        if constexpr (VALUES == kStreamValues)
+            __builtin_nontemporal_store(moe_u32x4{v.x, v.y, v.z, v.w}, to);
+        else
+            *to = moe_u32x4{v.x, v.y, v.z, v.w};
+    }
 }
 
 template <int TYPE>
 void launch(const uint8_t *x, size_t x_stride, uint32_t units, uint32_t per, bool fit, uint8_t *out, size_t out_stride,
             uint16_t *values, hipStream_t s) {
     const dim3 grid((units + kThreads - 1) / kThreads), block(kThreads);
-    if (values)
-        hipLaunchKernelGGL((mx_quant_kernel<TYPE, true>), grid, block, 0, s, x, x_stride, units, per, fit, out,
-                           out_stride, values);
-    else
-        hipLaunchKernelGGL((mx_quant_kernel<TYPE, false>), grid, block, 0, s, x, x_stride, units, per, fit, out,
-                           out_stride, values);
+    auto *kernel = !values                                    ? mx_quant_kernel<TYPE, kNoValues>
+                   : (int64_t)units * 16 < kStreamFrom ? mx_quant_kernel<TYPE, kValues>
+                                                       : mx_quant_kernel<TYPE, kStreamValues>;
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, x, x_stride, units, per, fit, out, out_stride, values);
 }
 
 }  // namespace

@@ -55,6 +55,9 @@ def test_matmul_refusals():
     assert m(at=L.MOE_MXFP4, as_=32) == L.MOE_E_SHAPE
     assert m(a=ODD) == L.MOE_E_ARG and m(w=ODD) == L.MOE_E_ARG and m(as_=136) == L.MOE_E_ARG and m(ws=56) == L.MOE_E_ARG
     assert m(y=ODD) == L.MOE_E_ARG and m(ys=10) == L.MOE_E_ARG and m(bias=ODD) == L.MOE_E_ARG
+    assert m(M=(1 << 26) + 1) == L.MOE_E_SHAPE and m(N=(1 << 26) + 1, ys=1 << 40) == L.MOE_E_SHAPE
+    assert m(K=(1 << 27) + 32) == L.MOE_E_SHAPE
+    assert m(as_=(1 << 28) + 16) == L.MOE_E_SHAPE and m(ws=(1 << 28) + 16) == L.MOE_E_SHAPE
     for M, N in ((0, 2), (2, 0)):  # nothing to compute
         L.moe_mx_matmul(None, L.MOE_BF16, 0, None, 0, M, N, 64, None, None, L.MOE_FP32, 0)
         assert L.moe_mx_matmul_workspace_bytes(M, N, 64, L.MOE_BF16) == 0

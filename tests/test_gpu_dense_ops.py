@@ -141,6 +141,13 @@ def operand(rng, kind, R, K, low=126, high=128):
     return dev(v, torch.bfloat16), v
 
 
+def row_values(rows, K):
+    """The values of MXFP4 rows on the device."""
+    r = rows.cpu().numpy()
+    codes = np.stack([r[:, :K // 2] & 15, r[:, :K // 2] >> 4], -1).reshape(r.shape[0], K).astype(np.int64)
+    return mxkit.values(codes, r[:, K // 2:K // 2 + K // 32].astype(np.int64))
+
+
 # M and N on both sides of every tile the kernels use, K with and without a short last group
 M_SIZES = [1, 2, 3, 7, 15, 16, 17, 31, 33, 48, 64, 65, 100, 128, 129, 200, 257, 300]
 N_SIZES = [1, 3, 16, 17, 31, 64, 65, 128, 130, 255, 257, 512, 700]
@@ -198,6 +205,32 @@ def test_matmul_exact_sums_larger(M, N, K, kind):
             L.moe_mx_matmul(a, kind, a.stride(0) * a.element_size(), w, mxkit.row_bytes(K), M, N, K, None, y,
                             L.MOE_BF16, 2 * y.shape[1], ws, need - 1, torch.cuda.current_stream())
         assert ei.value.status == L.MOE_E_NOMEM
+
+
+@pytest.mark.parametrize("kind", [L.MOE_BF16, L.MOE_MXFP4])
+@pytest.mark.parametrize("M,far", [(3, "w"), (40, "w"), (150, "w"), (20, "a"), (70, "a"), (20, "both")])
+def test_matmul_rows_far_apart(M, far, kind):
+    """Operands whose rows lie 9 MB apart: views of larger buffers, beyond a tile's 32-bit offsets."""
+    rng = np.random.default_rng(M)
+    N, K, apart = 21, 544, 9 << 20
+    a, av = operand(rng, kind, M, K)
+    c, s = mxkit.random_rows(rng, N, K, 126, 128)
+    w, wv = dev(mxkit.pack(c, s)), mxkit.values(c, s)
+
+    def spread(t):
+        rows = t.view(torch.uint8).reshape(t.shape[0], -1)
+        wide = torch.zeros((t.shape[0], apart), dtype=torch.uint8, device="cuda")
+        wide[:, :rows.shape[1]] = rows
+        return wide
+    a_far, w_far = far in ("a", "both"), far in ("w", "both")
+    pa, pw = (spread(a) if a_far else a), (spread(w) if w_far else w)
+    y = torch.zeros((M, N), device="cuda")
+    need = L.moe_mx_matmul_workspace_bytes(M, N, K, kind)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    L.moe_mx_matmul(pa, kind, apart if a_far else a.stride(0) * a.element_size(), pw,
+                    apart if w_far else mxkit.row_bytes(K), M, N, K, None, y, L.MOE_FP32, 4 * N, ws, need,
+                    torch.cuda.current_stream())
+    assert np.array_equal(host(y), av @ wv.T)
 
 
 def check_product(got, av, wv, bias, K, y_type):
@@ -430,10 +463,7 @@ def test_layers_in_a_row_streams_and_graphs(T):
     codes, scales = mxkit.quantise(host(wf[1]), "fit")
     wv = mxkit.values(codes, scales)
     assert np.array_equal(w[1].cpu().numpy(), mxkit.pack(codes, scales))
-    rows = one["rows"].cpu().numpy()
-    nib = np.stack([rows[:, :K // 2] & 15, rows[:, :K // 2] >> 4], -1).reshape(T, K).astype(np.int64)
-    av = mxkit.values(nib, rows[:, K // 2:K // 2 + K // 32].astype(np.int64))
-    check_product(host(one["y"][1]), av, wv, None, K, L.MOE_BF16)
+    check_product(host(one["y"][1]), row_values(one["rows"], K), wv, None, K, L.MOE_BF16)
     # another stream
     other = torch.cuda.Stream()
     two = buffers()
@@ -460,33 +490,52 @@ def test_layers_in_a_row_streams_and_graphs(T):
 
 def test_calls_on_two_streams_at_once():
     rng = np.random.default_rng(11)
-    N, K = 1000, 2048
-    streams = [torch.cuda.Stream() for _ in range(2)]
+    K = 4096
+    streams = [torch.cuda.Stream() for _ in range(4)]
     data = []
-    for M in (3, 60):
+    for M, N in ((3, 1000), (60, 1000), (128, 2048), (256, 4096)):
         c, sc = mxkit.random_rows(rng, N, K, 120, 124)
         a = dev(rng.standard_normal((M, K)), torch.bfloat16)
         need = L.moe_mx_matmul_workspace_bytes(M, N, K, L.MOE_BF16)
-        data.append((M, a, dev(mxkit.pack(c, sc)), torch.zeros((M, N), device="cuda"),
+        data.append((M, N, a, dev(mxkit.pack(c, sc)), torch.zeros((M, N), device="cuda"),
                      torch.zeros(max(need, 1), dtype=torch.uint8, device="cuda"), need))
+    assert any(d[-1] for d in data)  # K in parts somewhere
 
     def go(d, stream):
-        M, a, w, y, ws, need = d
+        M, N, a, w, y, ws, need = d
         L.moe_mx_matmul(a, L.MOE_BF16, 2 * K, w, mxkit.row_bytes(K), M, N, K, None, y, L.MOE_FP32, 4 * N, ws, need, stream)
 
     want = []
     for d in data:
         go(d, torch.cuda.current_stream())
         torch.cuda.synchronize()
-        want.append(d[3].clone())
-        d[3].zero_()
+        want.append(d[4].clone())
+        check_product(host(d[4]), host(d[2]), row_values(d[3], K), None, K, L.MOE_FP32)
+        d[4].zero_()
     torch.cuda.synchronize()
     for _ in range(5):
         for d, st in zip(data, streams):
             go(d, st)
     torch.cuda.synchronize()
     for d, v in zip(data, want):
-        assert torch.equal(d[3], v)
+        assert torch.equal(d[4], v)
+    # each in a graph of its own, all replayed together between eager calls
+    graphs = []
+    for d in data:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            go(d, torch.cuda.current_stream())
+    for _ in range(3):
+        for d in data:
+            d[4].zero_()
+        torch.cuda.synchronize()
+        for gr, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+        torch.cuda.synchronize()
+        for d, v in zip(data, want):
+            assert torch.equal(d[4], v)
+            go(d, torch.cuda.current_stream())
 
 
 def test_quantised_experts_in_the_routed_ffn():

@@ -843,6 +843,11 @@ constexpr int kCUs = 256;
 int64_t few_bytes(int M, int K) { return (int64_t)((K + 511) / 512) * M * kXRow; }  // bf16 A in LDS
 constexpr int64_t kFewMost = 136 << 10;
 
+// One W tile of 16 rows a workgroup while that is one round, two beyond: 32 x 2048 x 6144
+// in MXFP4 5.4 us against 6.6 with two, 32 x 6144 x 6144 11.2 against 8.3; bf16 A, 32 x
+// 4096 x 2048, 5.3 against 6.4.
+bool one_w_tile(int M, int N) { return (int64_t)((M + 31) / 32) * ((N + 15) / 16) <= kCUs; }
+
 Plan plan(bool mx, int M, int N, int K, bool near) {
     Plan best{Plan::ROWS1, K, 1};
     if (M <= 16) {
@@ -855,6 +860,7 @@ Plan plan(bool mx, int M, int N, int K, bool near) {
     if (!near) return best;
     const int turns = (int)over((int)over(K, 512), mx ? 8 : 2);
     double least = rounds(over(M, 32) * over(N, 32)) * (mx ? 2.0 + 2.1 * turns : 2.2 + 2.1 * turns);
+    if (one_w_tile(M, N)) least *= 0.85;
     const struct {
         Plan::Kind kind;
         int bm, bn;
@@ -906,17 +912,21 @@ int run(const MatArgs &p, const Plan &how, float *sums, hipStream_t s) {
             break;
         }
         case Plan::ROWS1:
-            // 9 to 16 MXFP4 rows of A are as many bytes as a tile of W: with more tiles than
-            // CUs, two tiles a workgroup read them half as often (16 x 6144 x 6144 6.9 us
-            // against 8.3, 16 x 65536 x 4096 43 against 50; 4 x 65536 x 4096 38 against 35)
-            if constexpr (MX)
-                if (p.M > 8 && p.N > 16 * kCUs) {
-                    launch_rows<MX, 1, 2, 8, 16>(p, s);
-                    break;
-                }
-            launch_rows<MX, 1, 1, MX ? 8 : 4, 16>(p, s);
+            // A of many rows, or of bf16 rows too long for LDS, is as many bytes as a tile of
+            // W: with more tiles than CUs, two tiles a workgroup read it half as often (MXFP4
+            // 16 x 6144 x 6144 6.9 us against 8.3, 16 x 65536 x 4096 43 against 50, but 4 x
+            // 65536 x 4096 38 against 35; bf16 16 x 6144 x 6144 10.3 against 13.6)
+            if ((!MX || p.M > 8) && p.N > 16 * kCUs)
+                launch_rows<MX, 1, 2, MX ? 8 : 4, 16>(p, s);
+            else
+                launch_rows<MX, 1, 1, MX ? 8 : 4, 16>(p, s);
             break;
-        case Plan::ROWS2: launch_rows<MX, 2, 2, MX ? 8 : 2, 32>(p, s); break;
+        case Plan::ROWS2:
+            if (one_w_tile(p.M, p.N))
+                launch_rows<MX, 2, 1, MX ? 8 : 2, 32>(p, s);
+            else
+                launch_rows<MX, 2, 2, MX ? 8 : 2, 32>(p, s);
+            break;
         case Plan::TILE_L:
             if constexpr (MX)
                 launch_tile<MX, 2, 4, 8, 3>(t, how.k_part, s);

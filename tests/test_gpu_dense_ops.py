@@ -180,10 +180,11 @@ def test_matmul_exact_sums(M, kind):
 @pytest.mark.parametrize("kind", [L.MOE_BF16, L.MOE_MXFP4])
 @pytest.mark.parametrize("M,N,K", [(2040, 6100, 1056), (2040, 4090, 1056), (1000, 2000, 544), (513, 1030, 1024),
                                    (130, 2100, 1056), (20, 5000, 1056), (64, 257, 1024), (3, 20011, 96),
-                                   (8, 9001, 2048), (16, 4500, 544), (12, 5003, 96), (16, 9000, 1056), (1, 13000, 512)])
+                                   (8, 9001, 2048), (16, 4500, 544), (12, 5003, 96), (16, 9000, 1056), (1, 13000, 512),
+                                   (16, 4200, 4608)])
 def test_matmul_exact_sums_larger(M, N, K, kind):
-    """As above, at sizes where the larger tiles, the parts of K and several tiles a workgroup are taken (2048 terms:
-    below 2^19, 23 bits)."""
+    """As above, at sizes where the larger tiles, the parts of K and several tiles a workgroup are taken (4608
+    terms of at most 144, or 48 where bf16 ones stop at 4: below 2^20 in 16ths, 24 bits)."""
     rng = np.random.default_rng(M + N)
     a, av = operand(rng, kind, M, K)
     c, s = mxkit.random_rows(rng, N, K, 126, 128)

@@ -668,3 +668,51 @@ def test_chained_layers_with_norms(post, gate):
                 st.forward_chained(h0, xs2, resid2, out, norms=bad)
     finally:
         st.close()
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+def test_offsets_past_32_bits():
+    """Operands beyond 4 GiB: their last rows give what a small call on those rows gives."""
+    s = torch.cuda.current_stream()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    K = 8192
+    rb = mxkit.row_bytes(K)
+    # weights: 1,100,000 rows of 4352 bytes
+    N, tail = 1100000, 70
+    w = torch.randint(0, 256, (N, rb), dtype=torch.uint8, device="cuda", generator=g)
+    w[:, K // 2:] = 120
+    wv = row_values(w[-tail:], K)
+    for M, kind in ((2, L.MOE_BF16), (2, L.MOE_MXFP4), (40, L.MOE_MXFP4), (130, L.MOE_BF16)):
+        rng = np.random.default_rng(M)
+        a, av = operand(rng, kind, M, K)
+        y = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+        need = L.moe_mx_matmul_workspace_bytes(M, N, K, kind)
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+        L.moe_mx_matmul(a, kind, a.stride(0) * a.element_size(), w, rb, M, N, K, None, y, L.MOE_BF16, 2 * N, ws, need, s)
+        check_product(host(y[:, -tail:]), av, wv, None, K, L.MOE_BF16)
+    del w, y, ws
+    # activations and output: 300,000 rows
+    M, N = 300000, 8200
+    a = torch.randint(0, 256, (M, rb), dtype=torch.uint8, device="cuda", generator=g)
+    a[:, K // 2:] = 124
+    c, sc = mxkit.random_rows(np.random.default_rng(1), N, K, 118, 121)
+    w = dev(mxkit.pack(c, sc))
+    y = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    assert L.moe_mx_matmul_workspace_bytes(M, N, K, L.MOE_MXFP4) == 0
+    L.moe_mx_matmul(a, L.MOE_MXFP4, rb, w, rb, M, N, K, None, y, L.MOE_BF16, 2 * N, None, 0, s)
+    check_product(host(y[-5:]), row_values(a[-5:], K), mxkit.values(c, sc), None, K, L.MOE_BF16)
+    del a, y, w
+    # quantiser and norm: 300,000 x 8192
+    x = torch.randn((M, K), dtype=torch.bfloat16, device="cuda", generator=g)
+    rows = torch.empty((M, rb), dtype=torch.uint8, device="cuda")
+    vals = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    L.moe_mx_quant(x, L.MOE_BF16, 2 * K, M, K, L.MOE_MX_SCALE_FLOOR, rows, rb, vals, s)
+    codes, scales = mxkit.quantise(host(x[-2:]), "floor")
+    assert np.array_equal(rows[-2:].cpu().numpy(), mxkit.pack(codes, scales))
+    assert np.array_equal(host(vals[-2:]), mxkit.values(codes, scales))
+    resid = torch.randn((M, K), device="cuda", generator=g)
+    out = torch.empty_like(resid)
+    L.moe_block_norm(x, 1, None, None, L.MOE_GATE_NONE, 0.5, resid, out, L.MOE_FP32, None, M, K, 1e-6, vals, rows, s)
+    check_norm(x[-3:], resid[-3:], out[-3:], vals[-3:], 1, None, None, L.MOE_GATE_NONE, 0.5, None, L.MOE_FP32, 1e-6)
+    codes, scales = mxkit.quantise(host(vals[-1:]), "floor")
+    assert np.array_equal(rows[-1:].cpu().numpy(), mxkit.pack(codes, scales))

@@ -19,6 +19,7 @@
 // then by the matrix cores).
 #include "common.h"
 #include "dequant.h"
+#include "mx_quant.h"
 
 namespace {
 
@@ -40,17 +41,13 @@ struct MatArgs {
     bool y_f32;
 };
 
-// 8 consecutive weights (one dword of codes) -> bf16, times 2^(v-127) given as a float
+// 8 consecutive weights (one dword of codes) -> bf16, times 2^(v-127) as the converts take it
 __device__ __forceinline__ bf16x8_t codes_bf16(uint32_t c, float scale) {
     const uint32_t w0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0));
     const uint32_t w1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1));
     const uint32_t w2 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2));
     const uint32_t w3 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3));
     return __builtin_bit_cast(bf16x8_t, make_uint4(w0, w1, w2, w3));
-}
-
-__device__ __forceinline__ float scale_f32(uint32_t v) {
-    return v == 255u ? __builtin_nanf("") : __uint_as_float(v ? v << 23 : 0x00400000u);
 }
 
 // One product of 16 x 16 x 128; byte B of ws / as is the lane's block's scale.
@@ -193,7 +190,7 @@ __device__ __forceinline__ void multiply_run(const Run (&w)[NT], const uint8_t *
     for (int j = 0; j < 4; ++j) {
         float sc[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) sc[t] = scale_f32(w[t].s >> 8 * j & 255u);
+        for (int t = 0; t < NT; ++t) sc[t] = moe::mx_scale_operand(w[t].s >> 8 * j & 255u);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             bf16x8_t wv[NT];
@@ -709,7 +706,7 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles, int k_part) {
         } else {
             bf16x8_t wv[2][NT];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) wv[0][t] = codes_bf16(w[cur][t].x, scale_f32(sw[t] >> 8 * b & 255u));
+            for (int t = 0; t < NT; ++t) wv[0][t] = codes_bf16(w[cur][t].x, moe::mx_scale_operand(sw[t] >> 8 * b & 255u));
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
 #pragma unroll
@@ -733,7 +730,7 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles, int k_part) {
                         for (int t = 0; t < NT; ++t)
                             if (t % MT == u)
                                 wv[(s + 1) & 1][t] = codes_bf16(s == 0 ? w[cur][t].y : s == 1 ? w[cur][t].z : w[cur][t].w,
-                                                                scale_f32(sw[t] >> 8 * b & 255u));
+                                                                moe::mx_scale_operand(sw[t] >> 8 * b & 255u));
                     if (s == 3)
 #pragma unroll
                         for (int j = 0; j < T::PER_WAVE; ++j)

@@ -134,9 +134,11 @@ def quantise_mx(w: torch.Tensor, out: torch.Tensor | None = None, out_stride: in
     apart = w.numel() > 0 and w.dim() == 2 and w.shape[1] > 1 and w.stride(1) != 1  # columns
     if w.dim() != 2 or w.dtype not in _ELEMENT or apart or w.device.type != "cuda":
         raise ValueError("quantise_mx: needs [rows, K] on the GPU in bf16, fp16 or fp32, each row contiguous")
-    if out is not None and (out.dtype != torch.uint8 or out.device != w.device):
-        raise ValueError(f"quantise_mx: out must be uint8 on {w.device}")
     rows, K = w.shape
+    if out is not None:
+        need = (rows - 1) * out_stride + L.moe_mx_row_bytes(K) if rows else 0
+        if out.dtype != torch.uint8 or out.device != w.device or not out.is_contiguous() or out.numel() < need:
+            raise ValueError(f"quantise_mx: out must be {need} contiguous bytes (uint8) on {w.device}")
     with torch.cuda.device(w.device):
         if out is None:
             out_stride = L.moe_mx_row_bytes(K)

@@ -578,6 +578,21 @@ def test_quantised_experts_in_the_routed_ffn():
 
 
 # ------------------------------------------------------------------ through the runtime
+def test_quantise_mx_refuses_a_small_or_foreign_out():
+    w = torch.ones((3, 64), dtype=torch.bfloat16, device="cuda")
+    for out, stride in ((torch.zeros(2 * 48 + 47, dtype=torch.uint8, device="cuda"), 48),
+                        (torch.zeros(3 * 48, dtype=torch.uint8), 48),
+                        (torch.zeros(3 * 48, dtype=torch.int8, device="cuda"), 48),
+                        (torch.zeros((3, 96), dtype=torch.uint8, device="cuda")[:, :48], 96)):
+        with pytest.raises(ValueError):
+            quantise_mx(w, out, stride)
+    with pytest.raises(L.MoEError):
+        quantise_mx(w, torch.zeros(3 * 48, dtype=torch.uint8, device="cuda"), 32)  # rows would overlap
+    out = torch.zeros(2 * 64 + 48, dtype=torch.uint8, device="cuda")
+    quantise_mx(w, out, 64)
+    assert torch.equal(out[64:64 + 48], quantise_mx(w)[1])
+
+
 def test_pack_mx_expert():
     rng = np.random.default_rng(9)
     H, I = 96, 64

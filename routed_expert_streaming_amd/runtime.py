@@ -126,11 +126,20 @@ class BlockNorms:
 _ELEMENT = {torch.bfloat16: L.MOE_BF16, torch.float16: L.MOE_FP16, torch.float32: L.MOE_FP32}
 
 
+def _readable_rows(m: torch.Tensor) -> torch.Tensor:
+    """m [rows, n], each row contiguous; a copy of it where the dense operators do not take its rows as they
+    lie: they have to begin on 16-byte boundaries and not to overlap."""
+    apart = m.stride(0) * m.element_size()
+    if m.data_ptr() % 16 == 0 and (m.shape[0] < 2 or (apart % 16 == 0 and m.stride(0) >= m.shape[1])):
+        return m
+    return m.clone(memory_format=torch.contiguous_format)
+
+
 def quantise_mx(w: torch.Tensor, out: torch.Tensor | None = None, out_stride: int = 0,
                 scale_rule: int = L.MOE_MX_SCALE_FLOOR) -> torch.Tensor:
-    """MXFP4 rows of w [rows, K] (bf16, fp16 or fp32; rows may be strided): a new [rows, row bytes]
-    uint8 tensor, or out, whose rows lie out_stride bytes apart.  Runs on torch's current stream of
-    w's device."""
+    """MXFP4 rows of w [rows, K] (bf16, fp16 or fp32; rows may be strided; a view whose rows do not begin on
+    16-byte boundaries, or overlap, is copied first): a new [rows, row bytes] uint8 tensor, or out, whose
+    rows lie out_stride bytes apart.  Runs on torch's current stream of w's device."""
     apart = w.numel() > 0 and w.dim() == 2 and w.shape[1] > 1 and w.stride(1) != 1  # columns
     if w.dim() != 2 or w.dtype not in _ELEMENT or apart or w.device.type != "cuda":
         raise ValueError("quantise_mx: needs [rows, K] on the GPU in bf16, fp16 or fp32, each row contiguous")
@@ -140,6 +149,7 @@ def quantise_mx(w: torch.Tensor, out: torch.Tensor | None = None, out_stride: in
         if out.dtype != torch.uint8 or out.device != w.device or not out.is_contiguous() or out.numel() < need:
             raise ValueError(f"quantise_mx: out must be {need} contiguous bytes (uint8) on {w.device}")
     with torch.cuda.device(w.device):
+        w = _readable_rows(w)
         if out is None:
             out_stride = L.moe_mx_row_bytes(K)
             out = torch.empty((rows, out_stride), dtype=torch.uint8, device=w.device)
@@ -192,8 +202,9 @@ class MxLinear:
         self.out_dtype = out_dtype
 
     def __call__(self, x: torch.Tensor) -> torch.Tensor:
-        """x [..., K] bf16, or [M, row bytes] uint8 MXFP4 rows (moe_block_norm's x_rows); on torch's
-        current stream of the weights' device."""
+        """x [..., K] bf16, or [M, row bytes] uint8 MXFP4 rows (moe_block_norm's x_rows), copied first where
+        it is strided or does not begin on a 16-byte boundary; on torch's current stream of the weights'
+        device.  No gradients."""
         if x.device != self.rows.device:
             raise ValueError(f"MxLinear: x on {x.device}, weights on {self.rows.device}")
         row = self.rows.shape[1]
@@ -201,12 +212,12 @@ class MxLinear:
             if x.dtype == torch.uint8:
                 if x.dim() != 2 or x.shape[1] != row or not x.is_contiguous():
                     raise ValueError(f"MxLinear: MXFP4 rows must be [M, {row}], contiguous")
-                shape, a, a_type, a_stride = (x.shape[0],), x, L.MOE_MXFP4, row
+                shape, a, a_type, a_stride = (x.shape[0],), _readable_rows(x), L.MOE_MXFP4, row
             else:
                 if x.dtype != torch.bfloat16 or x.shape[-1] != self.K:
                     raise ValueError(f"MxLinear: x must be bf16 [..., {self.K}], got {x.dtype} {tuple(x.shape)}")
                 shape, a, a_type, a_stride = x.shape[:-1], x.reshape(-1, self.K), L.MOE_BF16, 2 * self.K
-                a = a if a.is_contiguous() else a.contiguous()
+                a = _readable_rows(a.contiguous())
                 if self.quantise_input:
                     a, a_type, a_stride = quantise_mx(a), L.MOE_MXFP4, row
             M = a.shape[0]

@@ -135,14 +135,18 @@ def _readable_rows(m: torch.Tensor) -> torch.Tensor:
     return m.clone(memory_format=torch.contiguous_format)
 
 
+def _check_matrix(w: torch.Tensor, what: str):
+    apart = w.numel() > 0 and w.dim() == 2 and w.shape[1] > 1 and w.stride(1) != 1  # columns
+    if w.dim() != 2 or w.dtype not in _ELEMENT or apart or w.device.type != "cuda":
+        raise ValueError(f"{what}: needs [rows, K] on the GPU in bf16, fp16 or fp32, each row contiguous")
+
+
 def quantise_mx(w: torch.Tensor, out: torch.Tensor | None = None, out_stride: int = 0,
                 scale_rule: int = L.MOE_MX_SCALE_FLOOR) -> torch.Tensor:
     """MXFP4 rows of w [rows, K] (bf16, fp16 or fp32; rows may be strided; a view whose rows do not begin on
     16-byte boundaries, or overlap, is copied first): a new [rows, row bytes] uint8 tensor, or out, whose
     rows lie out_stride bytes apart.  Runs on torch's current stream of w's device."""
-    apart = w.numel() > 0 and w.dim() == 2 and w.shape[1] > 1 and w.stride(1) != 1  # columns
-    if w.dim() != 2 or w.dtype not in _ELEMENT or apart or w.device.type != "cuda":
-        raise ValueError("quantise_mx: needs [rows, K] on the GPU in bf16, fp16 or fp32, each row contiguous")
+    _check_matrix(w, "quantise_mx")
     rows, K = w.shape
     if out is not None:
         need = (rows - 1) * out_stride + L.moe_mx_row_bytes(K) if rows else 0
@@ -162,7 +166,12 @@ def pack_mx_expert(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, slab: t
                    scale_rule: int = L.MOE_MX_SCALE_FLOOR) -> torch.Tensor:
     """One expert's MXFP4 slab (weight format 1) from its gate w1 [I,H], up w3 [I,H] and down w2
     [H,I] matrices: the row pairs (w1 row r, w3 row r), then w2's rows.  slab: where to write it
-    (uint8, moe_expert_bytes_mx(H, I) bytes; a slot of a pool, say), or None for a new tensor."""
+    (uint8, moe_expert_bytes_mx(H, I) bytes; a slot of a pool, say), or None for a new tensor.  A call
+    that is refused has written nothing."""
+    for w in (w1, w3, w2):
+        _check_matrix(w, "pack_mx_expert")
+        if w.device != w1.device:
+            raise ValueError(f"pack_mx_expert: matrices on {w1.device} and {w.device}")
     I, H = w1.shape
     if tuple(w3.shape) != (I, H) or tuple(w2.shape) != (H, I):
         raise ValueError(f"pack_mx_expert: shapes {tuple(w1.shape)}, {tuple(w3.shape)}, {tuple(w2.shape)}")
@@ -171,8 +180,9 @@ def pack_mx_expert(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, slab: t
         raise ValueError(f"pack_mx_expert: H={H}, I={I} must be multiples of 32")
     if slab is None:
         slab = torch.empty(nbytes, dtype=torch.uint8, device=w1.device)
-    if slab.dtype != torch.uint8 or slab.numel() != nbytes or not slab.is_contiguous():
-        raise ValueError(f"pack_mx_expert: the slab must be {nbytes} contiguous bytes")
+    if (slab.dtype != torch.uint8 or slab.numel() != nbytes or not slab.is_contiguous()
+            or slab.device != w1.device):
+        raise ValueError(f"pack_mx_expert: the slab must be {nbytes} contiguous bytes (uint8) on {w1.device}")
     slab = slab.view(-1)
     gate, down = L.moe_mx_row_bytes(H), L.moe_mx_row_bytes(I)
     quantise_mx(w1, slab, 2 * gate, scale_rule)

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from routed_expert_streaming_amd import _lib as L
-from routed_expert_streaming_amd.runtime import MxLinear, quantise_mx
+from routed_expert_streaming_amd.runtime import MxLinear, pack_mx_expert, quantise_mx
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,25 @@ def test_mx_linear_takes_any_view(quantise_input):
     assert torch.equal(lin(x[1:2].expand(3, K)), lin(x[1:2]).expand(3, N))
     rows = quantise_mx(x)
     assert torch.equal(lin(shifted(rows, 8)), lin(rows))
+
+
+def test_pack_mx_expert_refused_leaves_the_slab():
+    """A slot of a live pool: matrices that are refused (the last one a transposed view, a wrong type, on the host) must
+    not leave half an expert behind."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    H, I = 96, 64
+    w1, w3, w2 = (torch.randn(s, generator=g, device="cuda").to(torch.bfloat16) for s in ((I, H), (I, H), (H, I)))
+    slab = torch.full((L.moe_expert_bytes_mx(H, I),), 0xA5, dtype=torch.uint8, device="cuda")
+    for bad in ((w1, w3, w2.t().contiguous().t()), (w1, w3.double(), w2), (w1, w3, w2.cpu()), (w1, w3.cpu(), w2)):
+        with pytest.raises(ValueError):
+            pack_mx_expert(*bad, slab=slab)
+        assert (slab == 0xA5).all()
+    with pytest.raises(L.MoEError):
+        pack_mx_expert(w1, w3, w2, slab=slab, scale_rule=2)
+    assert (slab == 0xA5).all()
+    wide = torch.full((slab.numel() + 16,), 0xA5, dtype=torch.uint8, device="cuda")
+    with pytest.raises(L.MoEError):
+        pack_mx_expert(w1, w3, w2, slab=wide[8:8 + slab.numel()])  # off a 16-byte boundary
+    assert (wide == 0xA5).all()
+    pack_mx_expert(w1, w3, w2, slab=slab)
+    assert torch.equal(slab, pack_mx_expert(shifted(w1), shifted(w3), shifted(w2)))

@@ -165,9 +165,12 @@ def quantise_mx(w: torch.Tensor, out: torch.Tensor | None = None, out_stride: in
 def pack_mx_expert(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, slab: torch.Tensor | None = None,
                    scale_rule: int = L.MOE_MX_SCALE_FLOOR) -> torch.Tensor:
     """One expert's MXFP4 slab (weight format 1) from its gate w1 [I,H], up w3 [I,H] and down w2
-    [H,I] matrices: the row pairs (w1 row r, w3 row r), then w2's rows.  slab: where to write it
-    (uint8, moe_expert_bytes_mx(H, I) bytes; a slot of a pool, say), or None for a new tensor.  A call
-    that is refused has written nothing."""
+    [H,I] matrices on the GPU: the row pairs (w1 row r, w3 row r), then w2's rows.  slab: where to write
+    it (uint8, moe_expert_bytes_mx(H, I) contiguous bytes), or None for a new tensor.  It may be a slot of a
+    pool on the matrices' device, or host memory: torch.from_numpy(stack.host_pool_slabs(l)[e]) is an
+    expert of a streamed stack (the host copy is complete on return; an expert that is already cached
+    stays as it was until it is evicted or reset_cache is called).  A call that is refused has written
+    nothing."""
     for w in (w1, w3, w2):
         _check_matrix(w, "pack_mx_expert")
         if w.device != w1.device:
@@ -180,10 +183,15 @@ def pack_mx_expert(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, slab: t
         raise ValueError(f"pack_mx_expert: H={H}, I={I} must be multiples of 32")
     if slab is None:
         slab = torch.empty(nbytes, dtype=torch.uint8, device=w1.device)
+    on_host = slab.device.type == "cpu"
     if (slab.dtype != torch.uint8 or slab.numel() != nbytes or not slab.is_contiguous()
-            or slab.device != w1.device):
-        raise ValueError(f"pack_mx_expert: the slab must be {nbytes} contiguous bytes (uint8) on {w1.device}")
+            or not (on_host or slab.device == w1.device)):
+        raise ValueError(f"pack_mx_expert: the slab must be {nbytes} contiguous bytes (uint8) on {w1.device} or the "
+                         "host")
     slab = slab.view(-1)
+    if on_host:
+        slab.copy_(pack_mx_expert(w1, w3, w2, None, scale_rule))  # waits for the copy
+        return slab
     gate, down = L.moe_mx_row_bytes(H), L.moe_mx_row_bytes(I)
     quantise_mx(w1, slab, 2 * gate, scale_rule)
     quantise_mx(w3, slab[gate:], 2 * gate, scale_rule)
@@ -382,7 +390,7 @@ class MoEStack:
         return self.host[self.cfg.weight_layer(l)].ptr + e * self.slab
 
     def host_pool_slabs(self, l: int):
-        """Layer l's routed slabs as views of the pinned host pool the cache streams from."""
+        """Layer l's routed slabs as views of the pinned host pool the cache streams from (until close())."""
         arr = self.host[self.cfg.weight_layer(l)].array
         return [arr[e * self.slab:(e + 1) * self.slab] for e in range(self.E)]
 

@@ -1,9 +1,12 @@
 """The dense MXFP4 operators through the runtime: the views, slabs and pools that its documentation allows."""
+import numpy as np
 import pytest
 import torch
 
+import oracle
+import synth
 from routed_expert_streaming_amd import _lib as L
-from routed_expert_streaming_amd.runtime import MxLinear, pack_mx_expert, quantise_mx
+from routed_expert_streaming_amd.runtime import MoEStack, MxLinear, pack_mx_expert, quantise_mx
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +80,51 @@ def test_pack_mx_expert_refused_leaves_the_slab():
     assert (wide == 0xA5).all()
     pack_mx_expert(w1, w3, w2, slab=slab)
     assert torch.equal(slab, pack_mx_expert(shifted(w1), shifted(w3), shifted(w2)))
+
+
+@pytest.fixture
+def stacks():
+    """A streamed and a resident stack of one configuration, closed after a failure has been shown: the views of the
+    host pool die with them."""
+    cfg = synth.get("tiny", fmt=1, layers=2, cap=0.5)
+    both = MoEStack(cfg), MoEStack(cfg, cap=1.0)
+    yield cfg, *both
+    for st in both:
+        st.close()
+
+
+def test_a_streamed_stack_runs_a_users_experts(stacks):
+    """Matrices of one's own packed into the pinned host pool of a streamed stack (and into the device pool of a
+    resident one): the routed layers compute with them.  One expert has blocks of zeros."""
+    cfg, streamed, resident = stacks
+    assert streamed.streaming and not resident.streaming
+    g = torch.Generator(device="cuda").manual_seed(6)
+    H, I, E = streamed.H, streamed.I, streamed.E
+    for l in range(2):
+        for e in range(E):
+            mats = [(torch.randn(s, generator=g, device="cuda") * 0.05).to(torch.bfloat16)
+                    for s in ((I, H), (I, H), (H, I))]
+            if e == 3:
+                mats[0][5, :64] = 0.0
+                mats[2][:, 32:64] = 0.0
+            to = torch.from_numpy(streamed.host_pool_slabs(l)[e])
+            assert pack_mx_expert(*mats, slab=to).data_ptr() == to.data_ptr()
+            pack_mx_expert(*mats, slab=resident.pool[l * E + e])
+            assert torch.equal(resident.pool[l * E + e].cpu(), to)
+    x, out, out2 = streamed.make_inputs(0), streamed.new_output(), streamed.new_output()
+    streamed.forward(x, out)
+    resident.forward(x, out2)
+    torch.cuda.synchronize()
+    for l in range(2):
+        bits = x[l].view(torch.int16).cpu().numpy().view(np.uint16)
+        ref = oracle.moe_layer(bits, streamed.wr[l].cpu().numpy(), None, cfg.top_k,
+                               [np.array(s) for s in streamed.host_pool_slabs(l)], None, I, fmt=1)
+        assert (streamed.idx[l].cpu().numpy() == ref["idx"]).all()
+        for o in (out, out2):
+            err = np.abs(o[l].double().cpu().numpy() - ref["out64"]).max()
+            assert err <= 2e-2 * np.abs(ref["out64"]).max()
+    refused = torch.from_numpy(np.full(streamed.slab, 0xA5, np.uint8))
+    for bad in (refused[:-1], refused.view(torch.int8)):
+        with pytest.raises(ValueError):
+            pack_mx_expert(*mats, slab=bad)
+    assert (refused == 0xA5).all()

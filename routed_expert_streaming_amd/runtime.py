@@ -826,6 +826,8 @@ class MoEStack:
     def _check_norms(self, norms: BlockNorms):
         for name in ("pre", "post", "gate"):
             t = getattr(norms, name)
+            if t is None and name == "pre":
+                raise ValueError("BlockNorms.pre: every layer's input norm needs its weight")
             if t is not None and (tuple(t.shape) != (self.L, self.H) or t.dtype != torch.float32 or
                                   t.device != self.dev or not t.is_contiguous()):
                 raise ValueError(f"BlockNorms.{name}: needs contiguous fp32 [{self.L}, {self.H}] on {self.dev}")

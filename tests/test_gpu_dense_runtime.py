@@ -6,7 +6,7 @@ import torch
 import oracle
 import synth
 from routed_expert_streaming_amd import _lib as L
-from routed_expert_streaming_amd.runtime import MoEStack, MxLinear, pack_mx_expert, quantise_mx
+from routed_expert_streaming_amd.runtime import BlockNorms, MoEStack, MxLinear, pack_mx_expert, quantise_mx
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +128,12 @@ def test_a_streamed_stack_runs_a_users_experts(stacks):
         with pytest.raises(ValueError):
             pack_mx_expert(*mats, slab=bad)
     assert (refused == 0xA5).all()
+
+
+def test_chained_norms_need_their_input_norm(stacks):
+    _, streamed, _ = stacks
+    resid, xs = streamed.chain_buffers()
+    resid.fill_(7.0)
+    with pytest.raises(ValueError):
+        streamed.forward_chained(streamed.make_inputs(0)[0], xs, resid, streamed.new_output(), norms=BlockNorms(None))
+    assert (resid == 7.0).all()

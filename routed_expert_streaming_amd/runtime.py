@@ -114,9 +114,14 @@ RMS_EPS = 1e-6  # eps of the residual stream's RMS normalisation between chained
 @dataclass
 class BlockNorms:
     """The norms around the layers of a chained step (moe_block_norm), all fp32 on the device:
-    pre [L,H], the weight of each layer's input norm; post [L,H], the weight of the norm of each
-    layer's output, or None for no such norm; gate [L,H], a factor per channel of what a layer adds
-    to the residual stream, or None; scale, one factor of it for every layer."""
+    pre [L,H], the weight of each layer's input norm; post [L,H], the weight of the norm of a layer's
+    output, or None for no such norm; gate [L,H], a factor per channel of what a layer adds to the
+    residual stream, or None; scale, one factor of it for every layer.
+
+    A layer's output enters the stream on the way to the next layer, so the step itself does not read the
+    last rows of post and gate: what follows the last layer takes them, with its own norm weight,
+        moe_block_norm(out[L-1], 1, post[L-1], gate[L-1], MOE_GATE_CHANNEL, scale, resid, resid, MOE_FP32,
+                       w_final, T, H, RMS_EPS, x_final)."""
     pre: torch.Tensor
     post: torch.Tensor | None = None
     gate: torch.Tensor | None = None
@@ -838,7 +843,8 @@ class MoEStack:
         layer l's input xs[l] is the stream RMS-normalised after every earlier
         layer's output was added (moe_residual_norm), out[l] is layer l's output.
         With norms, the layers' learned norms, gates and residual scale are applied
-        (moe_block_norm).
+        (moe_block_norm).  The last layer's output is in out only: resid is the stream
+        before it.
 
         Streamed, a layer's routing is known only when the layer before it is
         done, so the copies for its own routing are exposed.  With lookahead = m

@@ -6,7 +6,8 @@ import torch
 import oracle
 import synth
 from routed_expert_streaming_amd import _lib as L
-from routed_expert_streaming_amd.runtime import BlockNorms, MoEStack, MxLinear, pack_mx_expert, quantise_mx
+from routed_expert_streaming_amd.runtime import RMS_EPS, BlockNorms, MoEStack, MxLinear, pack_mx_expert, quantise_mx
+from tests import mxkit
 
 pytestmark = pytest.mark.gpu
 
@@ -130,6 +131,20 @@ def test_a_streamed_stack_runs_a_users_experts(stacks):
     assert (refused == 0xA5).all()
 
 
+def learned(st, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = [1 + 0.2 * torch.randn((st.L, st.H), generator=g, device="cuda") for _ in range(2)]
+    return BlockNorms(*w, torch.rand((st.L, st.H), generator=g, device="cuda"), 0.5)
+
+
+def chain(st, h0, norms, lookahead=0):
+    resid, xs = st.chain_buffers()
+    out = st.new_output()
+    st.forward_chained(h0, xs, resid, out, lookahead, norms=norms)
+    torch.cuda.synchronize()
+    return resid, xs, out
+
+
 def test_chained_norms_need_their_input_norm(stacks):
     _, streamed, _ = stacks
     resid, xs = streamed.chain_buffers()
@@ -137,3 +152,42 @@ def test_chained_norms_need_their_input_norm(stacks):
     with pytest.raises(ValueError):
         streamed.forward_chained(streamed.make_inputs(0)[0], xs, resid, streamed.new_output(), norms=BlockNorms(None))
     assert (resid == 7.0).all()
+
+
+def test_chained_norms_after_the_last_layer(stacks):
+    """The stream does not hold the last layer's output; the call that the documentation gives for it does the rest."""
+    _, streamed, st = stacks
+    h0, norms = st.make_inputs(0)[0], learned(st, 8)
+    resid, xs, out = chain(st, h0, norms)
+    for t in (norms.post, norms.gate):
+        t[-1] = float("nan")  # not read by the step
+    again = chain(st, h0, norms)
+    for a, b in zip((resid, xs, out), again):
+        assert torch.equal(a, b)
+    last = learned(st, 9)
+    x = torch.empty((st.T, st.H), dtype=torch.bfloat16, device="cuda")
+    before = resid.double().cpu().numpy()
+    L.moe_block_norm(out[-1], 1, last.post[-1], last.gate[-1], L.MOE_GATE_CHANNEL, 0.5, resid, resid, L.MOE_FP32,
+                     last.pre[-1], st.T, st.H, RMS_EPS, x, None, torch.cuda.current_stream())
+    host = [t.double().cpu().numpy() for t in (out[-1], last.post[-1], last.gate[-1], last.pre[-1], resid, x)]
+    want = mxkit.block_norm(host[0], True, host[1], host[2], 0.5, before, RMS_EPS)
+    # 8 squares a thread, 6 sums of a wave, mean, eps, root, reciprocal and three products: 21 roundings
+    u = 24 * 2.0 ** -24
+    assert (np.abs(host[4] - want) <= u * np.abs(want - before) + 2.0 ** -24 * np.abs(want)).all()
+    final = mxkit.norm(host[4], host[3], RMS_EPS)
+    assert (np.abs(host[5] - final) <= (2.0 ** -8 * (1 + u) + u) * np.abs(final)).all()
+
+
+@pytest.mark.parametrize("lookahead", [0, 1])
+def test_chained_norms_streamed_equal_resident(lookahead):
+    cfg = synth.get("tiny", fmt=1, layers=3, cap=0.75)
+    streamed, resident = MoEStack(cfg), MoEStack(cfg, cap=1.0)
+    try:
+        assert streamed.streaming and not resident.streaming
+        for step in range(2):
+            h0, norms = resident.make_inputs(step)[0], learned(resident, 10 + step)
+            for a, b in zip(chain(streamed, h0, norms, lookahead), chain(resident, h0, norms)):
+                assert torch.equal(a, b)
+    finally:
+        streamed.close()
+        resident.close()

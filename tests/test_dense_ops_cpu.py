@@ -123,3 +123,18 @@ def test_runtime_refusals():
     odd = torch.zeros((40, 96), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         pack_mx_expert(odd, odd, odd.t())
+
+
+@pytest.mark.parametrize("kind,M,N,K", [(L.MOE_MXFP4, 98, 1030, 20512), (L.MOE_BF16, 65, 130, 6176)])
+def test_matmul_refuses_a_small_workspace(kind, M, N, K):
+    """Sizes whose K is split: the parts' sums need a workspace, and less of it, none or one off its alignment is
+    refused before anything runs."""
+    a_stride = L.moe_mx_row_bytes(K) if kind == L.MOE_MXFP4 else 2 * K
+    need = L.moe_mx_matmul_workspace_bytes(M, N, K, kind)
+    assert need > 0 and need % (4 * M * N) == 0
+
+    def m(ws, nbytes):
+        return status(L.moe_mx_matmul, FAKE, kind, a_stride, FAKE, L.moe_mx_row_bytes(K), M, N, K, None, FAKE,
+                      L.MOE_FP32, 4 * N, ws, nbytes)
+    assert m(FAKE, need - 1) == L.MOE_E_NOMEM and m(FAKE, 0) == L.MOE_E_NOMEM and m(None, need) == L.MOE_E_NOMEM
+    assert m(FAKE + 8, need) == L.MOE_E_ARG

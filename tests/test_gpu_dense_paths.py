@@ -1,0 +1,120 @@
+"""Every kernel, tile, part of K and row form of the dense MXFP4 operators that their launch rules can choose."""
+import numpy as np
+import pytest
+import torch
+
+from routed_expert_streaming_amd import _lib as L
+from tests import mxkit
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    L.lib()
+    torch.cuda.set_device(0)
+    yield
+    torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ product
+# (M, N, K, parts of K): 64 x 64 tiles, 128 x 128, 256 x 192 (bf16 128 x 256), the rows kernels.  K past 2048 brings a
+# tile's scales in more than once; most last groups of 128 columns, last parts and last tiles are cut short, N is odd,
+# even and a multiple of what a 16-byte store holds.
+MX_PARTS = [(65, 130, 32800, 8), (98, 1030, 20512, 4), (98, 2168, 8224, 2), (65, 3001, 4128, 1),
+            (98, 2168, 32800, 8), (200, 2169, 12320, 4), (520, 1801, 8224, 2), (520, 1801, 4128, 1),
+            (520, 1801, 32800, 8), (1000, 2169, 20512, 4), (1030, 4090, 12320, 2), (2040, 2167, 4128, 1),
+            (65, 3000, 4128, 1), (520, 1800, 4128, 1), (2040, 2168, 4128, 1), (40, 33, 6176, 1),
+            (32, 6001, 1056, 1), (16, 5000, 6176, 1), (8, 4100, 6176, 1)]
+BF16_PARTS = [(65, 130, 32800, 8), (65, 130, 6176, 4), (98, 2169, 4128, 2), (40, 4100, 2080, 1),
+              (1500, 131, 32800, 8), (65, 5000, 6176, 4), (520, 1801, 4128, 2), (2040, 1030, 4128, 1),
+              (257, 1801, 32800, 8), (200, 5000, 12320, 4), (385, 5000, 12320, 2), (2040, 2169, 4128, 1),
+              (40, 4104, 2080, 1), (2040, 1032, 4128, 1), (2040, 2168, 4128, 1), (40, 33, 2080, 1),
+              (32, 6001, 544, 1), (16, 5000, 6176, 1), (3, 4099, 6176, 1)]
+
+
+def exact_operands(kind, M, N, K, seed):
+    """(a, its values, w, its values, bias, unit of a product).  Scale bytes are drawn per block on both sides (125 ..
+    129, for the longest rows 126 .. 128), so that a scale of another block, row or run is seen."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    low, high = (125, 129) if K < 16384 else (126, 128)
+
+    def rows(R):
+        codes = torch.randint(0, 16, (R, K), generator=g, device="cuda", dtype=torch.uint8)
+        scales = torch.randint(low, high + 1, (R, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+        packed = torch.zeros((R, mxkit.row_bytes(K)), dtype=torch.uint8, device="cuda")
+        packed[:, :K // 2] = codes[:, 0::2] + 16 * codes[:, 1::2]
+        packed[:, K // 2:K // 2 + K // 32] = scales
+        e2m1 = torch.tensor([*mxkit.MAGNITUDES, *-mxkit.MAGNITUDES], device="cuda")
+        v = e2m1[codes.int()].view(R, -1, 32) * torch.exp2(scales.double() - 127).unsqueeze(-1)
+        v = v.reshape(R, K)
+        few = slice(0, 2)
+        assert np.array_equal(v[few].cpu().numpy(), mxkit.values(codes[few].cpu().numpy().astype(np.int64),
+                                                                 scales[few].cpu().numpy().astype(np.int64)))
+        return packed, v
+    w, wv = rows(N)
+    if kind == L.MOE_MXFP4:
+        a, av = rows(M)
+    else:
+        av = torch.randint(-16, 17, (M, K), generator=g, device="cuda").double() * 0.25
+        a = av.to(torch.bfloat16)
+    b = torch.randint(-64, 65, (N,), generator=g, device="cuda").float()
+    least = 0.5 * 2.0 ** (low - 127)  # a weight's unit, and an MXFP4 activation's
+    return a, av, w, wv, b, least * (least if kind == L.MOE_MXFP4 else 0.25)
+
+
+@pytest.mark.parametrize("kind,M,N,K,parts", [(L.MOE_MXFP4, *s) for s in MX_PARTS] +
+                         [(L.MOE_BF16, *s) for s in BF16_PARTS])
+def test_matmul_exact_sums_in_parts(kind, M, N, K, parts):
+    """Every product is a multiple of one unit, and the magnitudes of a result's terms add up to less than 2^24 of
+    them (checked on the values themselves): 32 bits hold every partial sum, so every order gives what 64 bits do."""
+    a, av, w, wv, b, unit = exact_operands(kind, M, N, K, M + N + K)
+    assert float((av.abs() @ wv.abs().t()).max()) + 64 < 2.0 ** 24 * unit
+    a_stride, w_stride = a.stride(0) * a.element_size(), w.stride(0)
+    need = L.moe_mx_matmul_workspace_bytes(M, N, K, kind)
+    assert need == (0 if parts == 1 else 4 * parts * M * N)
+    ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN sums
+    plain = av @ wv.t()
+    for bias in (b, None):
+        want = plain + (0.0 if bias is None else bias.double())
+        for y_type, dtype in ((L.MOE_FP32, torch.float32), (L.MOE_BF16, torch.bfloat16)):
+            for pitch in (N + 5, (N + 7) // 8 * 8):  # rows of y off 16-byte boundaries, and on them
+                y = torch.full((M + 1, pitch), 5.0, dtype=dtype, device="cuda")
+                L.moe_mx_matmul(a, kind, a_stride, w, w_stride, M, N, K, bias, y, y_type, pitch * y.element_size(), ws,
+                                need, torch.cuda.current_stream())
+                assert torch.equal(y[:M, :N], want.float().to(dtype)), (y_type, bias is None, pitch)
+                y[:M, :N] = 5.0
+                assert (y == 5.0).all() and (ws[need:] == 0xFF).all()
+    if need:
+        with pytest.raises(L.MoEError) as ei:
+            L.moe_mx_matmul(a, kind, a_stride, w, w_stride, M, N, K, None, y, L.MOE_BF16, 2 * y.stride(0), ws, need - 1,
+                            torch.cuda.current_stream())
+        assert ei.value.status == L.MOE_E_NOMEM and (y == 5.0).all()
+
+
+@pytest.mark.parametrize("kind", [L.MOE_MXFP4, L.MOE_BF16])
+@pytest.mark.parametrize("M", [1, 5, 20, 40, 150, 300])
+def test_matmul_keeps_subnormal_sums(M, kind):
+    """Results in and around fp32's subnormal range: every product is a multiple of 2^-137 and the magnitudes of a
+    result's terms stay below 2^-113, so 32 bits hold the sums unless something flushes them to zero."""
+    rng = np.random.default_rng(M)
+    K, N = 288, 40
+    c, s = mxkit.random_rows(rng, N, K, 60, 60)
+    w, wv = torch.from_numpy(mxkit.pack(c, s)).cuda(), mxkit.values(c, s)
+    if kind == L.MOE_MXFP4:
+        c, s = mxkit.random_rows(rng, M, K, 60, 60)
+        a, av = torch.from_numpy(mxkit.pack(c, s)).cuda(), mxkit.values(c, s)
+    else:
+        av = rng.integers(-16, 17, (M, K)) * 0.25 * 2.0 ** -67
+        a = torch.from_numpy(av).cuda().to(torch.bfloat16)
+    want = av @ wv.T
+    assert (np.abs(av) @ np.abs(wv).T).max() < 2.0 ** -113  # 24 bits of the unit
+    assert ((want != 0) & (np.abs(want) < 2.0 ** -126)).any()
+    y = torch.zeros((M, N), device="cuda")
+    need = L.moe_mx_matmul_workspace_bytes(M, N, K, kind)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    L.moe_mx_matmul(a, kind, a.stride(0) * a.element_size(), w, mxkit.row_bytes(K), M, N, K, None, y, L.MOE_FP32, 4 * N,
+                    ws, need, torch.cuda.current_stream())
+    assert np.array_equal(y.double().cpu().numpy(), want)

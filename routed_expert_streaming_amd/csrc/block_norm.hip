@@ -274,9 +274,15 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(NormArgs a) {
 template <int V, bool RF32, bool STREAM>
 void launch(const NormArgs &a, int T, int threads, int items, hipStream_t s) {
     const dim3 grid(T), block(threads);
-    if (items == 1)
-        hipLaunchKernelGGL((block_norm_kernel<V, 1, RF32, STREAM>), grid, block, 0, s, a);
-    else if (items == 2)
+    // One item holds eight values of each of 1024 threads, and is taken below 256 rows: a
+    // bf16 stream of that is never large enough to be written past the caches.
+    static_assert(255 * 8 * kMaxThreads * 2 < kStreamFrom, "one item, bf16, past the caches");
+    if constexpr (RF32 || !STREAM)
+        if (items == 1) {
+            hipLaunchKernelGGL((block_norm_kernel<V, 1, RF32, STREAM>), grid, block, 0, s, a);
+            return;
+        }
+    if (items <= 2)
         hipLaunchKernelGGL((block_norm_kernel<V, 2, RF32, STREAM>), grid, block, 0, s, a);
     else if (items <= 4)
         hipLaunchKernelGGL((block_norm_kernel<V, 4, RF32, STREAM>), grid, block, 0, s, a);

@@ -118,3 +118,87 @@ def test_matmul_keeps_subnormal_sums(M, kind):
     L.moe_mx_matmul(a, kind, a.stride(0) * a.element_size(), w, mxkit.row_bytes(K), M, N, K, None, y, L.MOE_FP32, 4 * N,
                     ws, need, torch.cuda.current_stream())
     assert np.array_equal(y.double().cpu().numpy(), want)
+
+
+# ------------------------------------------------------------------ norms around a block
+def norm_roundings(T, H, wide):
+    """Roundings on the way to a row's factor and through it: a thread's squares, one after the other (eight values, or
+    one, at a time: one time for few rows, two from 256 on, up to four, or as often as 1024 threads need for a
+    row beyond that), 6 sums of a wave, the waves' sums, mean, eps, root, reciprocal and three products."""
+    V = 8 if wide else 1
+    units = -(-H // V)
+    items = 1 if T < 256 else 2
+    while items < 4 and units > items * 1024:
+        items *= 2
+    threads = min(-(-(-(-units // items)) // 64) * 64, 1024)
+    return V * -(-units // threads) + 6 + threads // 64 - 1 + 7
+
+
+def offset(t, elements):
+    """t's values from `elements` elements into a fresh buffer on."""
+    flat = torch.empty(t.numel() + elements, dtype=t.dtype, device=t.device)
+    flat[elements:] = t.flatten()
+    return flat[elements:].view(t.shape)
+
+
+def rms(v, w, eps):
+    x = v / torch.sqrt((v * v).mean(1, keepdim=True) + eps)
+    return x if w is None else x * w
+
+
+# rows in registers (one, two, four values or eights of them a thread) and rows read again; streams below and from 4
+# MiB on, which are written past the caches; widths and pointers that 16-byte accesses cannot take
+@pytest.mark.parametrize("rt", [L.MOE_FP32, L.MOE_BF16])
+@pytest.mark.parametrize("T,H,shift", [(3, 1001, 0), (300, 1001, 0), (2, 3001, 0), (3, 5001, 0), (3, 5000, 1),
+                                       (2, 6144, 0), (257, 2048, 0), (3, 20000, 0), (3, 40000, 0),
+                                       (200, 6144, 0), (600, 6144, 0), (70, 20000, 0), (120, 20000, 0),
+                                       (40, 40000, 0), (80, 40000, 0), (2048, 6143, 0)])
+def test_block_norm_on_every_path(T, H, shift, rt):
+    g = torch.Generator(device="cuda").manual_seed(T * 7 + H)
+    dtype = torch.float32 if rt == L.MOE_FP32 else torch.bfloat16
+    eps, scale = 1e-6, 0.37
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device="cuda")
+    add = offset((normal(T, H) * 3).to(torch.bfloat16), shift)
+    resid = offset((normal(T, H) * 5).to(dtype), shift)
+    w_post, w_pre = 1 + 0.3 * normal(H), 1 + 0.3 * normal(H)
+    gate = offset(normal(T, H).to(torch.bfloat16), shift)
+    wide = H % 8 == 0 and not shift
+    u = norm_roundings(T, H, wide) * 2.0 ** -24
+    s = torch.cuda.current_stream()
+
+    def call(resid, out, x, rows):
+        L.moe_block_norm(add, 1, w_post, gate, L.MOE_GATE_ELEMENT, scale, resid, out, rt, w_pre, T, H, eps, x, rows, s)
+    out, x = torch.full((T + 1, H), 3.0, dtype=dtype, device="cuda"), torch.full((T + 1, H), 3.0, dtype=torch.bfloat16,
+                                                                                 device="cuda")
+    rows = None
+    if wide:
+        rows = torch.full((T + 1, mxkit.row_bytes(H)), 0xA5, dtype=torch.uint8, device="cuda")
+    before = resid.clone()
+    call(resid, out, x, rows)
+    assert torch.equal(resid, before) and (out[T] == 3.0).all() and (x[T] == 3.0).all()
+    d = rms(add.double(), w_post.double(), eps) * gate.double() * float(np.float32(scale))
+    want = before.double() + d
+    tol = u * d.abs() + 2.0 ** -24 * want.abs()
+    if rt == L.MOE_BF16:
+        tol = tol + 2.0 ** -8 * (want.abs() + tol)
+    assert ((out[:T].double() - want).abs() <= tol).all()
+    nx = rms(out[:T].double(), w_pre.double(), eps)
+    assert ((x[:T].double() - nx).abs() <= (2.0 ** -8 * (1 + u) + u) * nx.abs()).all()
+    if wide:
+        packed = torch.empty_like(rows[:T])
+        L.moe_mx_quant(x, L.MOE_BF16, 2 * H, T, H, L.MOE_MX_SCALE_FLOOR, packed, mxkit.row_bytes(H), None, s)
+        assert torch.equal(rows[:T], packed) and (rows[T] == 0xA5).all()
+        rows.fill_(0xA5)
+        call(resid, out, None, rows)  # the rows alone
+        assert torch.equal(rows[:T], packed) and (rows[T] == 0xA5).all()
+    # in place, with and without a next block: the same bits
+    for follow in (x.clone(), None):
+        inplace = offset(before, shift)
+        call(inplace, inplace, follow, None)
+        assert torch.equal(inplace, out[:T]) and (follow is None or torch.equal(follow, x))
+    # the pre-norm of the kept stream alone
+    alone = torch.full_like(x, 3.0)
+    L.moe_block_norm(None, 0, None, None, L.MOE_GATE_NONE, scale, inplace, None, rt, w_pre, T, H, eps, alone, None, s)
+    assert torch.equal(alone, x)

@@ -52,6 +52,7 @@
 #include "common.h"
 #include "dequant.h"
 #include "ffn.h"
+#include "lds_dma.h"
 
 namespace {
 
@@ -92,30 +93,7 @@ struct __attribute__((aligned(16))) XStage {
     uint8_t x[kMC * kXRow];
 };
 
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(1))) const moe_u32x4 gu32x4;
-
-__device__ __forceinline__ uint32_t lds_addr(const void *lds) {
-    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_u8 *)lds);
-}
-// Direct global->LDS load: lane l's 16 bytes from g land at LDS byte lds + 16*l
-// (lds uniform).  Written as inline asm because the compiler, seeing these
-// loads, would make every later LDS read wait for all of them (it cannot tell
-// the ring's stages apart); completion is tracked with explicit vmcnt waits
-// instead.  The memory clobber keeps the compiler's own loads in program order
-// around it, which the wait counts rely on.
-// base (uniform, in SGPRs) + off (this lane's 32-bit byte offset).
-// The s_nop gives the 5 wait states a vector memory instruction needs after a
-// VALU instruction wrote an SGPR it reads (and the one after an M0 write): the
-// compiler inserts these for its own instructions but cannot see into inline
-// asm, and under register pressure it restores a spilled base half with
-// v_readlane right before the load -- without the wait the load can use the
-// stale half and go to a wrong address.
-__device__ __forceinline__ void dma16(const void *base, uint32_t off, uint32_t lds) {
-    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
-}
-
-constexpr int kWaitVm(int n) { return (n & 0xF) | (0x7 << 4) | (0xF << 8) | ((n >> 4) << 14); }
 
 // Loads a wave may still have in flight at the end of step gstep such that the
 // activation tile gstep + 1 has landed (vmcnt counts a wave's loads in issue
@@ -139,20 +117,6 @@ constexpr int loads_after_tile(int A, int D, int P, int TM, int gstep) {
         if (seen) count += TM;
     }
     return count;
-}
-
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    asm volatile("s_waitcnt %0" ::"n"(kWaitVm(N)) : "memory");
-}
-
-// Workgroup barrier without a memory fence (a fence would wait for every load
-// in flight); this wave's LDS reads are complete before it arrives.
-__device__ __forceinline__ void ring_barrier() {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
 }
 
 // 8 consecutive weights of one row (codes dword, its block record) -> bf16x8.
@@ -186,28 +150,6 @@ __device__ __forceinline__ Dequant dequant_consts() {
     asm volatile("v_mov_b32 %0, 0x64006400" : "=v"(d.magic_lo));
     asm volatile("v_mov_b32 %0, 0x54005400" : "=v"(d.magic_hi));
     return d;
-}
-
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-
-template <int N>
-struct IntC {
-    static constexpr int value = N;
-};
-
-// f(IntC<B>{}), f(IntC<B + 1>{}), ..., f(IntC<E - 1>{})
-template <int B, int E, class F>
-__device__ __forceinline__ void static_for(F &&f) {
-    if constexpr (B < E) {
-        f(IntC<B>{});
-        static_for<B + 1, E>(f);
-    }
-}
-
-// two floats -> bf16 pair (round to nearest even), lo in bits 0-15
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((float __attribute__((ext_vector_type(2)))){lo, hi},
-                                                                bf16x2_t));
 }
 
 // (a & mask) | pattern as one instruction (the compiler splits it into two)

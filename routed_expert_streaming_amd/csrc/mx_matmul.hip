@@ -19,6 +19,7 @@
 // then by the matrix cores).
 #include "common.h"
 #include "dequant.h"
+#include "lds_dma.h"
 #include "mx_quant.h"
 
 namespace {
@@ -58,12 +59,6 @@ __device__ __forceinline__ f32x4_t mfma_mx(const uint4 w, const uint4 a, f32x4_t
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, c, 4, 4, B, ws, B, as);  // 4: FP4 E2M1
 }
 
-// Two floats -> bf16 pair, rounded to nearest even, lo in bits 0-15 (one instruction).
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    return __builtin_bit_cast(
-        uint32_t, __builtin_convertvector((float __attribute__((ext_vector_type(2)))){lo, hi}, moe_bf16x2));
-}
-
 // Four outputs n .. n+3 of row m (those below N), bias added, rounded once.
 __device__ __forceinline__ void store4(const MatArgs &p, int m, int n, const f32x4_t v) {
     if (m >= p.M) return;
@@ -89,45 +84,6 @@ __device__ __forceinline__ void store4(const MatArgs &p, int m, int n, const f32
             for (int j = 0; j < 4; ++j)
                 if (n + j < p.N) o[j] = (uint16_t)pack_bf16(f[j], 0.0f);
         }
-    }
-}
-
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-
-__device__ __forceinline__ uint32_t lds_addr(const void *lds) {
-    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_u8 *)lds);
-}
-// Direct global -> LDS load of 16 bytes per lane: base (uniform) + off (this lane's
-// byte offset) -> LDS byte lds + 16 * lane.  Inline asm, because the compiler would
-// make every LDS read wait for all of these; the waits below count them instead
-// (a wave's loads complete in order).  s_nop 4: the wait states a vector memory
-// instruction needs after a VALU write of an SGPR it reads and after the M0 write.
-__device__ __forceinline__ void dma16(const void *base, uint32_t off, uint32_t lds) {
-    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
-}
-// Waits until at most N of the wave's vector memory operations are in flight.
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-// Workgroup barrier that leaves vector memory in flight; this wave's LDS accesses
-// are done when it arrives.
-__device__ __forceinline__ void ring_barrier() {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
-template <int N>
-struct IntC {
-    static constexpr int value = N;
-};
-template <int B, int E, class F>
-__device__ __forceinline__ void static_for(F &&f) {
-    if constexpr (B < E) {
-        f(IntC<B>{});
-        static_for<B + 1, E>(f);
     }
 }
 

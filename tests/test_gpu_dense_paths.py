@@ -202,3 +202,90 @@ def test_block_norm_on_every_path(T, H, shift, rt):
     alone = torch.full_like(x, 3.0)
     L.moe_block_norm(None, 0, None, None, L.MOE_GATE_NONE, scale, inplace, None, rt, w_pre, T, H, eps, alone, None, s)
     assert torch.equal(alone, x)
+
+
+# ------------------------------------------------------------------ more rows than one launch takes, and one row
+def test_quant_in_two_launches():
+    """2^28 rows of 32 columns are 2^30 lanes, the most of one launch: five rows more."""
+    rows, K = (1 << 28) + 5, 32
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty((rows, K), dtype=torch.bfloat16, device="cuda")
+    x.fill_(1.0)
+    edge = [0, 1, (1 << 28) - 1, 1 << 28, rows - 1]
+    x[edge] = torch.randn((len(edge), K), generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.full((rows, 32), 0xA5, dtype=torch.uint8, device="cuda")
+    vals = torch.zeros((rows, K), dtype=torch.bfloat16, device="cuda")
+    L.moe_mx_quant(x, L.MOE_BF16, 2 * K, rows, K, L.MOE_MX_SCALE_FLOOR, out, 32, vals, torch.cuda.current_stream())
+    codes, scales = mxkit.quantise(x[edge].double().cpu().numpy(), "floor")
+    assert np.array_equal(out[edge].cpu().numpy(), mxkit.pack(codes, scales))
+    assert np.array_equal(vals[edge].double().cpu().numpy(), mxkit.values(codes, scales))
+    ones = out[2].clone()  # a row of ones; every other row but the edge ones is one
+    assert ones[16] == 125 and (ones[:16] == 0x66).all()
+    same = (out.view(torch.int64) == ones.view(torch.int64)).all(1)
+    assert int(same.sum()) == rows - len(edge) and (vals[2:1000] == 1.0).all() and (vals[-4:-1] == 1.0).all()
+
+
+@pytest.mark.parametrize("kind", [L.MOE_GATE_ROW, L.MOE_GATE_ELEMENT])
+def test_block_norm_in_two_launches(kind):
+    """2^20 rows are the most of one launch: the others, on every operand, against a call on those rows alone."""
+    T, H = (1 << 20) + 37, 32
+    g = torch.Generator(device="cuda").manual_seed(2)
+    add = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    resid = torch.randn((T, H), generator=g, device="cuda")
+    gate = torch.rand((T,) if kind == L.MOE_GATE_ROW else (T, H), generator=g, device="cuda")
+    gate = gate if kind == L.MOE_GATE_ROW else gate.to(torch.bfloat16)
+
+    def call(lo, hi):
+        n = hi - lo
+        out, x = torch.empty((n, H), device="cuda"), torch.empty((n, H), dtype=torch.bfloat16, device="cuda")
+        rows = torch.empty((n, mxkit.row_bytes(H)), dtype=torch.uint8, device="cuda")
+        L.moe_block_norm(add[lo:hi], 1, None, gate[lo:hi], kind, 0.5, resid[lo:hi], out, L.MOE_FP32, None, n, H, 1e-6,
+                         x, rows, torch.cuda.current_stream())
+        return out, x, rows
+    whole = call(0, T)
+    for lo, hi in ((0, 8), ((1 << 20) - 8, 1 << 20), (1 << 20, T)):
+        for a, b in zip(whole, call(lo, hi)):
+            assert torch.equal(a[lo:hi], b)
+
+
+@pytest.mark.parametrize("kind", [L.MOE_MXFP4, L.MOE_BF16])
+def test_matmul_rows_in_two_launches(kind):
+    """Rows of W far apart take the rows kernel at any M, a grid of which holds 65535 tiles of 32 rows."""
+    M, N, K, apart = 65535 * 32 + 41, 3, 64, 9 << 20
+    g = torch.Generator(device="cuda").manual_seed(3)
+    packed = torch.zeros((N, mxkit.row_bytes(K)), dtype=torch.uint8, device="cuda")
+    packed[:, :K // 2] = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    packed[:, K // 2:K // 2 + K // 32] = 127
+    w = torch.zeros((N, apart), dtype=torch.uint8, device="cuda")
+    w[:, :packed.shape[1]] = packed
+    if kind == L.MOE_MXFP4:
+        a = torch.zeros((M, mxkit.row_bytes(K)), dtype=torch.uint8, device="cuda")
+        a[:, :K // 2] = torch.randint(0, 256, (M, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+        a[:, K // 2:K // 2 + K // 32] = 126
+    else:
+        a = torch.randint(-16, 17, (M, K), generator=g, device="cuda").to(torch.bfloat16)
+    y = torch.full((M + 1, N), 5.0, device="cuda")
+    L.moe_mx_matmul(a, kind, a.stride(0) * a.element_size(), w, apart, M, N, K, None, y, L.MOE_FP32, 4 * N, None, 0,
+                    torch.cuda.current_stream())
+    assert (y[M] == 5.0).all()
+
+    def values(rows):
+        r = rows.cpu().numpy()
+        codes = np.stack([r[:, :K // 2] & 15, r[:, :K // 2] >> 4], -1).reshape(len(r), K).astype(np.int64)
+        return mxkit.values(codes, r[:, K // 2:K // 2 + K // 32].astype(np.int64))
+    for lo, hi in ((0, 70), (65535 * 32 - 35, 65535 * 32 + 35), (M - 35, M)):
+        av = values(a[lo:hi]) if kind == L.MOE_MXFP4 else a[lo:hi].double().cpu().numpy()
+        assert np.array_equal(y[lo:hi].double().cpu().numpy(), av @ values(packed).T)
+
+
+@pytest.mark.parametrize("kind", [L.MOE_MXFP4, L.MOE_BF16])
+def test_strides_of_one_row_are_not_read(kind):
+    K, odd = 288, -7
+    a, av, w, wv, _, _ = exact_operands(kind, 1, 1, K, 5)
+    y = torch.zeros(2, device="cuda")
+    L.moe_mx_matmul(a, kind, odd, w, odd, 1, 1, K, None, y, L.MOE_FP32, odd, None, 0, torch.cuda.current_stream())
+    assert float(y[0]) == float(av @ wv.t()) and float(y[1]) == 0.0
+    if kind == L.MOE_BF16:
+        out = torch.zeros(mxkit.row_bytes(K), dtype=torch.uint8, device="cuda")
+        L.moe_mx_quant(a, kind, odd, 1, K, L.MOE_MX_SCALE_FIT, out, odd, None, torch.cuda.current_stream())
+        assert np.array_equal(out.cpu().numpy(), mxkit.pack(*mxkit.quantise(av.cpu().numpy(), "fit"))[0])

@@ -29,7 +29,7 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int64_t kMaxStride = 1 << 28;  // 16 rows' offsets stay in 32 bits
-constexpr int kMaxRows = 1 << 26;        // M and N: a grid's threads stay below 2^32
+constexpr int kMaxRows = 1 << 26;        // M and N: a rows kernel's grid stays below 2^32 threads
 constexpr int kMaxK = 1 << 27;
 
 struct MatArgs {
@@ -792,6 +792,7 @@ struct Plan {
     int k_part, parts;
 };
 constexpr int kCUs = 256;
+constexpr int64_t kMostWgs = (1LL << 32) / 512 - 8;  // of a tile kernel's 512 threads: below 2^32 in all
 
 int64_t few_bytes(int M, int K) { return (int64_t)((K + 511) / 512) * M * kXRow; }  // bf16 A in LDS
 constexpr int64_t kFewMost = 136 << 10;
@@ -829,6 +830,7 @@ Plan plan(bool mx, int M, int N, int K, bool near) {
             const int64_t part = over((int)over(K, 512), parts) * 512;
             if (parts > 1 && part * (parts - 1) >= K) break;  // a part would be empty
             const int64_t wgs = over(M, t.bm) * over(N, t.bn) * parts, rest = wgs % kCUs;
+            if (wgs > kMostWgs) break;
             const double groups = (double)(part < K ? part : K) / 128;
             const double join = parts > 1 ? 3.0 + (double)M * N * 8.0 * parts / 4e6 : 0.0;
             const double whole = t.a + t.full * groups;

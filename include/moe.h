@@ -494,16 +494,16 @@ int moe_mx_quant(const void *x, int x_type, int64_t x_stride, int rows, int K, i
 /* y[m,n] = sum_k A[m,k] * W[n,k] + bias[n], sums in fp32, rounded once.
  * a [M, K]: bf16 (a_type MOE_BF16; the weights are then formed in bf16, exact for
  * scale bytes up to 252) or MXFP4 rows (MOE_MXFP4); w [N] MXFP4 rows; bias [N]
- * fp32 or NULL; y [M, N] bf16 or fp32 (y_type).  M and N from 0 (a no-op) to 2^26, K
- * a multiple of 32 up to 2^27, operands' rows at most 2^28 bytes apart.  A scale byte of 255 makes every output it enters NaN.  A row of y
- * does not depend on the other rows of a, but its last bits may depend on M
- * (which kernel runs).  workspace: moe_mx_matmul_workspace_bytes(M, N, K,
- * a_type) bytes (contents don't care, 16-byte aligned; calls sharing it must not
- * overlap in time; NULL when 0).  MOE_E_SHAPE for sizes or strides beyond these or
- * a stride below its row; MOE_E_ARG for negative sizes, unknown types, NULL pointers, a or w
- * pointers or strides that are not multiples of 16 bytes, or y and bias not
- * aligned to their types; MOE_E_NOMEM for a small workspace.  y must not overlap
- * the inputs. */
+ * fp32 or NULL; y [M, N] bf16 or fp32 (y_type).  M and N from 0 (a no-op) to 2^26,
+ * K a multiple of 32 up to 2^27, operands' rows at most 2^28 bytes apart.  A scale
+ * byte of 255 makes every output it enters NaN.  A row of y does not depend on the
+ * other rows of a, but its last bits may depend on M (which kernel runs).
+ * workspace: moe_mx_matmul_workspace_bytes(M, N, K, a_type) bytes (contents don't
+ * care, 16-byte aligned; calls sharing it must not overlap in time; NULL when 0).
+ * MOE_E_SHAPE for sizes or strides beyond these or a stride below its row;
+ * MOE_E_ARG for negative sizes, unknown types, NULL pointers, a or w pointers or
+ * strides that are not multiples of 16 bytes, or y, bias and workspace not aligned;
+ * MOE_E_NOMEM for a small workspace.  y must not overlap the inputs. */
 size_t moe_mx_matmul_workspace_bytes(int M, int N, int K, int a_type);
 int moe_mx_matmul(const void *a, int a_type, int64_t a_stride, const uint8_t *w, int64_t w_stride, int M, int N, int K,
                   const float *bias, void *y, int y_type, int64_t y_stride, void *workspace, size_t workspace_bytes,
@@ -521,8 +521,10 @@ int moe_mx_matmul(const void *a, int a_type, int64_t a_stride, const uint8_t *w,
  * MOE_BF16; the same buffer or two that do not overlap); w_post, w_pre [H] fp32;
  * x_next [T,H] bf16 or NULL; x_rows [T] contiguous MXFP4 rows of x_next's values
  * (as moe_mx_quant makes them from x_next, floor rule) or NULL; both may be NULL
- * after the last block.  Sums are fp32 in a fixed order.  x_next and x_rows must
- * not overlap the inputs.  A row of zeros with eps = 0 gives NaN.
+ * after the last block.  Squares and their sums are fp32, in a fixed order: a row
+ * whose mean square is beyond fp32 (values of 1e19 and more) normalises to zeros,
+ * and with eps = 0 one whose squares are all below it (values under 1e-23) to
+ * infinities, a row of zeros to NaN.  x_next and x_rows must not overlap the inputs.
  * MOE_E_ARG for T < 0, H <= 0, eps outside [0, 1], an unknown type or gate kind,
  * w_post without post_norm, NULL pointers, or a pointer not aligned to its type;
  * with x_rows MOE_E_SHAPE unless H % 32 == 0 and MOE_E_ARG unless every pointer is

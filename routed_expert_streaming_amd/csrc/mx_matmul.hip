@@ -186,14 +186,16 @@ __device__ __forceinline__ void zero_past_k(const MatArgs &p, uint8_t *xs, int r
 // whole lines, and product j takes block 4q + j from every quarter.  W is read once
 // from memory, the next run's while this one is multiplied; A comes from the caches.
 // 1 x 65536 x 4096 in MXFP4 takes 30 us (142 MB, 4.7 TB/s; a large copy reaches 4.9),
-// 32 x 6144 x 6144 8.3 us.  K split over the waves of a workgroup, not whole rows to
+// 32 x 6144 x 6144 8.3 us (2.5 TB/s: 192 workgroups, whose 8 waves have 12 runs between
+// them, and A's run is loaded only where it is used).  K split over the waves of a workgroup, not whole rows to
 // each, because 16 whole rows at a time keep the memory's pages open: with the same
 // loads alone a workgroup over 16 rows read 5.8 TB/s, one over 64 rows 4.0.
 // Rows past M or N repeat the last row (their results are not stored); blocks past K
 // repeat the row's last block, as zeros.
 //
 // bf16 A: a run of a row is 1 KB, one direct global -> LDS load into the wave's own
-// rows (XR of them, two runs in turn).
+// rows (XR of them, two runs in turn).  32 rows of two waves fill a CU's LDS, and two of
+// its SIMDs have no wave: 32 x 6144 x 6144 14.9 us, bound by six turns one after the other.
 template <bool MX, int MT, int NT, int WK, int XR>
 __global__ __launch_bounds__(64 * WK) void mx_matmul_rows_kernel(MatArgs p) {
     static_assert(MX || XR <= 16 * MT, "rows of A in LDS");
@@ -302,7 +304,8 @@ __global__ __launch_bounds__(64 * WK) void mx_matmul_rows_kernel(MatArgs p) {
 // joined.  4 x 65536 x 4096 (fp32 y): 32 us, 4.5 TB/s over W; from global memory, 16
 // scattered loads a run, 42 us, and with A brought in for each tile 40 us.  Four waves
 // and three workgroups a CU: eight waves each took 35 us, four workgroups 42 (the last
-// of 16 tiles a CU then runs alone).
+// of 16 tiles a CU then runs alone).  1 x 4096 x 4096, one tile a CU, takes 4.2 us: A, then
+// two runs a wave one after the other, then the join, each a latency.
 template <int WK, int KB>
 __global__ __launch_bounds__(64 * WK) void mx_matmul_few_kernel(MatArgs p, int tiles) {
     __shared__ uint4 xs4[KB * 64];
@@ -318,7 +321,8 @@ __global__ __launch_bounds__(64 * WK) void mx_matmul_few_kernel(MatArgs p, int t
     for (int h = wave; h < runs; h += WK)
         for (int m = 0; m < p.M; ++m) dma_run(p, m, h, lane, lds0 + (uint32_t)(h * p.M + m) * kXRow);
     wait_vm<0>();  // a wave reads only what it loaded itself
-    if (blocks % 16 != 0 && (runs - 1) % WK == wave) zero_past_k(p, xs + (size_t)(runs - 1) * p.M * kXRow, p.M, runs - 1, lane);
+    if (blocks % 16 != 0 && (runs - 1) % WK == wave)
+        zero_past_k(p, xs + (size_t)(runs - 1) * p.M * kXRow, p.M, runs - 1, lane);
     const uint8_t *xrow = xs + min(r, p.M - 1) * kXRow + 256 * q;
     int i = 0;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++i) {
@@ -363,12 +367,14 @@ __global__ __launch_bounds__(64 * WK) void mx_matmul_few_kernel(MatArgs p, int t
 //    thread per row turns 16 of them into one dword per quarter whose byte b belongs to
 //    group b: the products select it by its number (MXFP4) or shift it out (bf16).
 // Measured, 2048 x 6144 x 6144 in MXFP4, 256 x 192 tiles, one a CU: 44 us, 3.5
-// PFLOP/s.  A 128-column group takes 0.63 us; its products alone 0.45 (the scaled FP4
-// products reach 7.5 PFLOP/s in registers, 20 cycles each), its loads alone 0.35, and
-// the 88 KB of LDS reads and 28 KB of LDS writes 0.39 at 128 bytes a cycle: the three
-// share issue and LDS.  Prologue and epilogue take about 10 us of it.  2048 x 4096 x
-// 6144 with bf16 A, 128 x 256 tiles: 80 us, 1.29 PFLOP/s (bf16 products reach 2.1 in
-// registers; a library product of bf16 matrices of these sizes took 102 us).
+// PFLOP/s.  A 128-column group takes 0.63 us; its products alone 0.45, of which the
+// matrix cores are busy 0.35 (a scaled FP4 product takes 16 cycles of them: in
+// registers two waves a SIMD issue one every 16.7, 8.0 PFLOP/s at the 2.04 GHz that
+// the card then runs at, one wave every 17.5); its loads alone 0.35, and the 88 KB of
+// LDS reads and 28 KB of LDS writes 0.39 at 128 bytes a cycle: the three share issue
+// and LDS.  Prologue and epilogue take about 10 us of it.  2048 x 4096 x 6144 with
+// bf16 A, 128 x 256 tiles: 80 us, 1.29 PFLOP/s (bf16 products reach 2.1 in registers; a
+// library product of bf16 matrices of these sizes took 102 us).
 // The last group may end inside (K % 128 != 0): lanes past K load the last block
 // again, their operands become zeros and their scales 1.
 constexpr int kG = 128;          // columns of a group
@@ -502,7 +508,8 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles, int k_part) {
     const int piece = (lane % PIECES) ^ bank_key<PIECES>(wave * ROWS + lane / PIECES);
     const int piece_a = MX ? piece : r ^ bank_key<16>(4 * (wave - T::W_LOADS) + q);
     // what the last stage's lanes step back by, past K
-    const uint32_t cut = 16 * (piece - min(piece, nb - 1)), cut_a = MX ? cut : 16 * (piece_a - min(piece_a, 4 * nb - 1));
+    const uint32_t cut = 16 * (piece - min(piece, nb - 1));
+    const uint32_t cut_a = MX ? cut : 16 * (piece_a - min(piece_a, 4 * nb - 1));
     uint32_t off[T::PER_WAVE];
 #pragma unroll
     for (int j = 0; j < T::PER_WAVE; ++j) {
@@ -518,7 +525,8 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles, int k_part) {
     auto issue_one = [&](int i, int as, int j) {
         const int c0 = j * T::WAVES + wave, c = c0 < T::LOADS ? c0 : c0 - T::WAVES;
         const uint8_t *base = c < T::W_LOADS ? wbase + T::CODES * (size_t)i : abase + T::A_ROW * (size_t)i;
-        dma16(base, off[j] - (i == ns - 1 ? c < T::W_LOADS ? cut : cut_a : 0u), lds0 + (uint32_t)(as % S) * T::STAGE + 1024u * c);
+        dma16(base, off[j] - (i == ns - 1 ? c < T::W_LOADS ? cut : cut_a : 0u),
+              lds0 + (uint32_t)(as % S) * T::STAGE + 1024u * c);
     };
     // scales: an instruction brings 64 bytes of each of 16 rows (places past the row's
     // last 16 bytes repeat those)
@@ -662,7 +670,8 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles, int k_part) {
         } else {
             bf16x8_t wv[2][NT];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) wv[0][t] = codes_bf16(w[cur][t].x, moe::mx_scale_operand(sw[t] >> 8 * b & 255u));
+            for (int t = 0; t < NT; ++t)
+                wv[0][t] = codes_bf16(w[cur][t].x, moe::mx_scale_operand(sw[t] >> 8 * b & 255u));
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
 #pragma unroll
@@ -685,8 +694,9 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles, int k_part) {
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
                             if (t % MT == u)
-                                wv[(s + 1) & 1][t] = codes_bf16(s == 0 ? w[cur][t].y : s == 1 ? w[cur][t].z : w[cur][t].w,
-                                                                moe::mx_scale_operand(sw[t] >> 8 * b & 255u));
+                                wv[(s + 1) & 1][t] =
+                                    codes_bf16(s == 0 ? w[cur][t].y : s == 1 ? w[cur][t].z : w[cur][t].w,
+                                               moe::mx_scale_operand(sw[t] >> 8 * b & 255u));
                     if (s == 3)
 #pragma unroll
                         for (int j = 0; j < T::PER_WAVE; ++j)
@@ -783,10 +793,12 @@ __global__ __launch_bounds__(256) void mx_matmul_join_kernel(const float *__rest
 //   MXFP4 A   256 x 192  7 + 0.52 .. 0.78   128 x 128  3 + 0.31 .. 0.41     64 x 64  3 + 0.17 .. 0.18
 //   bf16 A    128 x 256  6 + 1.23 .. 1.60   128 x 128  2.8 + 0.81 .. 1.06   64 x 64  2.5 + 0.47
 // (of 64 x 64 tiles a CU holds two workgroups: rounds after the first take 0.65 of it)
-// and the rows kernel 2 (bf16 2.2) + 2.1 per turn of its waves' runs.  So 128 x 6144 x
-// 6144 in MXFP4 takes 31 us in 256 x 192 tiles and 12 us in 64 x 64 ones, 2048 rows 44
-// us and 129 us.  Parts cost a second kernel, about 3 us, and their sums written and
-// read: 64 x 6144 x 6144 with bf16 A 25 us in one part, 18 us in two.
+// and the rows kernel 2 (bf16 2.2) + 2.1 per turn of its waves' runs, which is low for
+// MXFP4 A and wide outputs: 32 x 6144 x 6144 takes 8.3 us where it says 6.2, 128 x 4096 x
+// 4096 12.0 where it says 8.2 and takes the rows kernel before 64 x 64 tiles at 8.6.
+// So 128 x 6144 x 6144 in MXFP4 takes 31 us in 256 x 192 tiles and 12 us in 64 x 64
+// ones, 2048 rows 44 us and 129 us.  Parts cost a second kernel, about 3 us, and their
+// sums written and read: 64 x 6144 x 6144 with bf16 A 25 us in one part, 18 us in two.
 struct Plan {
     enum Kind { FEW, ROWS1, ROWS2, TILE_L, TILE_M, TILE_S } kind;
     int k_part, parts;
@@ -835,7 +847,9 @@ Plan plan(bool mx, int M, int N, int K, bool near) {
             const double join = parts > 1 ? 3.0 + (double)M * N * 8.0 * parts / 4e6 : 0.0;
             const double whole = t.a + t.full * groups;
             const double part_round = rest ? t.a + (t.few + (t.full - t.few) * (double)rest / kCUs) * groups : 0.0;
-            const double us = (wgs < kCUs ? part_round : whole + t.more * ((double)(wgs / kCUs - 1) * whole + part_round)) + join;
+            const double tile_us =
+                wgs < kCUs ? part_round : whole + t.more * ((double)(wgs / kCUs - 1) * whole + part_round);
+            const double us = tile_us + join;
             if (us < least) {
                 least = us;
                 best = Plan{t.kind, part < K ? (int)part : K, parts};
@@ -894,8 +908,8 @@ int run(const MatArgs &p, const Plan &how, float *sums, hipStream_t s) {
     MOE_LAUNCH_CHECK("mx_matmul_kernel");
     if (how.parts > 1) {
         const size_t blocks = ((size_t)p.M * p.N + 255) / 256;
-        hipLaunchKernelGGL(mx_matmul_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, sums,
-                           how.parts, p);
+        hipLaunchKernelGGL(mx_matmul_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s,
+                           sums, how.parts, p);
         MOE_LAUNCH_CHECK("mx_matmul_join_kernel");
     }
     return MOE_OK;
@@ -909,7 +923,8 @@ size_t sums_bytes(const Plan &how, int M, int N) { return how.parts > 1 ? (size_
 }  // namespace
 
 extern "C" size_t moe_mx_matmul_workspace_bytes(int M, int N, int K, int a_type) {
-    if (M <= 0 || N <= 0 || K <= 0 || K % 32 || M > kMaxRows || N > kMaxRows || K > kMaxK || (a_type != MOE_BF16 && a_type != MOE_MXFP4)) return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || K % 32 || M > kMaxRows || N > kMaxRows || K > kMaxK) return 0;
+    if (a_type != MOE_BF16 && a_type != MOE_MXFP4) return 0;
     return sums_bytes(plan(a_type == MOE_MXFP4, M, N, K, true), M, N);
 }
 

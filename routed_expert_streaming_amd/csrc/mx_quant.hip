@@ -4,11 +4,11 @@
 //
 // Bound by memory: 2 or 4 bytes read and 17/32 byte written per value, 2 more when
 // the values the codes stand for are asked for (2048 x 6144 bf16 with values: 57 MB
-// in 9.6 us, 5.9 TB/s from and to the caches).  A lane takes eight neighbouring
+// in 9.1 us, 6.2 TB/s from and to the caches).  A lane takes eight neighbouring
 // values (16 or 32 bytes), so a wave reads and writes whole lines and a block's
 // maximum is two quad permutes away, with no LDS; gfx950's scaled converts do the
-// rounding (rounding in plain arithmetic took 11.5 us; two or four units a lane
-// measured 9.6 and 9.3).
+// rounding.  With every store into the caches this took 9.6 us, rounding in plain
+// arithmetic 11.5, two or four units a lane 9.6 and 9.3.
 #include "common.h"
 #include "mx_quant.h"
 #include "dequant.h"
@@ -18,7 +18,7 @@ namespace {
 constexpr int kThreads = 256;
 
 // Whether the values are written: not, or into the caches, or past them (non-temporal
-// stores; 2048 x 6144 9.0 us against 9.6, 1533 x 2080 fp32 4.7 against 5.0), from an
+// stores; 2048 x 6144 9.1 us against 9.6, 1533 x 2080 fp32 4.6 against 5.0), from an
 // XCD's L2 on.
 enum { kNoValues, kValues, kStreamValues };
 constexpr int64_t kStreamFrom = 4 << 20;

@@ -522,9 +522,10 @@ int moe_mx_matmul(const void *a, int a_type, int64_t a_stride, const uint8_t *w,
  * x_next [T,H] bf16 or NULL; x_rows [T] contiguous MXFP4 rows of x_next's values
  * (as moe_mx_quant makes them from x_next, floor rule) or NULL; both may be NULL
  * after the last block.  Squares and their sums are fp32, in a fixed order: a row
- * whose mean square is beyond fp32 (values of 1e19 and more) normalises to zeros,
- * and with eps = 0 one whose squares are all below it (values under 1e-23) to
- * infinities, a row of zeros to NaN.  x_next and x_rows must not overlap the inputs.
+ * whose sum of squares is beyond fp32 (above 1.8e19 / sqrt(H) for equal values)
+ * normalises to zeros, and with eps = 0 one whose squares are all below it (values
+ * under 1e-23) to infinities, a row of zeros to NaN.  x_next and x_rows must not
+ * overlap the inputs.
  * MOE_E_ARG for T < 0, H <= 0, eps outside [0, 1], an unknown type or gate kind,
  * w_post without post_norm, NULL pointers, or a pointer not aligned to its type;
  * with x_rows MOE_E_SHAPE unless H % 32 == 0 and MOE_E_ARG unless every pointer is

@@ -289,3 +289,20 @@ def test_strides_of_one_row_are_not_read(kind):
         out = torch.zeros(mxkit.row_bytes(K), dtype=torch.uint8, device="cuda")
         L.moe_mx_quant(a, kind, odd, 1, K, L.MOE_MX_SCALE_FIT, out, odd, None, torch.cuda.current_stream())
         assert np.array_equal(out.cpu().numpy(), mxkit.pack(*mxkit.quantise(av.cpu().numpy(), "fit"))[0])
+
+
+@pytest.mark.parametrize("H", [64, 63])
+def test_block_norm_squares_beyond_fp32(H):
+    """What the interface says of rows whose squares leave fp32's range; the rows beside them are as ever."""
+    resid = torch.ones((5, H), device="cuda")
+    resid[1], resid[2], resid[3] = 1e19, 1e-24, 0.0  # 1e38 * H is beyond fp32, 1e-48 below it
+    s = torch.cuda.current_stream()
+    for eps in (0.0, 1e-6):
+        x = torch.empty((5, H), dtype=torch.bfloat16, device="cuda")
+        L.moe_block_norm(None, 0, None, None, L.MOE_GATE_NONE, 1.0, resid, None, L.MOE_FP32, None, 5, H, eps, x, None,
+                         s)
+        assert (x[0] == 1.0).all() and (x[4] == 1.0).all() and (x[1] == 0.0).all()
+        if eps:
+            assert ((x[2].float() - 1e-21).abs() <= 1e-21 * 2.0 ** -7).all() and (x[3] == 0.0).all()
+        else:
+            assert x[2].isinf().all() and x[3].isnan().all()

@@ -118,8 +118,10 @@ class BlockNorms:
     output, or None for no such norm; gate [L,H], a factor per channel of what a layer adds to the
     residual stream, or None; scale, one factor of it for every layer.
 
-    A layer's output enters the stream on the way to the next layer, so the step itself does not read the
-    last rows of post and gate: what follows the last layer takes them, with its own norm weight,
+    The stream is fp32 and a gate one value per channel; gates per row or element, a bf16 stream and inputs
+    as MXFP4 rows are moe_block_norm's own.  A layer's output enters the stream on the way to the next
+    layer, so the step itself does not read the last rows of post and gate: what follows the last layer
+    takes them (where there are any), with its own norm weight,
         moe_block_norm(out[L-1], 1, post[L-1], gate[L-1], MOE_GATE_CHANNEL, scale, resid, resid, MOE_FP32,
                        w_final, T, H, RMS_EPS, x_final)."""
     pre: torch.Tensor

@@ -109,6 +109,40 @@ int moe_router_topk_layers(const uint16_t *x, int n_layers, int T, int H, const 
                            const float *bias, int E, int k, int32_t *topk_idx, float *topk_w, void *workspace,
                            size_t workspace_bytes, void *stream);
 
+/* Router by scores: the logits of moe_router_topk, then (in 64 bits)
+ *   p[t,e]  = 1 / (1 + exp(-logit[t,e]))           (MOE_SCORE_SIGMOID)
+ *             softmax of logit[t,:] over all E       (MOE_SCORE_SOFTMAX)
+ *   c[t,e]  = p[t,e] + balance[e]                   (balance NULL: p; it decides the choice only)
+ *   groups: the E experts are n_groups runs of E / n_groups; a group is worth its largest c
+ *           (MOE_GROUP_MAX) or the sum of its two largest (MOE_GROUP_TOP2), and only the
+ *           top_groups worthiest (ties to the lower group) stay in the choice;
+ *   topk_idx[t,:] = the k largest c, ties to the lower expert index, in descending order;
+ *   topk_w[t,i]   = fp32( scale * p_i / (renormalise ? sum of the k chosen p : 1) )   (a sum of zero gives zeros).
+ * n_layers independent routers in one call, laid out as in moe_router_topk_layers (bias and
+ * balance [n_layers, E] fp32 or NULL).  n_groups = top_groups = 1 for no groups.  A NaN
+ * score ranks first; a balance of -infinity leaves its expert to the last.
+ * 1 <= k <= min(64, top_groups * E / n_groups), E <= 1024, n_groups <= 64 and a divisor of
+ * E, H a multiple of 32 up to 16384, n_layers <= 65535 (MOE_E_SHAPE); MOE_E_ARG for a NULL
+ * pointer, a negative T or n_layers, an unknown score or rule, a scale that is not finite,
+ * or x, w_router or workspace not 16-byte aligned.  T = 0 or n_layers = 0 is a no-op.
+ * workspace: moe_router_scored_workspace_bytes(n_layers, T, E, H) bytes (contents don't
+ * care; calls sharing it must not overlap in time).  The description is read before the
+ * call returns. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+typedef struct moe_routing {
+    int score;       /* MOE_SCORE_* */
+    int n_groups;
+    int top_groups;
+    int group_rule;  /* MOE_GROUP_* */
+    int renormalise; /* nonzero: the weights are divided by their sum */
+    float scale;     /* of every weight */
+} moe_routing;
+size_t moe_router_scored_workspace_bytes(int n_layers, int T, int E, int H);
+int moe_router_scored(const uint16_t *x, int n_layers, int T, int H, const float *w_router, const float *bias,
+                      const float *balance, int E, int k, const moe_routing *routing, int32_t *topk_idx,
+                      float *topk_w, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------------ dispatch
  * Token -> expert permutation of the T*k (token, slot) pairs p = t*k + i
  * (LayerStoRm README, "TL;DR": each token activates only the few experts the
@@ -467,7 +501,7 @@ int moe_mx_route_ffn_combine(const uint16_t *x, int T, int H, int I, const float
  * Strides are bytes between rows; a stride of one row is not read.  Every pointer
  * belongs to the current device, which is the stream's.  Calls share nothing: any
  * number may be in flight, and all can be captured into graphs. */
-enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2, MOE_MXFP4 = 3 };       /* element types */
+enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2, MOE_MXFP4 = 3, MOE_FP8 = 4 };  /* element types */
 enum { MOE_MX_SCALE_FLOOR = 0, MOE_MX_SCALE_FIT = 1 };                   /* block scale rules */
 enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_ROW = 2, MOE_GATE_ELEMENT = 3 };
 
@@ -533,6 +567,75 @@ int moe_mx_matmul(const void *a, int a_type, int64_t a_stride, const uint8_t *w,
 int moe_block_norm(const uint16_t *add, int post_norm, const float *w_post, const void *gate, int gate_kind,
                    float scale, const void *resid, void *resid_out, int resid_type, const float *w_pre, int T, int H,
                    float eps, uint16_t *x_next, uint8_t *x_rows, void *stream);
+
+/* ------------------------------------------------------------------ FP8 weights in blocks of 128
+ * Weights kept as E4M3 codes (1 sign, 4 exponent and 3 mantissa bits, largest value 448,
+ * no infinities) with one fp32 scale for each block of 128 x 128, and activations as such
+ * codes with a scale for each 1 x 128; the last blocks of a row or a column may be short.
+ * Codes and scales are separate arrays, as checkpoints hold them: codes [rows, K], one
+ * byte each; scales [rows or ceil(rows / 128), ceil(K / 128)]; value = scale * code.
+ * Strides are bytes between rows (of a matrix of one row: not read).  Every pointer belongs
+ * to the current device, which is the stream's.  Calls share nothing but what the caller
+ * lets them share; all can be captured into graphs. */
+enum { MOE_FP8_SCALE_AMAX = 0, MOE_FP8_SCALE_POW2 = 1 };
+/* Rows of bf16, fp16 or fp32 values -> codes and scales, in blocks of block_rows (1 or 128)
+ * x 128.  A block's scale s puts its largest magnitude on 448, s = fp32(|x|max / 448)
+ * (MOE_FP8_SCALE_AMAX), or is the smallest power of two >= |x|max / 448
+ * (MOE_FP8_SCALE_POW2); at least 2^-126; 1 for a block of zeros.  A code is the E4M3 value
+ * nearest to x / s (the true quotient), ties to the even code; the sign is kept for zeros
+ * too.  A block with an infinity or a NaN gets the scale NaN and codes 0.
+ * K a multiple of 16 up to 2^28 and strides that hold a row (MOE_E_SHAPE otherwise);
+ * MOE_E_ARG for rows < 0, an unknown type, rule or block_rows, a NULL pointer, x or codes
+ * (or their strides) not multiples of 16 bytes, or scales (or its stride) not of 4; rows = 0
+ * is a no-op.  x, codes and scales must not overlap.  What lies behind a row is left. */
+int moe_fp8_quant(const void *x, int x_type, int64_t x_stride, int rows, int K, int block_rows, int scale_rule,
+                  uint8_t *codes, int64_t codes_stride, float *scales, int64_t scales_stride, void *stream);
+/* y[m,n] = sum over blocks b of K of a_scales[m,b] * w_scales[n / 128, b] * (sum over k in b of A[m,k] * W[n,k])
+ *          + bias[n],  sums in fp32, rounded once.
+ * With y in fp32 the products are exact.  With y in bf16 they run on the FP8 matrix cores,
+ * which keep of each 8 products (8 neighbouring columns) the bits down to 2^-13 of the
+ * largest one: a sum is off by at most 7 * 2^-13 of its terms' magnitudes, in practice by
+ * about 2e-5, a hundredth of bf16's rounding.
+ * a [M, K]: MOE_FP8 (codes, with a_scales [M, ceil(K/128)]) or MOE_BF16 (quantised as by
+ * moe_fp8_quant, 1 x 128, MOE_FP8_SCALE_AMAX; a_scales is not read); w [N, K] codes,
+ * w_scales [ceil(N/128), ceil(K/128)]; bias [N] fp32 or NULL; y [M, N] bf16 or fp32.
+ * A NaN code (0x7F, 0xFF) or scale makes every output it enters NaN.  A row of y does not
+ * depend on the other rows of a, but its last bits may depend on M and N (which kernel
+ * runs).  M and N from 0 (a no-op) to 2^26, K a multiple of 16 up to 2^27, operands' rows
+ * at most 2^28 bytes apart, y's at least a row.
+ * workspace: moe_fp8_matmul_workspace_bytes(M, N, K, a_type) bytes (contents don't care,
+ * 16-byte aligned; calls sharing it must not overlap in time; NULL when 0).
+ * MOE_E_SHAPE for sizes or strides beyond these; MOE_E_ARG for negative sizes, unknown
+ * types, NULL pointers, a, w or a_scales (pointers or strides) that are not multiples of 16
+ * bytes, w_scales, y, bias or workspace not aligned; MOE_E_NOMEM for a small workspace.  y
+ * must not overlap the inputs. */
+size_t moe_fp8_matmul_workspace_bytes(int M, int N, int K, int a_type);
+int moe_fp8_matmul(const void *a, int a_type, int64_t a_stride, const float *a_scales, int64_t a_scales_stride,
+                   const uint8_t *w, int64_t w_stride, const float *w_scales, int64_t w_scales_stride, int M, int N,
+                   int K, const float *bias, void *y, int y_type, int64_t y_stride, void *workspace,
+                   size_t workspace_bytes, void *stream);
+/* The routed experts' feed-forward on such weights, as moe_expert_ffn and
+ * moe_expert_ffn_combine (arguments, rows of y, mask, shared expert):
+ *   g = W1 q(x_t), u = W3 q(x_t), h = silu(g) * u in fp32, y = W2 q(h), sums in fp32
+ * with q the quantisation of moe_fp8_quant (1 x 128, MOE_FP8_SCALE_AMAX); the products of
+ * g and u are exact, those of y run on the FP8 matrix cores (see moe_fp8_matmul).
+ * Slab (H, I multiples of 32): the codes of W1 [I,H], W3 [I,H] and W2 [H,I], then the fp32
+ * scales of W1 and W3 [ceil(I/128), ceil(H/128)] and of W2 [ceil(H/128), ceil(I/128)],
+ * zeros to a multiple of 16 bytes: moe_expert_bytes_fp8(H, I) bytes (0 for other sizes),
+ * 16-byte aligned.
+ * T*k <= 16384, E <= 1024, H, I <= 16384 (MOE_E_SHAPE); pairs whose expert number is
+ * outside 0 .. E-1 with T*k <= 512 are left out (their rows of y stay as they were).
+ * MOE_E_ARG for T < 0, NULL pointers, or x, shared_slab, y, out or workspace not 16-byte
+ * aligned; MOE_E_NOMEM for a workspace below moe_fp8_expert_ffn_workspace_bytes; T = 0 is
+ * a no-op.  The combine call needs every routed expert's slab and has no mask. */
+size_t moe_expert_bytes_fp8(int hidden, int inter);
+size_t moe_fp8_expert_ffn_workspace_bytes(int T, int H, int I, int E, int k, int has_shared);
+int moe_fp8_expert_ffn(const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_idx, int k,
+                       const void *const *expert_table, const void *shared_slab, const uint8_t *expert_mask, float *y,
+                       void *workspace, size_t workspace_bytes, void *stream);
+int moe_fp8_expert_ffn_combine(const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_idx,
+                               const float *topk_w, int k, const void *const *expert_table, const void *shared_slab,
+                               uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------ super-block weights
  * A k-quant-style format (the pages' own weights are a 4-bit k-quant GGUF

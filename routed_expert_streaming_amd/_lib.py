@@ -17,7 +17,10 @@ LIB_PATH = os.environ.get("MOE_LIB_PATH") or os.path.join(_HERE, "libmoe.so")
 
 MOE_OK, MOE_E_ARG, MOE_E_SHAPE, MOE_E_NOT_PINNED, MOE_E_NOMEM, MOE_E_CAPACITY, MOE_E_HIP, MOE_E_STATE = \
     0, -1, -2, -3, -4, -5, -6, -7
-MOE_BF16, MOE_FP16, MOE_FP32, MOE_MXFP4 = 0, 1, 2, 3
+MOE_BF16, MOE_FP16, MOE_FP32, MOE_MXFP4, MOE_FP8 = 0, 1, 2, 3, 4
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+MOE_FP8_SCALE_AMAX, MOE_FP8_SCALE_POW2 = 0, 1
 MOE_MX_SCALE_FLOOR, MOE_MX_SCALE_FIT = 0, 1
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_ROW, MOE_GATE_ELEMENT = 0, 1, 2, 3
 MOE_FFN_AUTO, MOE_FFN_PAIRS, MOE_FFN_GROUPED, MOE_FFN_MFMA, MOE_FFN_SPLIT = 0, 1, 2, 3, 4
@@ -34,6 +37,11 @@ class MoEError(RuntimeError):
 class moe_cache_desc(ctypes.Structure):
     _fields_ = [("n_layers", ctypes.c_int), ("n_experts", ctypes.c_int), ("hidden", ctypes.c_int),
                 ("inter", ctypes.c_int), ("slots_per_layer", ctypes.c_int), ("format", ctypes.c_int)]
+
+
+class moe_routing(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("n_groups", ctypes.c_int), ("top_groups", ctypes.c_int),
+                ("group_rule", ctypes.c_int), ("renormalise", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 def lib():
@@ -107,6 +115,15 @@ def lib():
             "moe_mx_matmul_workspace_bytes": ([i, i, i, i], sz),
             "moe_mx_matmul": ([vp, i, i64, vp, i64, i, i, i, vp, vp, i, i64, vp, sz, vp], i),
             "moe_block_norm": ([vp, i, vp, vp, i, ctypes.c_float, vp, vp, i, vp, i, i, ctypes.c_float, vp, vp, vp], i),
+            "moe_router_scored_workspace_bytes": ([i, i, i, i], sz),
+            "moe_router_scored": ([vp, i, i, i, vp, vp, vp, i, i, ctypes.POINTER(moe_routing), vp, vp, vp, sz, vp], i),
+            "moe_fp8_quant": ([vp, i, i64, i, i, i, i, vp, i64, vp, i64, vp], i),
+            "moe_fp8_matmul_workspace_bytes": ([i, i, i, i], sz),
+            "moe_fp8_matmul": ([vp, i, i64, vp, i64, vp, i64, vp, i64, i, i, i, vp, vp, i, i64, vp, sz, vp], i),
+            "moe_expert_bytes_fp8": ([i, i], sz),
+            "moe_fp8_expert_ffn_workspace_bytes": ([i, i, i, i, i, i], sz),
+            "moe_fp8_expert_ffn": ([vp, i, i, i, i, vp, i, vp, vp, vp, vp, vp, sz, vp], i),
+            "moe_fp8_expert_ffn_combine": ([vp, i, i, i, i, vp, vp, i, vp, vp, vp, vp, sz, vp], i),
             "moe_cpu_lane_create": ([i, ctypes.POINTER(vp)], i),
             "moe_cpu_lane_submit": ([vp, vp, i, i, i, vp, vp, u64p], i),
             "moe_cpu_lane_wait": ([vp, ctypes.c_uint64], i),
@@ -203,6 +220,17 @@ def moe_router_topk_layers(x, n_layers, T, H, w_router, bias, E, k, topk_idx, to
     _check(lib().moe_router_topk_layers(_ptr(x), n_layers, T, H, _ptr(w_router), _ptr(bias), E, k, _ptr(topk_idx),
                                         _ptr(topk_w), _ptr(workspace), workspace_bytes, _stream(stream)),
            "moe_router_topk_layers")
+
+
+def moe_router_scored_workspace_bytes(n_layers: int, T: int, E: int, H: int) -> int:
+    return lib().moe_router_scored_workspace_bytes(n_layers, T, E, H)
+
+
+def moe_router_scored(x, n_layers, T, H, w_router, bias, balance, E, k, routing: moe_routing | None, topk_idx, topk_w,
+                      workspace, workspace_bytes, stream=None):
+    _check(lib().moe_router_scored(_ptr(x), n_layers, T, H, _ptr(w_router), _ptr(bias), _ptr(balance), E, k,
+                                   None if routing is None else ctypes.byref(routing), _ptr(topk_idx), _ptr(topk_w),
+                                   _ptr(workspace), workspace_bytes, _stream(stream)), "moe_router_scored")
 
 
 def moe_permute(topk_idx, T, k, E, count, offset, pair_of_row, stream=None):
@@ -527,6 +555,46 @@ def moe_block_norm(add, post_norm, w_post, gate, gate_kind, scale, resid, resid_
     _check(lib().moe_block_norm(_ptr(add), int(bool(post_norm)), _ptr(w_post), _ptr(gate), gate_kind, scale,
                                 _ptr(resid), _ptr(resid_out), resid_type, _ptr(w_pre), T, H, eps, _ptr(x_next),
                                 _ptr(x_rows), _stream(stream)), "moe_block_norm")
+
+
+# ----------------------------------------------------------------------- FP8 weights in blocks of 128
+def moe_fp8_quant(x, x_type, x_stride, rows, K, block_rows, scale_rule, codes, codes_stride, scales, scales_stride,
+                  stream=None):
+    _check(lib().moe_fp8_quant(_ptr(x), x_type, x_stride, rows, K, block_rows, scale_rule, _ptr(codes), codes_stride,
+                               _ptr(scales), scales_stride, _stream(stream)), "moe_fp8_quant")
+
+
+def moe_fp8_matmul_workspace_bytes(M: int, N: int, K: int, a_type: int) -> int:
+    return lib().moe_fp8_matmul_workspace_bytes(M, N, K, a_type)
+
+
+def moe_fp8_matmul(a, a_type, a_stride, a_scales, a_scales_stride, w, w_stride, w_scales, w_scales_stride, M, N, K,
+                   bias, y, y_type, y_stride, workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().moe_fp8_matmul(_ptr(a), a_type, a_stride, _ptr(a_scales), a_scales_stride, _ptr(w), w_stride,
+                                _ptr(w_scales), w_scales_stride, M, N, K, _ptr(bias), _ptr(y), y_type, y_stride,
+                                _ptr(workspace), workspace_bytes, _stream(stream)), "moe_fp8_matmul")
+
+
+def moe_expert_bytes_fp8(H: int, I: int) -> int:
+    return lib().moe_expert_bytes_fp8(H, I)
+
+
+def moe_fp8_expert_ffn_workspace_bytes(T, H, I, E, k, has_shared) -> int:
+    return lib().moe_fp8_expert_ffn_workspace_bytes(T, H, I, E, k, int(bool(has_shared)))
+
+
+def moe_fp8_expert_ffn(x, T, H, I, E, topk_idx, k, expert_table, shared_slab, expert_mask, y, workspace,
+                       workspace_bytes, stream=None):
+    _check(lib().moe_fp8_expert_ffn(_ptr(x), T, H, I, E, _ptr(topk_idx), k, _ptr(expert_table), _ptr(shared_slab),
+                                    _ptr(expert_mask), _ptr(y), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "moe_fp8_expert_ffn")
+
+
+def moe_fp8_expert_ffn_combine(x, T, H, I, E, topk_idx, topk_w, k, expert_table, shared_slab, out, workspace,
+                               workspace_bytes, stream=None):
+    _check(lib().moe_fp8_expert_ffn_combine(_ptr(x), T, H, I, E, _ptr(topk_idx), _ptr(topk_w), k, _ptr(expert_table),
+                                            _ptr(shared_slab), _ptr(out), _ptr(workspace), workspace_bytes,
+                                            _stream(stream)), "moe_fp8_expert_ffn_combine")
 
 
 # ----------------------------------------------------------------------- super-block weights

@@ -1,0 +1,202 @@
+// y[m,n] = sum over blocks b of 128 columns of a_scale[m,b] w_scale[n/128,b] sum_k A[m,k] W[n,k],
+// plus bias[n]: E4M3 rows of activations (or bf16 ones, quantised first) times E4M3
+// weights in blocks of 128 x 128.  Sums over k are fp32.
+#include "common.h"
+#include "fp8_mma.h"
+#include "fp8_quant.h"
+#include "fp8_rows.h"
+
+namespace {
+
+using moe::f32x4;
+
+constexpr int kMaxRows = 1 << 26;        // M and N
+constexpr int kMaxK = 1 << 27;
+constexpr int64_t kMaxStride = 1 << 28;
+
+struct MatArgs {
+    moe::Fp8Act a;
+    const uint8_t *w;
+    size_t w_stride;
+    const uint8_t *ws;
+    size_t ws_stride;  // bytes between rows of blocks' scales
+    int M, N, K;
+    const float *bias;
+    uint8_t *y;
+    size_t y_stride;
+    bool y_f32;
+};
+
+// Four outputs n .. n+3 of row m (those below N), bias added, rounded once.
+__device__ __forceinline__ void store4(const MatArgs &p, int m, int n, const f32x4 v) {
+    if (m >= p.M) return;
+    uint8_t *row = p.y + (size_t)m * p.y_stride;
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = v[j] + (p.bias && n + j < p.N ? p.bias[n + j] : 0.0f);
+    if (p.y_f32) {
+        float *o = (float *)row + n;
+        if (n + 3 < p.N && (uintptr_t)o % 16 == 0) {
+            *reinterpret_cast<float4 *>(o) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < p.N) o[j] = f[j];
+        }
+    } else {
+        uint16_t *o = (uint16_t *)row + n;
+        if (n + 3 < p.N && (uintptr_t)o % 8 == 0) {
+            *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < p.N) o[j] = (uint16_t)pack_bf16(f[j], 0.0f);
+        }
+    }
+}
+
+template <bool WIDE, int MT, int NT, int WK, int U>
+__global__ __launch_bounds__(64 * WK) void fp8_matmul_rows_kernel(MatArgs p) {
+    __shared__ f32x4 part[WK][NT * MT][64];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int m0 = blockIdx.y * 16 * MT, n0 = blockIdx.x * 16 * NT;
+    const uint8_t *w[NT], *a[MT];
+    const float *ws[NT], *as[MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int n = min(n0 + 16 * t, p.N - 1);
+        w[t] = p.w + (size_t)min(n + r, p.N - 1) * p.w_stride;
+        ws[t] = reinterpret_cast<const float *>(p.ws + (size_t)(n / 128) * p.ws_stride);
+    }
+#pragma unroll
+    for (int u = 0; u < MT; ++u) {
+        const int m = min(m0 + 16 * u + r, p.M - 1);
+        a[u] = p.a.codes + (size_t)m * p.a.stride;
+        as[u] = reinterpret_cast<const float *>(p.a.scales + (size_t)m * p.a.scale_stride);
+    }
+    f32x4 acc[NT][MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < MT; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    moe::multiply_rows<WIDE, MT, NT, U, WK>(wave, p.K, q, w, ws, a, as, acc);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < MT; ++u) part[wave][t * MT + u][lane] = acc[t][u];
+    __syncthreads();
+#pragma unroll
+    for (int i0 = 0; i0 < NT * MT; i0 += WK) {
+        const int i = i0 + wave;
+        if (i >= NT * MT) break;
+        store4(p, m0 + 16 * (i % MT) + r, n0 + 16 * (i / MT) + 4 * q,
+               moe::joined<WK, NT * MT>(part, i, lane));
+    }
+}
+
+template <bool WIDE, int MT, int NT, int WK, int U>
+void launch_rows(MatArgs p, hipStream_t s) {
+    const int most = 32768 * 16 * MT, all = p.M;  // rows of A a grid holds
+    for (int m = 0;; m += most) {
+        p.M = min(all - m, most);
+        const dim3 grid((p.N + 16 * NT - 1) / (16 * NT), (p.M + 16 * MT - 1) / (16 * MT));
+        hipLaunchKernelGGL((fp8_matmul_rows_kernel<WIDE, MT, NT, WK, U>), grid, dim3(64 * WK), 0, s, p);
+        if (all - m <= most) return;
+        p.a.codes += (size_t)most * p.a.stride;
+        p.a.scales += (size_t)most * p.a.scale_stride;
+        p.y += (size_t)most * p.y_stride;
+    }
+}
+
+// WIDE: products of codes converted to bf16, for fp32 outputs.
+template <bool WIDE>
+int run(const MatArgs &p, hipStream_t s) {
+    if (p.M <= 16)
+        launch_rows<WIDE, 1, 1, 8, 2>(p, s);
+    else
+        launch_rows<WIDE, 2, 2, 8, 2>(p, s);
+    MOE_LAUNCH_CHECK("fp8_matmul_rows_kernel");
+    return MOE_OK;
+}
+
+// Quantised activations in the workspace: codes, then scales.
+struct Space {
+    size_t codes, scales, total;
+};
+Space layout(int M, int K, bool quantise) {
+    Space w{};
+    if (!quantise) return w;
+    w.scales = moe::align_up((size_t)M * K, 256);
+    w.total = w.scales + moe::align_up((size_t)M * moe::fp8_scale_row(K), 256);
+    return w;
+}
+
+}  // namespace
+
+extern "C" size_t moe_fp8_matmul_workspace_bytes(int M, int N, int K, int a_type) {
+    if (M <= 0 || N <= 0 || K <= 0 || K % 16 || M > kMaxRows || N > kMaxRows || K > kMaxK) return 0;
+    if (a_type != MOE_BF16 && a_type != MOE_FP8) return 0;
+    return layout(M, K, a_type == MOE_BF16).total;
+}
+
+extern "C" int moe_fp8_matmul(const void *a, int a_type, int64_t a_stride, const float *a_scales,
+                              int64_t a_scales_stride, const uint8_t *w, int64_t w_stride, const float *w_scales,
+                              int64_t w_scales_stride, int M, int N, int K, const float *bias, void *y, int y_type,
+                              int64_t y_stride, void *workspace, size_t workspace_bytes, void *stream) {
+    if (M < 0 || N < 0) return moe::fail(MOE_E_ARG, "fp8_matmul: M=%d, N=%d", M, N);
+    if (a_type != MOE_BF16 && a_type != MOE_FP8) return moe::fail(MOE_E_ARG, "fp8_matmul: a_type=%d", a_type);
+    if (y_type != MOE_BF16 && y_type != MOE_FP32) return moe::fail(MOE_E_ARG, "fp8_matmul: y_type=%d", y_type);
+    if (K <= 0 || K % 16) return moe::fail(MOE_E_SHAPE, "fp8_matmul: K=%d must be a positive multiple of 16", K);
+    if (M > kMaxRows || N > kMaxRows || K > kMaxK)
+        return moe::fail(MOE_E_SHAPE, "fp8_matmul: M=%d, N=%d above %d or K=%d above %d", M, N, kMaxRows, K, kMaxK);
+    if (M == 0 || N == 0) return MOE_OK;
+    const bool quantise = a_type == MOE_BF16;
+    if (!a || !w || !w_scales || !y || (!quantise && !a_scales))
+        return moe::fail(MOE_E_ARG, "fp8_matmul: NULL pointer");
+    const int64_t size = y_type == MOE_FP32 ? 4 : 2, a_row = quantise ? 2 * (int64_t)K : K;
+    const int64_t srow = 4 * (int64_t)moe::fp8_blocks(K);
+    if ((M > 1 && (a_stride < a_row || y_stride < size * N || (!quantise && a_scales_stride < srow))) ||
+        (N > 1 && w_stride < K) || (N > 128 && w_scales_stride < srow))
+        return moe::fail(MOE_E_SHAPE, "fp8_matmul: a row stride (%lld, %lld, %lld, %lld, %lld) is below the row's bytes",
+                         (long long)a_stride, (long long)a_scales_stride, (long long)w_stride,
+                         (long long)w_scales_stride, (long long)y_stride);
+    if (((uintptr_t)a | (uintptr_t)w) % 16 || (M > 1 && a_stride % 16) || (N > 1 && w_stride % 16))
+        return moe::fail(MOE_E_ARG, "fp8_matmul: operands' pointers and strides must be multiples of 16 bytes");
+    if (!quantise && ((uintptr_t)a_scales % 16 || (M > 1 && a_scales_stride % 16)))
+        return moe::fail(MOE_E_ARG, "fp8_matmul: a_scales and its stride must be multiples of 16 bytes");
+    if ((uintptr_t)w_scales % 4 || (N > 128 && w_scales_stride % 4))
+        return moe::fail(MOE_E_ARG, "fp8_matmul: w_scales or its stride is not a multiple of 4 bytes");
+    if ((uintptr_t)y % size || (M > 1 && y_stride % size) || (uintptr_t)bias % 4)
+        return moe::fail(MOE_E_ARG, "fp8_matmul: y, its stride or bias is not aligned to its type");
+    if ((M > 1 && (a_stride > kMaxStride || (!quantise && a_scales_stride > kMaxStride))) ||
+        (N > 1 && w_stride > kMaxStride))
+        return moe::fail(MOE_E_SHAPE, "fp8_matmul: operands' rows more than %lld bytes apart", (long long)kMaxStride);
+    const Space sp = layout(M, K, quantise);
+    if (workspace_bytes < sp.total || (sp.total && !workspace))
+        return moe::fail(MOE_E_NOMEM, "fp8_matmul: workspace %zu < %zu bytes", workspace_bytes, sp.total);
+    if (sp.total && (uintptr_t)workspace % 16)
+        return moe::fail(MOE_E_ARG, "fp8_matmul: workspace is not 16-byte aligned");
+    hipStream_t s = (hipStream_t)stream;
+    MatArgs p{};
+    p.a = {(const uint8_t *)a, (const uint8_t *)a_scales, M > 1 ? (size_t)a_stride : 0,
+           M > 1 ? (size_t)a_scales_stride : 0};
+    p.w = w;
+    p.w_stride = N > 1 ? (size_t)w_stride : 0;
+    p.ws = (const uint8_t *)w_scales;
+    p.ws_stride = N > 128 ? (size_t)w_scales_stride : 0;
+    p.M = M, p.N = N, p.K = K;
+    p.bias = bias;
+    p.y = (uint8_t *)y;
+    p.y_stride = M > 1 ? (size_t)y_stride : 0;
+    p.y_f32 = y_type == MOE_FP32;
+    if (quantise) {
+        uint8_t *codes = (uint8_t *)workspace + sp.codes;
+        float *scales = (float *)((uint8_t *)workspace + sp.scales);
+        const int rc = moe::fp8_quant_rows(a, MOE_BF16, p.a.stride, M, K, false, codes, (size_t)K, scales,
+                                           moe::fp8_scale_row(K), s);
+        if (rc != MOE_OK) return rc;
+        p.a = {codes, (const uint8_t *)scales, (size_t)K, moe::fp8_scale_row(K)};
+    }
+    return p.y_f32 ? run<true>(p, s) : run<false>(p, s);
+}

@@ -235,6 +235,14 @@ int router_partials(const uint16_t *x, int T, int H, const float *w_router, int 
     return MOE_OK;
 }
 
+int router_logits_rows(const uint16_t *x, int T, int H, const float *w_router, const float *bias, int E, float *logits,
+                       hipStream_t s) {
+    const dim3 grid((T + kRT - 1) / kRT, (E + kRE - 1) / kRE), block(256);
+    hipLaunchKernelGGL(router_mfma_kernel, grid, block, 0, s, x, T, H, w_router, bias, E, logits);
+    MOE_LAUNCH_CHECK("router_mfma_kernel");
+    return MOE_OK;
+}
+
 }  // namespace moe
 
 extern "C" size_t moe_router_workspace_bytes(int T, int E) {
@@ -292,10 +300,9 @@ int router_run(const uint16_t *x, int layers, int T, int H, const float *w_route
     for (int l = 0; l < layers; ++l) {
         const size_t xo = (size_t)l * T * H, wo = (size_t)l * E * H, io = (size_t)l * T * k;
         float *logits = moe::router_logits((char *)workspace + (size_t)l * per);
-        dim3 grid((T + kRT - 1) / kRT, (E + kRE - 1) / kRE);
-        hipLaunchKernelGGL(router_mfma_kernel, grid, block, 0, s, x + xo, T, H, w_router + wo,
-                           bias ? bias + (size_t)l * E : nullptr, E, logits);
-        MOE_LAUNCH_CHECK("router_mfma_kernel");
+        const int rc = moe::router_logits_rows(x + xo, T, H, w_router + wo, bias ? bias + (size_t)l * E : nullptr, E,
+                                               logits, s);
+        if (rc != MOE_OK) return rc;
         hipLaunchKernelGGL(router_topk_kernel, dim3((T + 3) / 4), block, 0, s, logits, T, E, k, topk_idx + io,
                            topk_w + io);
         MOE_LAUNCH_CHECK("router_topk_kernel");

@@ -11,6 +11,7 @@
 #include "fp8_mma.h"
 #include "fp8_quant.h"
 #include "fp8_rows.h"
+#include "fp8_tile.h"
 
 namespace {
 
@@ -21,32 +22,31 @@ constexpr int kMaxPairs = 16384;   // of a permutation
 constexpr int kScanPairs = 512;    // up to here a workgroup finds its expert's pairs itself
 
 struct ExpertArgs {
-    moe::Fp8Act a;  // gate/up: x, a row a token; down: h, a row a pair, then a row a token of the shared expert
+    moe::Fp8Act a;  // gate/up: x, a row a token; down: h
     int T, H, I, E, k;
     const int32_t *topk_idx;
     const void *const *table;
     const uint8_t *shared, *mask;
-    const int32_t *count, *offset, *pair_of_row;  // or NULL: workgroups find their pairs
-    float *out;  // gate/up: h [rows, I]; down: y [rows, H]
+    uint8_t *out;        // rows kernels: fp32 h [rows, I] or y [rows, H]; tile kernels: codes of h, or y
+    uint8_t *out_scales;  // tile kernel, gate/up: h's
+    const int32_t *offset, *pair_of_row, *tiles;  // tile kernels
 };
 
-// The rows of one group: pair numbers, or T * k + t for the shared expert's.
+// ---------------------------------------------------------------- few tokens
+// Group blockIdx.y: pair blockIdx.y stands for its expert where it is the expert's first
+// pair, and all waves together find the expert's other pairs (no launch for a
+// permutation); the shared expert, all tokens in order, comes last.  Rows of h and y: pair
+// numbers, then T * k + t.  list: kScanPairs numbers.
 struct Group {
     const uint8_t *slab;
     const int32_t *pairs;  // NULL: all tokens, in order
     int rows;
 };
-
-// Group blockIdx.y.  With a permutation: expert blockIdx.y, the shared expert last.
-// Without: pair blockIdx.y stands for its expert where it is the expert's first pair, and
-// the expert's other pairs are found by all waves together; list: kScanPairs numbers.
 __device__ __forceinline__ Group find_group(const ExpertArgs &p, int32_t *list) {
     const int P = p.T * p.k, g = blockIdx.y, lane = threadIdx.x & 63;
-    const int groups = p.count ? p.E : P;
-    if (g >= groups) return {p.shared, nullptr, p.T};
-    const int e = p.count ? g : p.topk_idx[g];
+    if (g >= P) return {p.shared, nullptr, p.T};
+    const int e = p.topk_idx[g];
     if ((unsigned)e >= (unsigned)p.E || (p.mask && !p.mask[e])) return {nullptr, nullptr, 0};
-    if (p.count) return {(const uint8_t *)p.table[e], p.pair_of_row + p.offset[e], p.count[e]};
     int n = 0;
     for (int b = 0; b < P; b += 64) {
         const bool mine = b + lane < P && p.topk_idx[b + lane] == e;
@@ -116,14 +116,154 @@ __global__ __launch_bounds__(64 * WK) void fp8_experts_rows_kernel(ExpertArgs p)
                 for (int j = 0; j < 4; ++j) v[j] = moe::silu(v[j]) * up[j];
             }
             if (m < g.rows && n < N)  // N % 32 == 0: all four columns exist
-                *reinterpret_cast<float4 *>(p.out + (size_t)row_of(m) * N + n) = make_float4(v[0], v[1], v[2], v[3]);
+                reinterpret_cast<float4 *>(p.out)[((size_t)row_of(m) * N + n) / 4] = make_float4(v[0], v[1], v[2], v[3]);
         }
     }
 }
 
-struct Space {
-    size_t xq, xs, h, hq, hs, count, offset, pairs, y, total;
+// ---------------------------------------------------------------- many tokens
+// The (token, expert) pairs in expert order (a permutation); a workgroup owns 64 rows of
+// one expert and 128 columns of h or 256 of y.  Rows of h: the pairs' places in that
+// order, then T * k + t; so the down projection reads neighbouring rows.
+using Tile = moe::Fp8Tile<2, 4, 2, 4, 3, 3>;
+constexpr int kGroupBits = 11;  // of a tile's number: its expert (E: the shared one); above: its first row / BM
+
+// tiles[0]: how many tiles of BM rows, tiles[1 ..]: each one's expert and rows, expert by
+// expert.  One workgroup of 1024.
+__global__ __launch_bounds__(1024) void fp8_experts_tiles_kernel(const int32_t *__restrict__ count,
+                                                                 const uint8_t *__restrict__ mask, int E, int T,
+                                                                 bool shared, int BM, int32_t *__restrict__ tiles) {
+    __shared__ int sums[16];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int n = tid < E && (!mask || mask[tid]) ? (count[tid] + BM - 1) / BM : 0;
+    int at = n;  // inclusive sum
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(at, o, 64);
+        if (lane >= o) at += u;
+    }
+    if (lane == 63) sums[wave] = at;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        if (w < wave) before += sums[w];
+        all += sums[w];
+    }
+    for (int i = 0; i < n; ++i) tiles[1 + before + at - n + i] = tid | i << kGroupBits;
+    const int more = shared ? (T + BM - 1) / BM : 0;
+    for (int i = tid; i < more; i += 1024) tiles[1 + all + i] = E | i << kGroupBits;
+    if (tid == 0) tiles[0] = all + more;
+}
+
+// Rows of y, for store_tile.
+struct YRows {
+    int M, N;
+    uint8_t *y;
+    size_t y_stride;
+    const int32_t *pairs;
+    __device__ __forceinline__ uint8_t *row(int m) const { return y + (size_t)(pairs ? pairs[m] : m) * y_stride; }
 };
+
+template <bool GATEUP>
+__global__ __launch_bounds__(64 * Tile::WAVES) void fp8_experts_tile_kernel(ExpertArgs p) {
+    using T = Tile;
+    constexpr int BN = GATEUP ? T::BN / 2 : T::BN, MT = T::MT, NT = T::NT;  // columns of h or y
+    __shared__ uint4 smem4[T::LDS / 16];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(smem4);
+    const int H = p.H, I = p.I, P = p.T * p.k, K = GATEUP ? H : I, N = GATEUP ? I : H;
+    // each XCD takes a run of neighbouring tiles, an expert's columns fastest: the workgroups
+    // that run together share its rows of A, and of W with the expert's next rows
+    const int n_tiles = (N + BN - 1) / BN, tiles = p.tiles[0] * n_tiles, per = (tiles + 7) / 8;
+    const int i = blockIdx.x >> 3, tile = (blockIdx.x & 7) * per + i;
+    if (i >= per || tile >= tiles) return;
+    const int number = p.tiles[1 + tile / n_tiles], e = number & ((1 << kGroupBits) - 1);
+    const int m0 = (number >> kGroupBits) * T::BM, n0 = tile % n_tiles * BN;
+    const bool shared = e == p.E;
+    const int first = shared ? P : p.offset[e], rows = (shared ? p.T : p.offset[e + 1] - first) - m0;  // from m0 on
+    const int32_t *pairs = shared ? nullptr : p.pair_of_row + first + m0;
+    const uint8_t *slab = shared ? p.shared : (const uint8_t *)p.table[e];
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / T::WN, wn = wave % T::WN;
+
+    f32x4 acc[NT][MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < MT; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto row_of = [&](int row) { return min(row, rows - 1); };
+    if constexpr (GATEUP) {
+        // a wave's first NT / 2 tiles are rows of W1, the others the same rows of W3
+        const moe::Fp8Slab w1 = moe::fp8_slab(slab, H, I, 0), w3 = moe::fp8_slab(slab, H, I, 1);
+        const float *const ws[2] = {w1.s + (size_t)(n0 / 128) * w1.s_row, w3.s + (size_t)(n0 / 128) * w3.s_row};
+        auto token = [&](int row) { return (uint32_t)(pairs ? pairs[row_of(row)] / p.k : m0 + row_of(row)); };
+        moe::fp8_tile<T, true, 2>(
+            smem, w1.w, p.a.codes, p.a.scales, ws, K,
+            [&](int row) {
+                const int w = row / (16 * NT), t = row / 16 % NT, c = n0 + (w * (NT / 2) + t % (NT / 2)) * 16 + row % 16;
+                return (uint32_t)((t >= NT / 2 ? I : 0) + min(c, I - 1)) * (uint32_t)H;
+            },
+            [&](int row) { return token(row) * (uint32_t)p.a.stride; },
+            [&](int row) { return token(row) * (uint32_t)p.a.scale_stride; }, acc);
+        // h, its largest magnitude per row over the block's columns, its codes
+        uint32_t(*tops)[T::WN] = reinterpret_cast<uint32_t(*)[T::WN]>(smem);
+        uint8_t *codes = smem + T::BM * T::WN * 4;
+        constexpr int PITCH = BN + 16;
+        static_assert(NT == 4 && BN == 128, "eight of a block's columns a lane");
+        float h[MT][8];
+#pragma unroll
+        for (int u = 0; u < MT; ++u) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = n0 + (wn * 2 + j / 4) * 16 + 4 * q + j % 4;
+                h[u][j] = c < I ? moe::silu(acc[j / 4][u][j % 4]) * acc[2 + j / 4][u][j % 4] : 0.0f;
+            }
+            uint32_t top = moe::top8(h[u]);
+            top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+            top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+            if (q == 0) tops[(wm * MT + u) * 16 + r][wn] = top;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < MT; ++u) {
+            const int m = (wm * MT + u) * 16 + r;
+            uint32_t top = 0;
+#pragma unroll
+            for (int w = 0; w < T::WN; ++w) top = max(top, tops[m][w]);
+            const float s = moe::fp8_scale(top, false);
+            const uint2 c = moe::fp8_codes8<false>(h[u], s);
+            uint8_t *o = codes + m * PITCH + wn * 32 + 4 * q;
+            *reinterpret_cast<uint32_t *>(o) = c.x;
+            *reinterpret_cast<uint32_t *>(o + 16) = c.y;
+            if (wn == 0 && q == 0 && m < rows)
+                *reinterpret_cast<float *>(p.out_scales + (size_t)(first + m0 + m) * moe::fp8_scale_row(I) +
+                                           4 * (size_t)(n0 / 128)) = s;
+        }
+        __syncthreads();
+        for (int v = threadIdx.x; v < T::BM * (BN / 16); v += 64 * T::WAVES) {
+            const int m = v / (BN / 16), c = v % (BN / 16) * 16;
+            if (m < rows && n0 + c < I)
+                *reinterpret_cast<uint4 *>(p.out + (size_t)(first + m0 + m) * I + n0 + c) =
+                    *reinterpret_cast<const uint4 *>(codes + m * PITCH + c);
+        }
+    } else {
+        const moe::Fp8Slab w2 = moe::fp8_slab(slab, H, I, 2);
+        const float *const ws[1] = {w2.s + (size_t)(min(n0 + wn * NT * 16, H - 1) / 128) * w2.s_row};
+        moe::fp8_tile<T, false, 1>(
+            smem, w2.w + (size_t)n0 * I, p.a.codes + (size_t)(first + m0) * p.a.stride,
+            p.a.scales + (size_t)(first + m0) * p.a.scale_stride, ws, K,
+            [&](int row) { return (uint32_t)min(row, H - 1 - n0) * (uint32_t)I; },
+            [&](int row) { return (uint32_t)row_of(row) * (uint32_t)p.a.stride; },
+            [&](int row) { return (uint32_t)row_of(row) * (uint32_t)p.a.scale_stride; }, acc);
+        const YRows y{min(rows, T::BM), H, p.out + (shared ? (size_t)(P + m0) * H * 4 : 0), (size_t)H * 4, pairs};
+        moe::store_tile<T, MT, NT, float, true>(y, smem, 0, n0, wm, wn, lane, acc);
+    }
+}
+
+struct Space {
+    size_t xq, xs, h, hq, hs, count, offset, pairs, tiles, y, total;
+};
+bool few(int T, int k) { return T * k <= kScanPairs; }
 Space layout(int T, int H, int I, int E, int k, bool shared) {
     Space w{};
     const size_t rows = (size_t)T * k + (shared ? (size_t)T : 0);
@@ -135,12 +275,16 @@ Space layout(int T, int H, int I, int E, int k, bool shared) {
     };
     w.xq = take((size_t)T * H);
     w.xs = take((size_t)T * moe::fp8_scale_row(H));
-    w.h = take(rows * I * 4);
     w.hq = take(rows * I);
     w.hs = take(rows * moe::fp8_scale_row(I));
-    w.count = take((size_t)E * 4);
-    w.offset = take((size_t)(E + 1) * 4);
-    w.pairs = take((size_t)T * k * 4);
+    if (few(T, k)) {
+        w.h = take(rows * I * 4);
+    } else {
+        w.count = take((size_t)E * 4);
+        w.offset = take((size_t)(E + 1) * 4);
+        w.pairs = take((size_t)T * k * 4);
+        w.tiles = take(4 * (1 + rows / Tile::BM + (size_t)E + 1));
+    }
     w.y = take(rows * H * 4);
     w.total = o;
     return w;
@@ -157,30 +301,48 @@ int experts(const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_i
     a.table = expert_table;
     a.shared = (const uint8_t *)shared_slab;
     a.mask = expert_mask;
-    const bool scan = T * k <= kScanPairs;
-    if (!scan) {
-        int32_t *count = (int32_t *)(ws + sp.count), *offset = (int32_t *)(ws + sp.offset);
-        int32_t *pairs = (int32_t *)(ws + sp.pairs);
-        const int rc = moe::permute_launch(topk_idx, T, k, E, count, offset, pairs, s);
-        if (rc != MOE_OK) return rc;
-        a.count = count, a.offset = offset, a.pair_of_row = pairs;
-    }
-    const int groups = (scan ? T * k : E) + (shared ? 1 : 0);
-    float *h = (float *)(ws + sp.h);
     int rc = moe::fp8_quant_rows(x, MOE_BF16, (size_t)2 * H, T, H, false, ws + sp.xq, (size_t)H,
                                  (float *)(ws + sp.xs), moe::fp8_scale_row(H), s);
     if (rc != MOE_OK) return rc;
-    a.a = {ws + sp.xq, ws + sp.xs, (size_t)H, moe::fp8_scale_row(H)};
-    a.out = h;
-    hipLaunchKernelGGL((fp8_experts_rows_kernel<true, 1, 2, 8, 2>), dim3(I / 16, groups), dim3(512), 0, s, a);
-    MOE_LAUNCH_CHECK("fp8_experts_rows_kernel<gate/up>");
-    rc = moe::fp8_quant_rows(h, MOE_FP32, (size_t)4 * I, rows, I, false, ws + sp.hq, (size_t)I,
-                             (float *)(ws + sp.hs), moe::fp8_scale_row(I), s);
+    const moe::Fp8Act xa{ws + sp.xq, ws + sp.xs, (size_t)H, moe::fp8_scale_row(H)};
+    const moe::Fp8Act ha{ws + sp.hq, ws + sp.hs, (size_t)I, moe::fp8_scale_row(I)};
+    a.a = xa;
+    if (few(T, k)) {
+        const int groups = T * k + (shared ? 1 : 0);
+        a.out = ws + sp.h;
+        hipLaunchKernelGGL((fp8_experts_rows_kernel<true, 1, 2, 8, 2>), dim3(I / 16, groups), dim3(512), 0, s, a);
+        MOE_LAUNCH_CHECK("fp8_experts_rows_kernel<gate/up>");
+        rc = moe::fp8_quant_rows(ws + sp.h, MOE_FP32, (size_t)4 * I, rows, I, false, ws + sp.hq, (size_t)I,
+                                 (float *)(ws + sp.hs), moe::fp8_scale_row(I), s);
+        if (rc != MOE_OK) return rc;
+        a.a = ha;
+        a.out = (uint8_t *)y;
+        hipLaunchKernelGGL((fp8_experts_rows_kernel<false, 1, 2, 8, 2>), dim3((H + 31) / 32, groups), dim3(512), 0, s,
+                           a);
+        MOE_LAUNCH_CHECK("fp8_experts_rows_kernel<down>");
+        return MOE_OK;
+    }
+    int32_t *count = (int32_t *)(ws + sp.count), *offset = (int32_t *)(ws + sp.offset);
+    int32_t *pairs = (int32_t *)(ws + sp.pairs), *tiles = (int32_t *)(ws + sp.tiles);
+    rc = moe::permute_launch(topk_idx, T, k, E, count, offset, pairs, s);
     if (rc != MOE_OK) return rc;
-    a.a = {ws + sp.hq, ws + sp.hs, (size_t)I, moe::fp8_scale_row(I)};
-    a.out = y;
-    hipLaunchKernelGGL((fp8_experts_rows_kernel<false, 1, 2, 8, 2>), dim3((H + 31) / 32, groups), dim3(512), 0, s, a);
-    MOE_LAUNCH_CHECK("fp8_experts_rows_kernel<down>");
+    hipLaunchKernelGGL(fp8_experts_tiles_kernel, dim3(1), dim3(1024), 0, s, count, expert_mask, E, T, shared, Tile::BM,
+                       tiles);
+    MOE_LAUNCH_CHECK("fp8_experts_tiles_kernel");
+    a.offset = offset, a.pair_of_row = pairs, a.tiles = tiles;
+    // at most so many tiles of rows: every expert's last one may be short
+    const int most = rows / Tile::BM + (E < T * k ? E : T * k) + 1;
+    auto grid = [&](int n) { return dim3((unsigned)((most * n + 7) / 8 * 8)); };
+    a.out = ws + sp.hq;
+    a.out_scales = ws + sp.hs;
+    hipLaunchKernelGGL(fp8_experts_tile_kernel<true>, grid((I + Tile::BN / 2 - 1) / (Tile::BN / 2)),
+                       dim3(64 * Tile::WAVES), 0, s, a);
+    MOE_LAUNCH_CHECK("fp8_experts_tile_kernel<gate/up>");
+    a.a = ha;
+    a.out = (uint8_t *)y;
+    hipLaunchKernelGGL(fp8_experts_tile_kernel<false>, grid((H + Tile::BN - 1) / Tile::BN), dim3(64 * Tile::WAVES), 0,
+                       s, a);
+    MOE_LAUNCH_CHECK("fp8_experts_tile_kernel<down>");
     return MOE_OK;
 }
 

@@ -5,6 +5,7 @@
 #include "fp8_mma.h"
 #include "fp8_quant.h"
 #include "fp8_rows.h"
+#include "fp8_tile.h"
 
 namespace {
 
@@ -13,6 +14,9 @@ using moe::f32x4;
 constexpr int kMaxRows = 1 << 26;        // M and N
 constexpr int kMaxK = 1 << 27;
 constexpr int64_t kMaxStride = 1 << 28;
+// bytes of y from which a tile kernel writes past the caches (2048 x 6144 x 6144: 3.5 us
+// less, which the caches took to write back at the kernel's end)
+constexpr int64_t kStreamFrom = 4 << 20;
 
 struct MatArgs {
     moe::Fp8Act a;
@@ -25,6 +29,7 @@ struct MatArgs {
     uint8_t *y;
     size_t y_stride;
     bool y_f32;
+    __device__ __forceinline__ uint8_t *row(int m) const { return y + (size_t)m * y_stride; }
 };
 
 // Four outputs n .. n+3 of row m (those below N), bias added, rounded once.
@@ -109,13 +114,78 @@ void launch_rows(MatArgs p, hipStream_t s) {
     }
 }
 
+template <bool WIDE, class T, bool STREAM>
+__global__ __launch_bounds__(64 * T::WAVES) void fp8_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles) {
+    __shared__ uint4 smem4[T::LDS / 16];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(smem4);
+    constexpr int MT = T::MT, NT = T::NT;
+    constexpr int SN = 128 % (16 * NT) == 0 ? 1 : NT;  // a wave's columns lie in one block of W's rows, or each tile's do
+    // consecutive workgroups go to the 8 XCDs in turn: each XCD takes a run of
+    // neighbouring tiles, m fastest, so that its L2 holds the W rows they share
+    const int tiles = m_tiles * n_tiles, per = (tiles + 7) / 8;
+    const int tile = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if (tile >= tiles) return;
+    const int m0 = tile % m_tiles * T::BM, n0 = tile / m_tiles * T::BN;
+    const int m_last = min(T::BM, p.M - m0) - 1, n_last = min(T::BN, p.N - n0) - 1;
+    const int lane = threadIdx.x & 63, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / T::WN, wn = wave % T::WN;
+    const float *ws[SN];
+#pragma unroll
+    for (int i = 0; i < SN; ++i)
+        ws[i] = reinterpret_cast<const float *>(
+            p.ws + (size_t)(min(n0 + (wn * NT + i) * 16, p.N - 1) / 128) * p.ws_stride);
+    f32x4 acc[NT][MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < MT; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    moe::fp8_tile<T, WIDE, SN>(
+        smem, p.w + (size_t)n0 * p.w_stride, p.a.codes + (size_t)m0 * p.a.stride,
+        p.a.scales + (size_t)m0 * p.a.scale_stride, ws, p.K,
+        [&](int row) { return (uint32_t)min(row, n_last) * (uint32_t)p.w_stride; },
+        [&](int row) { return (uint32_t)min(row, m_last) * (uint32_t)p.a.stride; },
+        [&](int row) { return (uint32_t)min(row, m_last) * (uint32_t)p.a.scale_stride; }, acc);
+    if (p.bias)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float c = p.bias[min(n0 + (wn * NT + t) * 16 + 4 * q + j, p.N - 1)];
+#pragma unroll
+                for (int u = 0; u < MT; ++u) acc[t][u][j] += c;
+            }
+    if (p.y_f32)
+        moe::store_tile<T, MT, NT, float>(p, smem, m0, n0, wm, wn, lane, acc);
+    else
+        moe::store_tile<T, MT, NT, uint16_t, STREAM>(p, smem, m0, n0, wm, wn, lane, acc);
+}
+
+template <bool WIDE, class T>
+void launch_tile(const MatArgs &p, hipStream_t s) {
+    const int m_tiles = (p.M + T::BM - 1) / T::BM, n_tiles = (p.N + T::BN - 1) / T::BN;
+    const unsigned grid = (unsigned)(((int64_t)m_tiles * n_tiles + 7) / 8 * 8);
+    auto *kernel = (int64_t)p.M * p.N * 2 < kStreamFrom ? fp8_matmul_tile_kernel<WIDE, T, false>
+                                                        : fp8_matmul_tile_kernel<WIDE, T, true>;
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * T::WAVES), 0, s, p, m_tiles, n_tiles);
+}
+
 // WIDE: products of codes converted to bf16, for fp32 outputs.
 template <bool WIDE>
 int run(const MatArgs &p, hipStream_t s) {
     if (p.M <= 16)
         launch_rows<WIDE, 1, 1, 8, 2>(p, s);
-    else
+    else if (p.M <= 64)
         launch_rows<WIDE, 2, 2, 8, 2>(p, s);
+    else if (WIDE || p.M <= 512)
+        launch_tile<WIDE, moe::Fp8Tile<2, 4, 4, 2, 3, 3>>(p, s);
+    else
+        {
+#ifndef BIG
+        launch_tile<false, moe::Fp8Tile<2, 4, 8, 3, 2, 3>>(p, s);
+#else
+        launch_tile<false, moe::Fp8Tile<2, 4, 8, 4, 2, 2>>(p, s);
+#endif
+    }
     MOE_LAUNCH_CHECK("fp8_matmul_rows_kernel");
     return MOE_OK;
 }

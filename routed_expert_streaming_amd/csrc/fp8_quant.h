@@ -104,7 +104,7 @@ __device__ __forceinline__ uint32_t top8(const float (&v)[8]) {
 
 inline int fp8_blocks(int n) { return n / kFp8Block + (n % kFp8Block ? 1 : 0); }
 // bytes between the scale rows of quantised activations that the library lays out
-inline size_t fp8_scale_row(int K) { return align_up((size_t)fp8_blocks(K) * 4, 16); }
+__host__ __device__ inline size_t fp8_scale_row(int K) { return ((size_t)(K / kFp8Block + (K % kFp8Block ? 1 : 0)) * 4 + 15) / 16 * 16; }
 
 // rows of TYPE values -> codes and scales of 1 x 128 blocks (checked arguments)
 int fp8_quant_rows(const void *x, int x_type, size_t x_stride, int rows, int K, bool pow2, uint8_t *codes,

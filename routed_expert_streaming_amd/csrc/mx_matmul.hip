@@ -21,6 +21,7 @@
 #include "dequant.h"
 #include "lds_dma.h"
 #include "mx_quant.h"
+#include "tile.h"
 
 namespace {
 
@@ -40,6 +41,7 @@ struct MatArgs {
     uint8_t *y;
     size_t y_stride;
     bool y_f32;
+    __device__ __forceinline__ uint8_t *row(int m) const { return y + (size_t)m * y_stride; }
 };
 
 // 8 consecutive weights (one dword of codes) -> bf16, times 2^(v-127) as the converts take it
@@ -379,17 +381,6 @@ __global__ __launch_bounds__(64 * WK) void mx_matmul_few_kernel(MatArgs p, int t
 // again, their operands become zeros and their scales 1.
 constexpr int kG = 128;          // columns of a group
 
-// What the 16-byte pieces of row r of 16 are moved by (xor), for rows of 4, 8 or 16
-// pieces: a wave's 16-byte LDS reads are served in sets of 16 lanes that take rows
-// 0-3 and 12-15 from one quarter and rows 4-11 from the next (or the other way
-// round); with these keys every such set, and 16 consecutive lanes too, falls into
-// different banks (row-wise order measured 44% of the LDS cycles as conflicts).
-template <int PIECES>
-__device__ __forceinline__ int bank_key(int r) {
-    const int k = 0x78 >> 2 * (r >> 2 & 3) & 3;  // 0 2 3 1 for rows 0-3, 4-7, 8-11, 12-15
-    return PIECES == 4 ? k : PIECES == 8 ? k | (r >> 1 & 1) << 2 : k << 2 | (r & 3);
-}
-
 template <bool MX, int WM, int WN, int MT, int NT>
 struct Tile {
     static constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, WAVES = WM * WN;
@@ -407,69 +398,6 @@ struct Tile {
     static constexpr int RING = STAGES * STAGE, LDS = RING + RAW_BYTES + PACKED_BYTES;
     static_assert(STAGES >= 2 && LOADS >= WAVES, "tile does not fit its workgroup");
 };
-
-// The sums of a workgroup's tile -> y, through the (now free) ring so that the
-// stores are whole rows: in the registers' order, four n of 16 different m, a 2048 x
-// 6144 output took 10 us, as whole rows 4.  In as many parts of m as the ring's size
-// asks for.  Kept short: it runs once, from a cold instruction cache.
-template <class T, int MT, int NT, typename OUT>
-__device__ __forceinline__ void store_tile(const MatArgs &p, uint8_t *smem, int m0, int n0, int wm, int wn, int lane,
-                                           const f32x4_t (&acc)[NT][MT]) {
-    constexpr int PITCH = T::BN * (int)sizeof(OUT) + 16;
-    constexpr int FULL = T::BM * PITCH, PARTS = FULL <= T::LDS ? 1 : FULL <= 2 * T::LDS ? 2 : 4;
-    static_assert(MT % PARTS == 0 && FULL <= PARTS * T::LDS, "a part of the tile fits the LDS");
-    constexpr int PM = MT / PARTS, ROWS = T::BM / PARTS;  // row tiles per wave, rows of a part
-    constexpr int PER16 = 16 / (int)sizeof(OUT), UNITS = T::BN / PER16, THREADS = 64 * T::WAVES;
-    constexpr int AT_ONCE = ROWS * UNITS % (4 * THREADS) == 0 ? 4 : ROWS * UNITS % (2 * THREADS) == 0 ? 2 : 1;
-    static_assert(ROWS * UNITS % (AT_ONCE * THREADS) == 0, "whole rounds of stores");
-    const int r = lane & 15, q = lane >> 4;
-    // 16 bytes at a time where every row begins and ends on such a piece
-    const bool wide = ((uintptr_t)p.y | p.y_stride) % 16 == 0 && p.N % PER16 == 0;
-#pragma unroll
-    for (int part = 0; part < PARTS; ++part) {
-        if (part) __syncthreads();
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int u = 0; u < PM; ++u) {
-                const f32x4_t v = acc[t][part * PM + u];
-                uint8_t *o = smem + ((wm * PM + u) * 16 + r) * PITCH + ((wn * NT + t) * 16 + 4 * q) * (int)sizeof(OUT);
-                if constexpr (sizeof(OUT) == 4)
-                    *reinterpret_cast<f32x4_t *>(o) = v;
-                else
-                    *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-            }
-        __syncthreads();
-        // row lr of the part: wave row lr / (16 * PM), its tiles part * PM and up
-        auto row_of = [&](int lr) { return m0 + lr / (16 * PM) * (16 * MT) + part * 16 * PM + lr % (16 * PM); };
-        if (wide) {
-#pragma unroll 1
-            for (int i0 = threadIdx.x; i0 < ROWS * UNITS; i0 += AT_ONCE * THREADS) {
-                uint4 v[AT_ONCE];
-#pragma unroll
-                for (int e = 0; e < AT_ONCE; ++e) {
-                    const int i = i0 + e * THREADS;
-                    v[e] = *reinterpret_cast<const uint4 *>(smem + i / UNITS * PITCH + 16 * (i % UNITS));
-                }
-#pragma unroll
-                for (int e = 0; e < AT_ONCE; ++e) {
-                    const int i = i0 + e * THREADS, m = row_of(i / UNITS), n = n0 + i % UNITS * PER16;
-                    if (m < p.M && n < p.N)
-                        *reinterpret_cast<uint4 *>(p.y + (size_t)m * p.y_stride + (size_t)n * sizeof(OUT)) = v[e];
-                }
-            }
-        } else {  // value by value, a wave on neighbouring ones
-            const int cols = min(T::BN, p.N - n0);
-            for (int lr = threadIdx.x / 64; lr < ROWS; lr += T::WAVES) {
-                const int m = row_of(lr);
-                if (m >= p.M) continue;
-                OUT *o = reinterpret_cast<OUT *>(p.y + (size_t)m * p.y_stride) + n0;
-                const OUT *v = reinterpret_cast<const OUT *>(smem + lr * PITCH);
-                for (int n = lane; n < cols; n += 64) o[n] = v[n];
-            }
-        }
-    }
-}
 
 template <bool MX, int WM, int WN, int MT, int NT>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM * WN / 4))) void
@@ -505,8 +433,8 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles, int k_part) {
     // their pieces)
     static_assert(T::WAVES % 4 == 0, "rows of a wave's load instructions modulo 16");
     constexpr int PIECES = T::CODES / 16, ROWS = 64 / PIECES;  // of a row of codes; rows of an instruction
-    const int piece = (lane % PIECES) ^ bank_key<PIECES>(wave * ROWS + lane / PIECES);
-    const int piece_a = MX ? piece : r ^ bank_key<16>(4 * (wave - T::W_LOADS) + q);
+    const int piece = (lane % PIECES) ^ moe::bank_key<PIECES>(wave * ROWS + lane / PIECES);
+    const int piece_a = MX ? piece : r ^ moe::bank_key<16>(4 * (wave - T::W_LOADS) + q);
     // what the last stage's lanes step back by, past K
     const uint32_t cut = 16 * (piece - min(piece, nb - 1));
     const uint32_t cut_a = MX ? cut : 16 * (piece_a - min(piece_a, 4 * nb - 1));
@@ -583,10 +511,10 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles, int k_part) {
     auto stage_of = [&](int g) { return (uint32_t)(g / T::KS % S) * T::STAGE; };
     auto read_w = [&](int g, int t) {
         return *reinterpret_cast<const uint4 *>(w_at + stage_of(g) + t * 16 * T::CODES +
-                                                16 * ((4 * (g % T::KS) + q) ^ bank_key<PIECES>(r)));
+                                                16 * ((4 * (g % T::KS) + q) ^ moe::bank_key<PIECES>(r)));
     };
     auto read_x = [&](int g, int s, int u) {
-        const int piece = MX ? (4 * (g % T::KS) + q) ^ bank_key<PIECES>(r) : (4 * q + s) ^ bank_key<16>(r);
+        const int piece = MX ? (4 * (g % T::KS) + q) ^ moe::bank_key<PIECES>(r) : (4 * q + s) ^ moe::bank_key<16>(r);
         return *reinterpret_cast<const uint4 *>(x_at + stage_of(g) + u * 16 * T::A_ROW + 16 * piece);
     };
     auto read_sw = [&](int t) { return scale_at[(wn * NT + t) * 64]; };
@@ -737,9 +665,9 @@ mx_matmul_tile_kernel(MatArgs p, int m_tiles, int n_tiles, int k_part) {
                 for (int u = 0; u < MT; ++u) acc[t][u][j] += c;
             }
     if (p.y_f32)
-        store_tile<T, MT, NT, float>(p, smem, m0, n0, wm, wn, lane, acc);
+        moe::store_tile<T, MT, NT, float>(p, smem, m0, n0, wm, wn, lane, acc);
     else
-        store_tile<T, MT, NT, uint16_t>(p, smem, m0, n0, wm, wn, lane, acc);
+        moe::store_tile<T, MT, NT, uint16_t>(p, smem, m0, n0, wm, wn, lane, acc);
 }
 
 template <bool MX, int MT, int NT, int WK, int XR>

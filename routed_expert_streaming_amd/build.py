@@ -22,7 +22,7 @@ ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["abi.cpp", "router.hip", "ffn_gemv.hip", "ffn_decode.hip", "ffn_mfma.hip", "ffn_entry.hip", "cache.hip",
            "residual.hip", "noalloc.hip", "cpu_lane.cpp", "mx_quant.hip", "mx_matmul.hip", "block_norm.hip",
-           "router_scored.hip", "fp8_quant.hip", "fp8_matmul.hip", "fp8_experts.hip"]
+           "router_scored.hip", "router_split.hip", "fp8_quant.hip", "fp8_matmul.hip", "fp8_experts.hip"]
 # host-only C++ (no HIP), built with the host compiler: the CPU lane
 HOST_SOURCES = {"cpu_lane.cpp"}
 

@@ -13,6 +13,7 @@
 
 #include "common.h"
 #include "router.h"
+#include "router_split.h"
 #include "topk.h"
 
 namespace {
@@ -40,6 +41,10 @@ __device__ __forceinline__ uint64_t score_ord(double c) {
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
+__device__ __forceinline__ double ord_score(uint64_t v) {
+    return __longlong_as_double((long long)((v >> 63) ? v & 0x7FFFFFFFFFFFFFFFull : ~v));
+}
+
 // The largest of the lanes' codes, in every lane.
 __device__ __forceinline__ uint64_t wave_max_code(uint64_t v) {
     const uint32_t hi = moe::topk_wave_max((uint32_t)(v >> 32));
@@ -54,167 +59,399 @@ __device__ __forceinline__ void merge2(double &a, double &b, double c, double d)
     b = fmax(low, fmax(b, d));
 }
 
-// Slots of one token from its logits (l[j]: expert lane + 64 j).  cs: this wave's E
-// scores in LDS, sel: its k chosen scores.
-template <int PER>
-__device__ __forceinline__ void choose(const float (&l)[PER], const float *balance, const Choice &c, double *cs,
-                                       double *sel, int32_t *idx_out, float *w_out) {
-    const int lane = threadIdx.x & 63;
-    double p[PER];
-    if (c.score == MOE_SCORE_SIGMOID) {
+// Where a token's logits come from.
+struct Logits {
+    enum Kind { PARTIALS, ROUNDED, SPLIT } kind;  // fp64 partial sums; fp32 logits; fp32 parts with a bound on their error
+    const char *ws;
+    size_t stride;            // bytes between layers
+    moe::RouterSplit sp;      // of SPLIT
+    const uint16_t *x;        // [layers, T, H] and
+    const float *w, *bias;    // [layers, E, H], for SPLIT's exact sums; [layers, E] or NULL
+    int T, H;
+};
+
+// This wave's quarter of two logits as the definition has them: products and sums in fp64.
+// (Six loads of each row in flight: the quarter of rows of 6144 is one memory latency.)
+__device__ __forceinline__ void exact_quarters(const uint16_t *const (&x)[2], const float *const (&w)[2], int H,
+                                               double (&sum)[2]) {
+    constexpr int AT_ONCE = 6;
+    double a[2] = {0.0, 0.0};
+    for (int h0 = 4 * threadIdx.x; h0 < H; h0 += 1024 * AT_ONCE) {
+        uint2 xv[2][AT_ONCE];
+        float4 wv[2][AT_ONCE];
 #pragma unroll
-        for (int j = 0; j < PER; ++j) p[j] = 1.0 / (1.0 + exp(-(double)l[j]));
-    } else {
-        float top = -INFINITY;
+        for (int i = 0; i < AT_ONCE; ++i)
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (lane + 64 * j < c.E) top = fmaxf(top, l[j]);
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-        double sum = 0.0;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            p[j] = exp((double)l[j] - (double)top);
-            if (lane + 64 * j < c.E) sum += p[j];
-        }
-        sum = wave_sum_f64(sum);
-#pragma unroll
-        for (int j = 0; j < PER; ++j) p[j] /= sum;
-    }
-    double s[PER];
-    uint64_t ord[PER];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int e = lane + 64 * j;
-        s[j] = p[j] + (balance && e < c.E ? (double)balance[e] : 0.0);
-        ord[j] = e < c.E ? score_ord(s[j]) : 0ull;
-    }
-    if (c.top_groups < c.groups) {
-        const int n = c.E / c.groups;
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (lane + 64 * j < c.E) cs[lane + 64 * j] = s[j];
-        wave_sync();
-        int per = 64;  // lanes of a group
-        while (per * c.groups > 64) per >>= 1;
-        const int g = lane / per;
-        double a = -INFINITY, b = -INFINITY;
-        bool nan = false;
-        if (g < c.groups)
-            for (int i = lane % per; i < n; i += per) {
-                const double v = cs[g * n + i];
-                nan |= v != v;
-                merge2(a, b, v, -INFINITY);
+            for (int k = 0; k < 2; ++k) {
+                const int h = h0 + 1024 * i;
+                xv[k][i] = h < H ? *reinterpret_cast<const uint2 *>(x[k] + h) : make_uint2(0u, 0u);
+                wv[k][i] = h < H ? *reinterpret_cast<const float4 *>(w[k] + h) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-        for (int o = 1; o < per; o <<= 1) {
-            const double c1 = __shfl_xor(a, o, 64), c2 = __shfl_xor(b, o, 64);
-            nan |= (bool)__shfl_xor((int)nan, o, 64);
-            merge2(a, b, c1, c2);
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                a[k] += (double)bf16_bits_to_f32(xv[k][i].x & 0xFFFFu) * (double)wv[k][i].x;
+                a[k] += (double)bf16_bits_to_f32(xv[k][i].x >> 16) * (double)wv[k][i].y;
+                a[k] += (double)bf16_bits_to_f32(xv[k][i].y & 0xFFFFu) * (double)wv[k][i].z;
+                a[k] += (double)bf16_bits_to_f32(xv[k][i].y >> 16) * (double)wv[k][i].w;
+            }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) sum[k] = wave_sum_f64(a[k]);
+}
+
+__device__ __forceinline__ double wave_max_f64(double v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v = fmax(v, __shfl_xor(v, o, 64));
+    return v;
+}
+
+// Slots of one token (lane l: experts l + 64 j).  cs: this wave's E scores in LDS, sel: its
+// k chosen scores (and its groups' bounds).
+//
+// SPLIT: logit j is within off[j] of the definition's.  Scores that are further apart than
+// both may be off keep their order, so only where two that matter are not -- a group's
+// worth next to the last group that stays, an expert next to another one among the first k
+// -- the logits behind them are summed again in fp64, and the choice is made again.  A
+// logit that is not finite, or whose bound is not, is summed again first.
+// The four waves of the workgroup do those sums together, two at a time, a quarter of the
+// columns each (asked: the bits of what is asked for, quarters: two rounds' sums, summed:
+// the logits [4][E]); there: this wave has a token.
+template <int PER, bool SPLIT>
+__device__ __forceinline__ void choose(float (&l)[PER], float (&off)[PER], bool there, const Choice &c,
+                                       const float *balance, const uint16_t *x, const float *w, const float *bias,
+                                       int H, double *cs, double *sel, uint64_t (*asked)[16],
+                                       double (*quarters)[2][4], float *summed,
+                                       int32_t *idx_out, float *w_out) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const bool sigmoid = c.score == MOE_SCORE_SIGMOID, drop = c.top_groups < c.groups;
+    const int n = c.E / c.groups;  // experts of a group
+    int per = 64;                  // lanes of a group
+    while (per * c.groups > 64) per >>= 1;
+    int slot = 0;
+    int told = SPLIT ? 0 : 3;  // what is told apart: all logits finite, then the groups, then the experts
+    // one choice; whether some logits (again: bit j, logit j) are to be summed again before the next
+    auto once = [&](uint32_t &again) __attribute__((always_inline)) {
+        // scores
+        double p[PER], key[PER];
+        if (sigmoid) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) p[j] = 1.0 / (1.0 + exp(-(double)l[j]));
+        } else {
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (lane + 64 * j < c.E) top = fmaxf(top, l[j]);
+#pragma unroll
+            for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+            double sum = 0.0;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                p[j] = exp((double)l[j] - (double)top);
+                if (lane + 64 * j < c.E) sum += p[j];
+            }
+            sum = wave_sum_f64(sum);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) p[j] /= sum;
         }
-        const uint64_t worth = score_ord(nan ? NAN : c.top2 ? a + b : a);
-        int rank = 0;
-        for (int h = 0; h < c.groups; ++h) {
-            const uint64_t other = __shfl((unsigned long long)worth, h * per, 64);
-            rank += other > worth || (other == worth && h < g);
-        }
-        const uint64_t in = __ballot(g < c.groups && rank < c.top_groups);  // lane g * per: group g
+        // How far a key may be off at most: a sigmoid by a quarter of its logit; of a softmax
+        // (SPLIT has none with a balance) only the ratios matter, so its sum may be any number.
+        double far = 0.0, far_logit = 0.0;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             const int e = lane + 64 * j;
-            if (e < c.E && !(in >> (e / n * per) & 1)) ord[j] = 0ull;
-        }
-    }
-    int slot = 0;
-    for (int i = 0; i < c.k; ++i) {
-        uint64_t best = 0;
-        int best_j = 0;
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (ord[j] > best) best = ord[j], best_j = j;  // strict: the lower index wins a tie inside the lane
-        const uint64_t top = wave_max_code(best);
-        uint32_t e = 0;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const uint64_t m = __ballot(best == top && best_j == j);
-            if (m) {
-                e = 64u * j + (uint32_t)(__ffsll((long long)m) - 1);
-                break;
+            key[j] = p[j] + (balance && e < c.E ? (double)balance[e] : 0.0);
+            if (SPLIT && e < c.E) {
+                far = fmax(far, sigmoid ? 0.25 * (double)off[j] : p[j] * expm1((double)off[j]));
+                far_logit = fmax(far_logit, (double)off[j]);
+                if (told == 0 && !(fabsf(l[j]) < 1e30f && off[j] < 1e30f)) again |= 1u << j;
             }
         }
+        if (SPLIT) {
+            far = wave_max_f64(far) + 1e-15;  // and what the 64-bit functions round
+            far_logit = wave_max_f64(far_logit) + 1e-15;
+        }
+        bool step = SPLIT && told == 0 && __any(again != 0);  // sum some logits again before going on
+        uint64_t in = ~0ull;                                  // bit g * per: group g stays
+        if (drop && !step) {
+            wave_sync();
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if ((uint32_t)(lane + 64 * j) == e) {  // the owner drops the winner
-                ord[j] = 0ull;
-                sel[i] = p[j];
+            for (int j = 0; j < PER; ++j)
+                if (lane + 64 * j < c.E) cs[lane + 64 * j] = key[j];
+            wave_sync();
+            const int g = lane / per;
+            double a = -INFINITY, b = -INFINITY;
+            bool nan = false;
+            if (g < c.groups)
+                for (int i = lane % per; i < n; i += per) {
+                    const double v = cs[g * n + i];
+                    nan |= v != v;
+                    merge2(a, b, v, -INFINITY);
+                }
+            for (int o = 1; o < per; o <<= 1) {
+                const double c1 = __shfl_xor(a, o, 64), c2 = __shfl_xor(b, o, 64);
+                nan |= (bool)__shfl_xor((int)nan, o, 64);
+                merge2(a, b, c1, c2);
             }
-        if (lane == i) slot = (int)e;
+            const double value = nan ? NAN : c.top2 ? a + b : a;
+            const uint64_t worth = score_ord(value);
+            int rank = 0;
+            for (int h = 0; h < c.groups; ++h) {
+                const uint64_t other = __shfl((unsigned long long)worth, h * per, 64);
+                rank += other > worth || (other == worth && h < g);
+            }
+            const bool stays = g < c.groups && rank < c.top_groups;
+            in = __ballot(stays);
+            if (SPLIT && told <= 1) {
+                // groups that are not told from one on the other side of the border, and of those
+                // the experts that may be among the ones that make the worth
+                const double gap = c.top2 ? 4.0 * far : 2.0 * far;
+                const double in_least = -wave_max_f64(stays ? -value : -INFINITY);
+                const double out_most = wave_max_f64(g < c.groups && !stays ? value : -INFINITY);
+                const uint64_t close =
+                    __ballot(g < c.groups && !(stays ? value - out_most > gap : in_least - value > gap));
+                if (close) {
+                    if (lane % per == 0 && g < c.groups) sel[g] = (c.top2 ? b : a) - 2.0 * far;
+                    wave_sync();
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        const int e = lane + 64 * j, ge = e / n;
+                        if (e < c.E && (close >> (ge * per) & 1) && off[j] > 0.0f && !(key[j] < sel[ge])) again |= 1u << j;
+                    }
+                    step = __any(again != 0);
+                    if (step) told = 2;
+                }
+            }
+        }
+        if (!step) {
+            uint64_t ord[PER];
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const int e = lane + 64 * j;
+                ord[j] = e < c.E && (!drop || (in >> (e / n * per) & 1)) ? score_ord(key[j]) : 0ull;
+            }
+            const bool look = SPLIT && told < 3;
+            double before = 0.0;  // the last winner's key or logit
+            int before_e = 0;
+            for (int i = 0; i < c.k || look; ++i) {
+                uint64_t best = 0;
+                int best_j = 0;
+                float best_l = 0.0f;
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    if (ord[j] > best) {  // strict: the lower index wins a tie inside the lane
+                        best = ord[j];
+                        best_j = j;
+                        best_l = l[j];
+                    }
+                const uint64_t top = wave_max_code(best);
+                if (i >= c.k && top == 0) break;
+                uint32_t e = 0;
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const uint64_t m = __ballot(best == top && best_j == j);
+                    if (m) {
+                        e = 64u * j + (uint32_t)(__ffsll((long long)m) - 1);
+                        break;
+                    }
+                }
+                if (look) {
+                    // next to the one before it: both again (softmax: by their logits, or where the
+                    // scores end)
+                    const double now = sigmoid ? ord_score(top) : (double)__shfl(best_l, (int)(e & 63), 64);
+                    const bool close = i > 0 && (!(before - now > 2.0 * (sigmoid ? far : far_logit)) ||
+                                                 (!sigmoid && ord_score(top) < 1e-290));
+                    if (i >= c.k && !close) break;
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        const int mine = lane + 64 * j;
+                        if (close && (mine == (int)e || mine == before_e) && off[j] > 0.0f) again |= 1u << j;
+                    }
+                    before = now;
+                    before_e = (int)e;
+                }
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    if ((uint32_t)(lane + 64 * j) == e) {  // the owner drops the winner
+                        ord[j] = 0ull;
+                        if (i < c.k) sel[i] = p[j];
+                    }
+                if (lane == i) slot = (int)e;
+            }
+            told = 3;
+            step = SPLIT && __any(again != 0);
+        } else if (told == 0) {
+            told = 1;
+        }
+        return step;
+    };
+    if constexpr (!SPLIT) {
+        uint32_t again = 0;
+        if (there) once(again);
+    } else {
+        for (bool open = there;;) {
+            uint32_t again = 0;
+            if (open) open = once(again);
+            if (!open) again = 0;
+            if (!__syncthreads_or(open)) break;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const uint64_t m = __ballot(again >> j & 1);
+                if (lane == 0) asked[wave][j] = m;
+            }
+            __syncthreads();
+            int have = 0, round = 0, token[2] = {}, expert[2] = {};
+            auto sum_them = [&]() __attribute__((always_inline)) {
+                const uint16_t *const xs[2] = {x + (size_t)token[0] * H, x + (size_t)token[1] * H};
+                const float *const wr[2] = {w + (size_t)expert[0] * H, w + (size_t)expert[1] * H};
+                double v[2];
+                exact_quarters(xs, wr, H, v);
+                double(*q)[4] = quarters[round & 1];
+                if (lane < 2) q[lane][wave] = lane ? v[1] : v[0];
+                __syncthreads();
+                if (threadIdx.x < 2) {
+                    const int k = threadIdx.x, e = k ? expert[1] : expert[0];
+                    summed[(k ? token[1] : token[0]) * c.E + e] =
+                        (float)(((q[k][0] + q[k][1]) + (q[k][2] + q[k][3])) + (bias ? (double)bias[e] : 0.0));
+                }
+                have = 0;
+                ++round;
+            };
+            for (int v = 0; v < 4; ++v)
+                for (int j = 0; j < PER; ++j)
+                    for (uint64_t m = asked[v][j]; m; m &= m - 1) {
+                        token[1] = token[0], expert[1] = expert[0];
+                        token[0] = v, expert[0] = 64 * j + __ffsll((long long)m) - 1;
+                        if (++have == 2) sum_them();
+                    }
+            if (have) {
+                token[1] = token[0], expert[1] = expert[0];
+                sum_them();
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (again >> j & 1) l[j] = summed[wave * c.E + lane + 64 * j], off[j] = 0.0f;
+        }
     }
+    if (!there) return;
     wave_sync();
-    double w = lane < c.k ? sel[lane] : 0.0;
+    double wt = lane < c.k ? sel[lane] : 0.0;
     if (c.renorm) {
-        const double sum = wave_sum_f64(w);
-        w = sum == 0.0 ? 0.0 : w / sum;
+        const double all = wave_sum_f64(wt);
+        wt = all == 0.0 ? 0.0 : wt / all;
     }
     if (lane < c.k) {
         idx_out[lane] = slot;
-        w_out[lane] = (float)((double)c.scale * w);
+        w_out[lane] = (float)((double)c.scale * wt);
     }
 }
 
-// Dynamic LDS: four waves' scores [E] (when groups are dropped), then their chosen ones [64].
-template <int PER, bool PARTIAL>
-__global__ __launch_bounds__(256) void router_choose_kernel(const void *__restrict__ from, size_t from_stride, int T,
-                                                            int nslices, const float *__restrict__ bias,
-                                                            const float *__restrict__ balance, Choice c,
+// Dynamic LDS: four waves' scores [E] (when groups are dropped), their chosen ones [64], then
+// (SPLIT) what is asked for and the four tokens' exact logits [E].
+template <int PER, int KIND>
+__global__ __launch_bounds__(256, 2) void router_choose_kernel(Logits from, const float *__restrict__ balance, Choice c,
                                                             int32_t *__restrict__ idx, float *__restrict__ w) {
     extern __shared__ double lds[];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int t = blockIdx.x * 4 + wave;
-    if (t >= T) return;
-    const void *src = (const char *)from + blockIdx.y * from_stride;
-    if (bias) bias += (size_t)blockIdx.y * c.E;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, T = from.T;
+    const int mine = blockIdx.x * 4 + wave, t = min(mine, T - 1);
+    const char *src = from.ws + blockIdx.y * from.stride;
+    const float *bias = from.bias ? from.bias + (size_t)blockIdx.y * c.E : nullptr;
     if (balance) balance += (size_t)blockIdx.y * c.E;
-    const size_t at = ((size_t)blockIdx.y * T + t) * c.k;
-    float l[PER];
+    const size_t row = (size_t)blockIdx.y * T + t;
+    float l[PER], off[PER];
+    if constexpr (KIND == Logits::SPLIT) {
+        // the parts' sums and norms, so many parts' loads in flight at a time
+        constexpr int AT_ONCE = PER <= 4 ? 8 : PER == 8 ? 4 : 2;
+        const int parts = from.sp.parts;
+        const float *part = reinterpret_cast<const float *>(src + from.sp.partial) + (size_t)t * c.E;
+        const float *xnorm = reinterpret_cast<const float *>(src + from.sp.xn) + t;
+        const float *wnorm = reinterpret_cast<const float *>(src + from.sp.wn);
+        double v[PER];
+        float xn = 0.0f, wn[PER];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int e = min(lane + 64 * j, c.E - 1);
-        if constexpr (PARTIAL)
-            l[j] = moe::router_logit((const double *)src + (size_t)t * c.E * moe::kMaxSlices, nslices, bias, e);
-        else
-            l[j] = ((const float *)src)[(size_t)t * c.E + e];
+        for (int j = 0; j < PER; ++j) v[j] = 0.0, wn[j] = 0.0f;
+        for (int i0 = 0; i0 < parts; i0 += AT_ONCE) {
+            float a[AT_ONCE][PER], b[AT_ONCE][PER], d[AT_ONCE];
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const int pi = min(i0 + i, parts - 1);
+                d[i] = xnorm[(size_t)pi * T];
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const int e = min(lane + 64 * j, c.E - 1);
+                    a[i][j] = part[(size_t)pi * T * c.E + e];
+                    b[i][j] = wnorm[(size_t)pi * c.E + e];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                if (i0 + i >= parts) break;
+                xn += d[i];
+#pragma unroll
+                for (int j = 0; j < PER; ++j) v[j] += a[i][j], wn[j] += b[i][j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            l[j] = (float)(v[j] + (bias ? (double)bias[min(lane + 64 * j, c.E - 1)] : 0.0));
+            // and the rounding of the definition's logit and of this one; rows of zeros are exact
+            off[j] = wn[j] > 0.0f ? moe::router_split_error(from.sp.columns) * sqrtf(xn) * sqrtf(wn[j]) +
+                                        0x1p-22f * fabsf(l[j])
+                                  : wn[j] == 0.0f ? 0.0f : INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int e = min(lane + 64 * j, c.E - 1);
+            off[j] = 0.0f;
+            if constexpr (KIND == Logits::PARTIALS)
+                l[j] = moe::router_logit((const double *)src + (size_t)t * c.E * moe::kMaxSlices,
+                                         (from.H + moe::kSlice - 1) / moe::kSlice, bias, e);
+            else
+                l[j] = ((const float *)src)[(size_t)t * c.E + e];
+        }
     }
     const int scores = c.top_groups < c.groups ? c.E : 0;
-    choose<PER>(l, balance, c, lds + wave * scores, lds + 4 * scores + 64 * wave, idx + at, w + at);
+    double *sel = lds + 4 * scores + 64 * wave;
+    uint64_t(*asked)[16] = reinterpret_cast<uint64_t(*)[16]>(lds + 4 * scores + 256);
+    choose<PER, KIND == Logits::SPLIT>(l, off, mine < T, c, balance, from.x + ((size_t)blockIdx.y * T + 4 * blockIdx.x) * from.H,
+                                       from.w + (size_t)blockIdx.y * c.E * from.H, bias, from.H, lds + wave * scores, sel,
+                                       asked, reinterpret_cast<double(*)[2][4]>(asked + 4),
+                                       reinterpret_cast<float *>(lds + 4 * scores + 256 + 64 + 16), idx + row * c.k,
+                                       w + row * c.k);
 }
 
-template <bool PARTIAL>
-int launch_choose(const void *from, size_t from_stride, int layers, int T, int H, const float *bias,
-                  const float *balance, const Choice &c, int32_t *idx, float *w, hipStream_t s) {
-    const dim3 grid((T + 3) / 4, layers), block(256);
-    const size_t lds = ((c.top_groups < c.groups ? (size_t)4 * c.E : 0) + 256) * sizeof(double);
-    const int nslices = (H + moe::kSlice - 1) / moe::kSlice;
-    auto *kernel = c.E <= 64    ? router_choose_kernel<1, PARTIAL>
-                   : c.E <= 128 ? router_choose_kernel<2, PARTIAL>
-                   : c.E <= 256 ? router_choose_kernel<4, PARTIAL>
-                   : c.E <= 512 ? router_choose_kernel<8, PARTIAL>
-                                : router_choose_kernel<16, PARTIAL>;
-    hipLaunchKernelGGL(kernel, grid, block, lds, s, from, from_stride, T, nslices, bias, balance, c, idx, w);
+template <int KIND>
+int launch_choose(const Logits &from, int layers, const float *balance, const Choice &c, int32_t *idx, float *w,
+                  hipStream_t s) {
+    const dim3 grid((from.T + 3) / 4, layers), block(256);
+    const size_t lds = ((c.top_groups < c.groups ? (size_t)4 * c.E : 0) + 256) * sizeof(double) +
+                       (KIND == Logits::SPLIT ? (64 + 16) * sizeof(double) + (size_t)4 * c.E * sizeof(float) : 0);
+    auto *kernel = c.E <= 64    ? router_choose_kernel<1, KIND>
+                   : c.E <= 128 ? router_choose_kernel<2, KIND>
+                   : c.E <= 256 ? router_choose_kernel<4, KIND>
+                   : c.E <= 512 ? router_choose_kernel<8, KIND>
+                                : router_choose_kernel<16, KIND>;
+    hipLaunchKernelGGL(kernel, grid, block, lds, s, from, balance, c, idx, w);
     MOE_LAUNCH_CHECK("router_choose_kernel");
     return MOE_OK;
 }
 
-// Bytes of one layer's workspace: fp64 partial logits, or fp32 logits.
-size_t layer_bytes(int T, int E) {
+// Bytes of one layer's workspace by where its logits come from.
+size_t exact_bytes(int T, int E) {
     return T <= kSmallT ? (size_t)T * E * moe::kMaxSlices * sizeof(double)
                         : moe::align_up((size_t)T * E * sizeof(float), 256);
 }
+bool split_pays(int layers, int T, int E, int H) { return T > 4; }
 
 }  // namespace
 
 extern "C" size_t moe_router_scored_workspace_bytes(int n_layers, int T, int E, int H) {
     if (n_layers <= 0 || T <= 0 || E <= 0 || E > kMaxE || H <= 0) return 0;
-    return (size_t)n_layers * layer_bytes(T, E);
+    const size_t exact = exact_bytes(T, E), split = moe::router_split_layout(n_layers, T, E, H).total;
+    return (size_t)n_layers * (split_pays(n_layers, T, E, H) && split > exact ? split : exact);
 }
 
 extern "C" int moe_router_scored(const uint16_t *x, int n_layers, int T, int H, const float *w_router,
@@ -249,22 +486,33 @@ extern "C" int moe_router_scored(const uint16_t *x, int n_layers, int T, int H, 
     if (n_layers > 65535) return moe::fail(MOE_E_SHAPE, "router_scored: n_layers=%d above 65535", n_layers);
     if (((uintptr_t)x | (uintptr_t)w_router) % 16 || (uintptr_t)workspace % 16)
         return moe::fail(MOE_E_ARG, "router_scored: x, w_router and workspace must be 16-byte aligned");
-    const size_t per = layer_bytes(T, E), need = (size_t)n_layers * per;
+    const size_t need = moe_router_scored_workspace_bytes(n_layers, T, E, H);
     if (workspace_bytes < need)
         return moe::fail(MOE_E_NOMEM, "router_scored: workspace %zu < %zu bytes", workspace_bytes, need);
     const Choice c{E, k, routing->score, groups, top, routing->group_rule == MOE_GROUP_TOP2, routing->renormalise,
                    routing->scale};
     hipStream_t s = (hipStream_t)stream;
-    if (T <= kSmallT) {
-        const int rc = moe::router_partials(x, T, H, w_router, E, (double *)workspace, s, n_layers, per);
+    Logits from{Logits::PARTIALS, (const char *)workspace, exact_bytes(T, E), {}, x, w_router, bias, T, H};
+    // (a softmax next to a balance needs every logit exact: the split would tell too little apart)
+    if (split_pays(n_layers, T, E, H) && !(balance && routing->score == MOE_SCORE_SOFTMAX)) {
+        from.kind = Logits::SPLIT;
+        from.sp = moe::router_split_layout(n_layers, T, E, H);
+        from.stride = from.sp.total;
+        const int rc = moe::router_split(x, n_layers, T, H, w_router, E, from.sp, workspace, s);
         if (rc != MOE_OK) return rc;
-        return launch_choose<true>(workspace, per, n_layers, T, H, bias, balance, c, topk_idx, topk_w, s);
+        return launch_choose<Logits::SPLIT>(from, n_layers, balance, c, topk_idx, topk_w, s);
     }
+    if (T <= kSmallT) {
+        const int rc = moe::router_partials(x, T, H, w_router, E, (double *)workspace, s, n_layers, from.stride);
+        if (rc != MOE_OK) return rc;
+        return launch_choose<Logits::PARTIALS>(from, n_layers, balance, c, topk_idx, topk_w, s);
+    }
+    from.kind = Logits::ROUNDED;
     for (int l = 0; l < n_layers; ++l) {
         const int rc = moe::router_logits_rows(x + (size_t)l * T * H, T, H, w_router + (size_t)l * E * H,
                                                bias ? bias + (size_t)l * E : nullptr, E,
-                                               (float *)((char *)workspace + (size_t)l * per), s);
+                                               (float *)((char *)workspace + (size_t)l * from.stride), s);
         if (rc != MOE_OK) return rc;
     }
-    return launch_choose<false>(workspace, per, n_layers, T, H, bias, balance, c, topk_idx, topk_w, s);
+    return launch_choose<Logits::ROUNDED>(from, n_layers, balance, c, topk_idx, topk_w, s);
 }

@@ -101,10 +101,9 @@ __device__ __forceinline__ void exact_quarters(const uint16_t *const (&x)[2], co
     for (int k = 0; k < 2; ++k) sum[k] = wave_sum_f64(a[k]);
 }
 
-__device__ __forceinline__ double wave_max_f64(double v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v = fmax(v, __shfl_xor(v, o, 64));
-    return v;
+// The largest of the lanes' values, none of them negative, in every lane.
+__device__ __forceinline__ float wave_max_positive(float v) {
+    return __uint_as_float(moe::topk_wave_max(__float_as_uint(v)));
 }
 
 // Slots of one token (lane l: experts l + 64 j).  cs: this wave's E scores in LDS, sel: its
@@ -139,12 +138,11 @@ __device__ __forceinline__ void choose(float (&l)[PER], float (&off)[PER], bool 
 #pragma unroll
             for (int j = 0; j < PER; ++j) p[j] = 1.0 / (1.0 + exp(-(double)l[j]));
         } else {
-            float top = -INFINITY;
+            uint32_t most = 0;
 #pragma unroll
             for (int j = 0; j < PER; ++j)
-                if (lane + 64 * j < c.E) top = fmaxf(top, l[j]);
-#pragma unroll
-            for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+                if (lane + 64 * j < c.E) most = max(most, moe::topk_ord(l[j]));
+            const float top = moe::topk_logit(moe::topk_wave_max(most));
             double sum = 0.0;
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
@@ -157,20 +155,24 @@ __device__ __forceinline__ void choose(float (&l)[PER], float (&off)[PER], bool 
         }
         // How far a key may be off at most: a sigmoid by a quarter of its logit; of a softmax
         // (SPLIT has none with a balance) only the ratios matter, so its sum may be any number.
-        double far = 0.0, far_logit = 0.0;
+        // (e^d - 1 <= d + d^2 up to 1; the margins are for these bounds' own rounding and the
+        // 64-bit functions'.)
+        float far32 = 0.0f, far_logit32 = 0.0f;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             const int e = lane + 64 * j;
             key[j] = p[j] + (balance && e < c.E ? (double)balance[e] : 0.0);
             if (SPLIT && e < c.E) {
-                far = fmax(far, sigmoid ? 0.25 * (double)off[j] : p[j] * expm1((double)off[j]));
-                far_logit = fmax(far_logit, (double)off[j]);
-                if (told == 0 && !(fabsf(l[j]) < 1e30f && off[j] < 1e30f)) again |= 1u << j;
+                const float d = off[j];
+                far32 = fmaxf(far32, sigmoid ? 0.25f * d : d <= 1.0f ? (float)p[j] * (d + d * d) : 1e30f);
+                far_logit32 = fmaxf(far_logit32, d);
+                if (told == 0 && !(fabsf(l[j]) < 1e30f && d < 1e30f)) again |= 1u << j;
             }
         }
+        double far = 0.0, far_logit = 0.0;
         if (SPLIT) {
-            far = wave_max_f64(far) + 1e-15;  // and what the 64-bit functions round
-            far_logit = wave_max_f64(far_logit) + 1e-15;
+            far = 1.0001 * (double)wave_max_positive(far32) + 1e-15;
+            far_logit = 1.0001 * (double)wave_max_positive(far_logit32) + 1e-15;
         }
         bool step = SPLIT && told == 0 && __any(again != 0);  // sum some logits again before going on
         uint64_t in = ~0ull;                                  // bit g * per: group g stays
@@ -207,8 +209,8 @@ __device__ __forceinline__ void choose(float (&l)[PER], float (&off)[PER], bool 
                 // groups that are not told from one on the other side of the border, and of those
                 // the experts that may be among the ones that make the worth
                 const double gap = c.top2 ? 4.0 * far : 2.0 * far;
-                const double in_least = -wave_max_f64(stays ? -value : -INFINITY);
-                const double out_most = wave_max_f64(g < c.groups && !stays ? value : -INFINITY);
+                const double in_least = ord_score(~wave_max_code(stays ? ~worth : 0ull));
+                const double out_most = ord_score(wave_max_code(g < c.groups && !stays ? worth : 0ull));
                 const uint64_t close =
                     __ballot(g < c.groups && !(stays ? value - out_most > gap : in_least - value > gap));
                 if (close) {
@@ -339,7 +341,8 @@ __device__ __forceinline__ void choose(float (&l)[PER], float (&off)[PER], bool 
     wave_sync();
     double wt = lane < c.k ? sel[lane] : 0.0;
     if (c.renorm) {
-        const double all = wave_sum_f64(wt);
+        double all = 0.0;
+        for (int i = 0; i < c.k; ++i) all += sel[i];
         wt = all == 0.0 ? 0.0 : wt / all;
     }
     if (lane < c.k) {
@@ -444,14 +447,18 @@ size_t exact_bytes(int T, int E) {
     return T <= kSmallT ? (size_t)T * E * moe::kMaxSlices * sizeof(double)
                         : moe::align_up((size_t)T * E * sizeof(float), 256);
 }
-bool split_pays(int layers, int T, int E, int H) { return T > 4; }
+// Where the logits come from the split sums: from a dozen tokens on.  One layer of 4096 x
+// 128 and of 6144 x 256, us with exact sums and split: 8 tokens 16 against 23, 21 against
+// 30; 16: 23 against 24, 30 against 36; 32: 38 against 26, 51 against 38.  Eight layers
+// of 4096 x 128: 8 tokens 24 against 30, 16: 37 against 33.
+bool split_pays(int layers, int T) { return T > (layers > 1 ? 8 : 16); }
 
 }  // namespace
 
 extern "C" size_t moe_router_scored_workspace_bytes(int n_layers, int T, int E, int H) {
     if (n_layers <= 0 || T <= 0 || E <= 0 || E > kMaxE || H <= 0) return 0;
     const size_t exact = exact_bytes(T, E), split = moe::router_split_layout(n_layers, T, E, H).total;
-    return (size_t)n_layers * (split_pays(n_layers, T, E, H) && split > exact ? split : exact);
+    return (size_t)n_layers * (split_pays(n_layers, T) && split > exact ? split : exact);
 }
 
 extern "C" int moe_router_scored(const uint16_t *x, int n_layers, int T, int H, const float *w_router,
@@ -494,7 +501,7 @@ extern "C" int moe_router_scored(const uint16_t *x, int n_layers, int T, int H, 
     hipStream_t s = (hipStream_t)stream;
     Logits from{Logits::PARTIALS, (const char *)workspace, exact_bytes(T, E), {}, x, w_router, bias, T, H};
     // (a softmax next to a balance needs every logit exact: the split would tell too little apart)
-    if (split_pays(n_layers, T, E, H) && !(balance && routing->score == MOE_SCORE_SOFTMAX)) {
+    if (split_pays(n_layers, T) && !(balance && routing->score == MOE_SCORE_SOFTMAX)) {
         from.kind = Logits::SPLIT;
         from.sp = moe::router_split_layout(n_layers, T, E, H);
         from.stride = from.sp.total;

@@ -26,7 +26,7 @@ def weight_error(x, w, T, H):
     return 2.0 ** -23 + 4 * logit
 
 
-FEW = 4  # tokens up to which every logit is summed in 64 bits
+FEW = 8  # tokens up to which every logit is summed in 64 bits
 SCORE = {"softmax": L.MOE_SCORE_SOFTMAX, "sigmoid": L.MOE_SCORE_SIGMOID}
 RULE = {"max": L.MOE_GROUP_MAX, "top2": L.MOE_GROUP_TOP2}
 

@@ -172,15 +172,18 @@ __global__ __launch_bounds__(64 * Tile::WAVES) void fp8_experts_tile_kernel(Expe
     __shared__ uint4 smem4[T::LDS / 16];
     uint8_t *smem = reinterpret_cast<uint8_t *>(smem4);
     const int H = p.H, I = p.I, P = p.T * p.k, K = GATEUP ? H : I, N = GATEUP ? I : H;
-    // each XCD takes a run of neighbouring tiles, an expert's columns fastest: the workgroups
-    // that run together share its rows of A, and of W with the expert's next rows
+    // Each XCD takes a run of neighbouring tiles, an expert's rows fastest: the tiles that
+    // share rows of W start together and read them from its L2.  (With the columns fastest
+    // they drifted apart: 2.9 GB came from memory for 1.6 GB of W1 and W3.)
     const int n_tiles = (N + BN - 1) / BN, tiles = p.tiles[0] * n_tiles, per = (tiles + 7) / 8;
     const int i = blockIdx.x >> 3, tile = (blockIdx.x & 7) * per + i;
     if (i >= per || tile >= tiles) return;
     const int number = p.tiles[1 + tile / n_tiles], e = number & ((1 << kGroupBits) - 1);
-    const int m0 = (number >> kGroupBits) * T::BM, n0 = tile % n_tiles * BN;
     const bool shared = e == p.E;
-    const int first = shared ? P : p.offset[e], rows = (shared ? p.T : p.offset[e + 1] - first) - m0;  // from m0 on
+    const int first = shared ? P : p.offset[e], all = shared ? p.T : p.offset[e + 1] - first;  // rows
+    const int m_tiles = (all + T::BM - 1) / T::BM;
+    const int local = tile - (tile / n_tiles - (number >> kGroupBits)) * n_tiles;  // of the expert's tiles
+    const int m0 = local % m_tiles * T::BM, n0 = local / m_tiles * BN, rows = all - m0;  // rows from m0 on
     const int32_t *pairs = shared ? nullptr : p.pair_of_row + first + m0;
     const uint8_t *slab = shared ? p.shared : (const uint8_t *)p.table[e];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;

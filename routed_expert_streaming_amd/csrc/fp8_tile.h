@@ -118,8 +118,14 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
     else
         wait_vm<0>();
     ring_barrier();
-    Fp8Frag wf[NT], xf = read_x(0, 0);
-    float sf = read_s(0, 0);
+    // A's operands are read AHEAD columns of tiles before their products: with one, the
+    // eight waves' reads in turn took longer than a column's products.
+    constexpr int AHEAD = MT >= 4 ? 2 : 1;
+    static_assert(MT % AHEAD == 0, "an operand's place");
+    Fp8Frag wf[NT], xf[AHEAD];
+    float sf[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) xf[u] = read_x(0, u), sf[u] = read_s(0, u);
 #pragma unroll
     for (int t = 0; t < NT; ++t) wf[t] = read_w(0, t);
 
@@ -164,15 +170,16 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
         for (int t = 0; t < NT; ++t) wo[t] = operand<WIDE>(wf[t]);
         static_for<0, MT>([&](auto u_const) __attribute__((always_inline)) {
             constexpr int u = decltype(u_const)::value;
-            if (CUT) cut_frag(xf, q, pieces);
-            const auto x = operand<WIDE>(xf);
+            if (CUT) cut_frag(xf[u % AHEAD], q, pieces);
+            const auto x = operand<WIDE>(xf[u % AHEAD]);
             float su[SN];
 #pragma unroll
-            for (int i = 0; i < SN; ++i) su[i] = sf * sw[i];
+            for (int i = 0; i < SN; ++i) su[i] = sf[u % AHEAD] * sw[i];
             // the next operands (past the last block whatever the rings hold)
-            if (u + 1 == MT) turn(g);
-            xf = u + 1 < MT ? read_x(g, u + 1) : read_x(g + 1, 0);
-            sf = u + 1 < MT ? read_s(g, u + 1) : read_s(g + 1, 0);
+            constexpr int next = u + AHEAD;
+            if (next == MT) turn(g);
+            xf[u % AHEAD] = next < MT ? read_x(g, next) : read_x(g + 1, next - MT);
+            sf[u % AHEAD] = next < MT ? read_s(g, next) : read_s(g + 1, next - MT);
             static_for<0, NT>([&](auto t_const) __attribute__((always_inline)) {
                 constexpr int t = decltype(t_const)::value, i = u * NT + t;
                 const f32x4 v = mfma_fp8(wo[t], x);
@@ -184,7 +191,7 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
             });
             // the loads that the last turn made room for: from there on, spread over the products,
             // because a wave whose load the memory pipeline does not take yet issues nothing else
-            constexpr int step = (u + 1) % MT, turned = u + 1 < MT ? 1 : 0;
+            constexpr int step = (u + AHEAD) % MT, turned = u + AHEAD < MT ? 1 : 0;
             if constexpr (step * T::SPREAD < T::EACH) {
                 const int from = g - turned;  // the turn's block
                 if (step == 0 && from >= 0 && ((from + SA) & 3) == 0 && from + SA < nb) issue_scales((from + SA) >> 2);

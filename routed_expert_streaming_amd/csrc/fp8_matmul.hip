@@ -128,7 +128,8 @@ __global__ __launch_bounds__(64 * T::WAVES) void fp8_matmul_tile_kernel(MatArgs 
     const int m0 = tile % m_tiles * T::BM, n0 = tile / m_tiles * T::BN;
     const int m_last = min(T::BM, p.M - m0) - 1, n_last = min(T::BN, p.N - n0) - 1;
     const int lane = threadIdx.x & 63, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / T::WN, wn = wave % T::WN;
+    const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = all % T::GROUP;
+    const int wm = wave / T::WN, wn = wave % T::WN;
     const float *ws[SN];
 #pragma unroll
     for (int i = 0; i < SN; ++i)
@@ -155,9 +156,9 @@ __global__ __launch_bounds__(64 * T::WAVES) void fp8_matmul_tile_kernel(MatArgs 
                 for (int u = 0; u < MT; ++u) acc[t][u][j] += c;
             }
     if (p.y_f32)
-        moe::store_tile<T, MT, NT, float>(p, smem, m0, n0, wm, wn, lane, acc);
+        moe::store_tile<T, MT, NT, float>(p, smem, m0, n0, wm, wn, lane, acc, all < T::GROUP);
     else
-        moe::store_tile<T, MT, NT, uint16_t, STREAM>(p, smem, m0, n0, wm, wn, lane, acc);
+        moe::store_tile<T, MT, NT, uint16_t, STREAM>(p, smem, m0, n0, wm, wn, lane, acc, all < T::GROUP);
 }
 
 template <bool WIDE, class T>
@@ -169,24 +170,131 @@ void launch_tile(const MatArgs &p, hipStream_t s) {
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * T::WAVES), 0, s, p, m_tiles, n_tiles);
 }
 
+// A few rows of bf16 activations, quantised by each workgroup (16 rows of W) for itself.
+template <bool WIDE, int WK, int U>
+__global__ __launch_bounds__(64 * WK) void fp8_matmul_few_kernel(MatArgs p) {
+    extern __shared__ uint4 few_smem[];
+    __shared__ f32x4 part[WK][1][64];
+    uint8_t *xs = reinterpret_cast<uint8_t *>(few_smem);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int n0 = blockIdx.x * 16;
+    const uint8_t *const w[1] = {p.w + (size_t)min(n0 + r, p.N - 1) * p.w_stride};
+    const float *const ws[1] = {reinterpret_cast<const float *>(p.ws + (size_t)(n0 / 128) * p.ws_stride)};
+    f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
+    moe::multiply_few<WIDE, 1, U, WK>(wave, p.K, q, w, ws, xs + min(r, p.M - 1) * moe::few_row(p.K), acc, [&]() {
+        moe::quantise_few<MOE_BF16>(xs, p.a.codes, p.a.stride, p.M, p.K, threadIdx.x, 64 * WK);
+        __syncthreads();
+    });
+    part[wave][0][lane] = acc[0];
+    __syncthreads();
+    if (wave == 0) store4(p, r, n0 + 4 * q, moe::joined<WK, 1>(part, 0, lane));
+}
+
+// Which kernel a product takes: the least estimated time, in us.  A round of as many
+// workgroups as the CUs hold takes a + b per turn, a turn being KW blocks of 128 columns
+// (of the rows kernels, 16 blocks); b grows from `few` workgroups to a full round (they
+// share L2 and power).  Measured at K = 1536 .. 6144, kernels alone:
+//                      y bf16: a, b few .. full       y fp32
+//   rows, 16 x 16      1.6  2.0 (+ 0.04 a row)          the same
+//   rows, 16 x 32      2.6  2.4 (+ 0.04 a row)          the same
+//   16 x 32,   KW 4    2.5  0.56                        2.5  0.62
+//   32 x 32,   KW 4    2.6  0.68                        2.9  0.82
+//   32 x 64,   KW 4    3.8  0.85                        3.2  1.20 (two stages)
+//   64 x 64,   KW 2    3.7  0.64                        5.0  0.84
+//   128 x 64,  KW 2    2.7  1.15                        3.0  1.36
+//   128 x 128, KW 1    4.9  0.60 .. 0.63                --  (two groups: 4.0  1.76)
+//   128 x 128, 4 waves 4.6  0.87 .. 1.20, two a CU      --
+//   256 x 192          7.0  1.27 .. 1.41                --
+//   256 x 256          8.0  1.36 .. 1.70                --
+// So 32 x 6144 x 6144 takes 10.9 us in 32 x 32 tiles (16.7 where each wave streams W and A
+// for itself), 2048 rows 75 us in 256 x 192 ones and 101 in 128 x 128.
+enum Kind { FEW, ROWS1, ROWS2, T16, T32, T32W, T64, T128N, T128, T128P, T256N, T256 };
+
+Kind plan(bool wide, int M, int N, int K, bool near) {
+    const int nb = moe::fp8_blocks(K);
+    auto over = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    const struct {
+        Kind kind;
+        int bm, bn, kw, slots;
+        float a, few, full;
+    } tiles[2][12] = {{{ROWS1, 16, 16, 16, 2, 1.6f, 2.0f + 0.04f * (float)M, 3.0f + 0.10f * (float)M},
+                       {ROWS2, 16, 32, 16, 1, 2.6f, 2.4f + 0.04f * (float)M, 2.4f + 0.04f * (float)M},
+                       {T16, 16, 32, 4, 1, 2.5f, 0.56f, 0.60f},
+                       {T32, 32, 32, 4, 1, 2.6f, 0.68f, 0.68f},
+                       {T32W, 32, 64, 4, 1, 3.8f, 0.85f, 0.87f},
+                       {T64, 64, 64, 2, 1, 3.7f, 0.64f, 0.68f},
+                       {T128N, 128, 64, 2, 1, 2.7f, 1.10f, 1.18f},
+                       {T128, 128, 128, 1, 1, 4.9f, 0.60f, 0.63f},
+                       {T128P, 128, 128, 1, 2, 4.6f, 0.80f, 1.20f},
+                       {T256N, 256, 192, 1, 1, 7.0f, 1.25f, 1.41f},
+                       {T256, 256, 256, 1, 1, 8.0f, 1.30f, 1.70f}},
+                      {{ROWS1, 16, 16, 16, 2, 1.6f, 2.0f + 0.04f * (float)M, 3.0f + 0.10f * (float)M},
+                       {ROWS2, 16, 32, 16, 1, 2.6f, 2.4f + 0.04f * (float)M, 2.4f + 0.04f * (float)M},
+                       {T16, 16, 32, 4, 1, 2.5f, 0.62f, 0.65f},
+                       {T32, 32, 32, 4, 1, 2.9f, 0.82f, 0.82f},
+                       {T32W, 32, 64, 4, 1, 3.2f, 1.20f, 1.25f},
+                       {T64, 64, 64, 2, 1, 5.0f, 0.84f, 0.86f},
+                       {T128N, 128, 64, 2, 1, 3.0f, 1.36f, 1.50f},
+                       {T128, 128, 128, 2, 1, 4.0f, 1.70f, 2.10f}}};
+    Kind best = ROWS1;
+    if (!near) return M <= 16 ? ROWS1 : ROWS2;
+    float least = 1e30f;
+    for (const auto &t : tiles[wide]) {
+        if (t.bm == 0 || ((t.kind == ROWS1 || t.kind == ROWS2) && M > 16)) continue;
+        const int64_t wgs = over(M, t.bm) * over(N, t.bn), round = 256 * t.slots, rest = wgs % round;
+        if (wgs > 4000000) continue;  // below 2^32 threads
+        const float turns = (float)over(nb, t.kw), whole = t.a + t.full * turns;
+        const float part = rest ? t.a + (t.few + (t.full - t.few) * (float)rest / (float)round) * turns : 0.0f;
+        const float us = (float)(wgs / round) * whole + part;
+        if (us < least) least = us, best = t.kind;
+    }
+    return best;
+}
+
+// Rows further apart than this take the rows kernels: a tile's lane offsets are 32 bits.
+constexpr int64_t kTileStride = 8 << 20;
+
+// Which activations the kernel quantises itself: up to kFewRows rows that leave LDS room
+// for two workgroups a CU, and few enough workgroups to do so again and again (1 x 4096 x
+// 4096: two launches 8.1 us, one 6.2).
+constexpr int kFewBytes = 52 << 10, kFewWgs = 1024;
+bool few(bool quantise, int M, int N, int K) {
+    return quantise && M <= moe::kFewRows && (int64_t)M * moe::few_row(K) <= kFewBytes && N <= 16 * kFewWgs;
+}
+
 // WIDE: products of codes converted to bf16, for fp32 outputs.
 template <bool WIDE>
-int run(const MatArgs &p, hipStream_t s) {
-    if (p.M <= 16)
-        launch_rows<WIDE, 1, 1, 8, 2>(p, s);
-    else if (p.M <= 64)
-        launch_rows<WIDE, 2, 2, 8, 2>(p, s);
-    else if (WIDE || p.M <= 512)
-        launch_tile<WIDE, moe::Fp8Tile<2, 4, 4, 2, 3, 3>>(p, s);
-    else
-        {
-#ifndef BIG
-        launch_tile<false, moe::Fp8Tile<2, 4, 8, 3, 2, 3>>(p, s);
-#else
-        launch_tile<false, moe::Fp8Tile<2, 4, 8, 4, 2, 2>>(p, s);
-#endif
+int run(const MatArgs &p, Kind kind, hipStream_t s) {
+    switch (kind) {
+        case FEW:
+            hipLaunchKernelGGL((fp8_matmul_few_kernel<WIDE, 8, 2>), dim3((p.N + 15) / 16), dim3(512),
+                               (size_t)p.M * moe::few_row(p.K), s, p);
+            break;
+        case ROWS1: launch_rows<WIDE, 1, 1, 8, 2>(p, s); break;
+        case ROWS2: launch_rows<WIDE, 1, 2, 8, 2>(p, s); break;
+        case T16: launch_tile<WIDE, moe::Fp8Tile<1, 2, 1, 1, 4, 4, 4>>(p, s); break;
+        case T32: launch_tile<WIDE, moe::Fp8Tile<1, 2, 2, 1, 3, 3, 4>>(p, s); break;
+        case T32W: launch_tile<WIDE, moe::Fp8Tile<1, 4, 2, 1, WIDE ? 2 : 3, WIDE ? 2 : 3, 4>>(p, s); break;
+        case T64: launch_tile<WIDE, moe::Fp8Tile<2, 2, 2, 2, 3, 3, 2>>(p, s); break;
+        case T128N: launch_tile<WIDE, moe::Fp8Tile<2, 2, 4, 2, 2, 2, 2>>(p, s); break;
+        case T128:
+            if constexpr (WIDE)
+                launch_tile<WIDE, moe::Fp8Tile<2, 2, 4, 4, 2, 2, 2>>(p, s);
+            else
+                launch_tile<WIDE, moe::Fp8Tile<2, 4, 4, 2, 3, 3>>(p, s);
+            break;
+        default:
+            if constexpr (!WIDE) {
+                if (kind == T128P)
+                    launch_tile<WIDE, moe::Fp8Tile<2, 2, 4, 4, 2, 2>>(p, s);
+                else if (kind == T256N)
+                    launch_tile<WIDE, moe::Fp8Tile<2, 4, 8, 3, 2, 3>>(p, s);
+                else
+                    launch_tile<WIDE, moe::Fp8Tile<2, 4, 8, 4, 2, 2>>(p, s);
+            }
     }
-    MOE_LAUNCH_CHECK("fp8_matmul_rows_kernel");
+    MOE_LAUNCH_CHECK("fp8_matmul_kernel");
     return MOE_OK;
 }
 
@@ -194,9 +302,9 @@ int run(const MatArgs &p, hipStream_t s) {
 struct Space {
     size_t codes, scales, total;
 };
-Space layout(int M, int K, bool quantise) {
+Space layout(int M, int N, int K, bool quantise) {
     Space w{};
-    if (!quantise) return w;
+    if (!quantise || few(quantise, M, N, K)) return w;
     w.scales = moe::align_up((size_t)M * K, 256);
     w.total = w.scales + moe::align_up((size_t)M * moe::fp8_scale_row(K), 256);
     return w;
@@ -207,7 +315,7 @@ Space layout(int M, int K, bool quantise) {
 extern "C" size_t moe_fp8_matmul_workspace_bytes(int M, int N, int K, int a_type) {
     if (M <= 0 || N <= 0 || K <= 0 || K % 16 || M > kMaxRows || N > kMaxRows || K > kMaxK) return 0;
     if (a_type != MOE_BF16 && a_type != MOE_FP8) return 0;
-    return layout(M, K, a_type == MOE_BF16).total;
+    return layout(M, N, K, a_type == MOE_BF16).total;
 }
 
 extern "C" int moe_fp8_matmul(const void *a, int a_type, int64_t a_stride, const float *a_scales,
@@ -242,7 +350,7 @@ extern "C" int moe_fp8_matmul(const void *a, int a_type, int64_t a_stride, const
     if ((M > 1 && (a_stride > kMaxStride || (!quantise && a_scales_stride > kMaxStride))) ||
         (N > 1 && w_stride > kMaxStride))
         return moe::fail(MOE_E_SHAPE, "fp8_matmul: operands' rows more than %lld bytes apart", (long long)kMaxStride);
-    const Space sp = layout(M, K, quantise);
+    const Space sp = layout(M, N, K, quantise);
     if (workspace_bytes < sp.total || (sp.total && !workspace))
         return moe::fail(MOE_E_NOMEM, "fp8_matmul: workspace %zu < %zu bytes", workspace_bytes, sp.total);
     if (sp.total && (uintptr_t)workspace % 16)
@@ -260,7 +368,8 @@ extern "C" int moe_fp8_matmul(const void *a, int a_type, int64_t a_stride, const
     p.y = (uint8_t *)y;
     p.y_stride = M > 1 ? (size_t)y_stride : 0;
     p.y_f32 = y_type == MOE_FP32;
-    if (quantise) {
+    const bool here = few(quantise, M, N, K);
+    if (quantise && !here) {
         uint8_t *codes = (uint8_t *)workspace + sp.codes;
         float *scales = (float *)((uint8_t *)workspace + sp.scales);
         const int rc = moe::fp8_quant_rows(a, MOE_BF16, p.a.stride, M, K, false, codes, (size_t)K, scales,
@@ -268,5 +377,7 @@ extern "C" int moe_fp8_matmul(const void *a, int a_type, int64_t a_stride, const
         if (rc != MOE_OK) return rc;
         p.a = {codes, (const uint8_t *)scales, (size_t)K, moe::fp8_scale_row(K)};
     }
-    return p.y_f32 ? run<true>(p, s) : run<false>(p, s);
+    const bool near = (M == 1 || p.a.stride < (size_t)kTileStride) && (N == 1 || p.w_stride < (size_t)kTileStride);
+    const Kind kind = here ? FEW : plan(p.y_f32, M, N, K, near);
+    return p.y_f32 ? run<true>(p, kind, s) : run<false>(p, kind, s);
 }

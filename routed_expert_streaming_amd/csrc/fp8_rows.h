@@ -86,6 +86,77 @@ __device__ __forceinline__ void multiply_rows(int wave, int K, int q, const uint
     }
 }
 
+// ---------------------------------------------------------------- a few rows, quantised here
+// Up to kFewRows rows of unquantised activations that fit LDS whole: the workgroup
+// quantises them itself, while its first weights are on their way, which saves a launch
+// for one token.  Row m: its codes at xs + m * few_row(K), then its scales.
+constexpr int kFewRows = 4;
+__host__ __device__ inline int few_row(int K) {
+    const int blocks = (K + 127) / 128;
+    return blocks * 128 + (blocks + 3) / 4 * 16 + 16;  // (the last 16: other banks for the next row)
+}
+template <int TYPE>
+__device__ __forceinline__ void quantise_few(uint8_t *xs, const uint8_t *x, size_t stride, int rows, int K, int tid,
+                                             int threads) {
+    const int per = (K + 127) / 128 * 16;  // lanes of a row, 16 a block
+    for (int u = tid; u < rows * per; u += threads) {  // threads % 16 == 0: the lanes of a block stay together
+        const int m = u / per, c = u - m * per;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (8 * c < K) load8<TYPE>(x + (size_t)m * stride + (size_t)c * (TYPE == MOE_FP32 ? 32 : 16), v);
+        const float s = fp8_scale(row16_max(top8(v)), false);
+        uint8_t *row = xs + m * few_row(K);
+        *reinterpret_cast<uint2 *>(row + 8 * c) = fp8_codes8<false>(v, s);  // zeros behind K
+        if ((c & 15) == 0) *reinterpret_cast<float *>(row + per * 8 + (c >> 4) * 4) = s;
+    }
+}
+// acc[t] += rows of W x the rows in LDS over the wave's steps; xs: this lane's row.
+// ready(): called once, when the wave's first weights are on their way.
+template <bool WIDE, int NT, int U, int WK, class Ready>
+__device__ __forceinline__ void multiply_few(int wave, int K, int q, const uint8_t *const (&w)[NT],
+                                             const float *const (&ws)[NT], const uint8_t *xs, f32x4 (&acc)[NT],
+                                             Ready ready) {
+    const int blocks = (K + 127) / 128, steps = (blocks + U - 1) / U;
+    struct Weights {
+        Fp8Frag w[NT][U];
+        float s[NT][U];
+    } now, next;
+    auto load = [&](Weights &d, int step) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int b = min(step * U + i, blocks - 1), last = min(8, (K - 128 * b) / 16) - 1;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                d.w[t][i].lo = load_global_u4(w[t] + 128 * b + 16 * min(q, last));
+                d.w[t][i].hi = load_global_u4(w[t] + 128 * b + 16 * min(q + 4, last));
+                d.s[t][i] = ws[t][b];
+            }
+        }
+    };
+    if (wave < steps) load(now, wave);
+    ready();
+    for (int s = wave; s < steps; s += WK) {
+        const bool more = s + WK < steps;
+        if (more) load(next, s + WK);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int b = s * U + i;
+            if (b >= blocks) break;
+            const int pieces = (K - 128 * b) / 16;
+            if (pieces < 8)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) cut_frag(now.w[t][i], q, pieces);
+            const Fp8Frag x{*reinterpret_cast<const uint4 *>(xs + 128 * b + 16 * q),
+                            *reinterpret_cast<const uint4 *>(xs + 128 * b + 16 * q + 64)};
+            const float xs_scale = *reinterpret_cast<const float *>(xs + blocks * 128 + 4 * b);
+            const auto xo = operand<WIDE>(x);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                acc[t] = fma4(mfma_fp8(operand<WIDE>(now.w[t][i]), xo), now.s[t][i] * xs_scale, acc[t]);
+        }
+        if (more) now = next;
+    }
+}
+
 // The waves' sums of tile i -> this wave's registers, in wave order.
 template <int WK, int TILES>
 __device__ __forceinline__ f32x4 joined(const f32x4 (*part)[TILES][64], int i, int lane) {

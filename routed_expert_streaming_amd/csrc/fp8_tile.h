@@ -7,33 +7,44 @@
 // different banks.  The activations' scales come in by four blocks (16 bytes a row), two
 // such chunks in turn; W's scales, one or a few a block for a wave's columns, lie in
 // registers across the lanes, 64 blocks at a time.
+//
+// KW groups of waves may share the outputs and take every KW-th block each, with rings of
+// their own (and an A scale chunk in every stage); their sums are joined through LDS, in
+// order, at the end.  A turn from one block to the next is a chain of latencies, about 0.4
+// us whatever the tile's size, which small tiles cannot fill otherwise.
 #pragma once
 #include "fp8_mma.h"
 #include "tile.h"
 
 namespace moe {
 
-template <int WM_, int WN_, int MT_, int NT_, int SW_, int SA_>
+template <int WM_, int WN_, int MT_, int NT_, int SW_, int SA_, int KW_ = 1>
 struct Fp8Tile {
     static constexpr int WM = WM_, WN = WN_, MT = MT_, NT = NT_;
     static constexpr int SW = SW_, SA = SA_;  // stages of W's rows and of A's
-    static constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, WAVES = WM * WN;
+    static constexpr int KW = KW_, GROUP = WM * WN;  // groups of waves along K, waves of one
+    static constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, WAVES = GROUP * KW;
     static constexpr int W_BYTES = BN * 128, A_BYTES = BM * 128;
     static constexpr int W_LOADS = BN / 8, A_LOADS = BM / 8;  // load instructions of a stage, 1 KB each
-    static constexpr int W_EACH = (W_LOADS + WAVES - 1) / WAVES, A_EACH = (A_LOADS + WAVES - 1) / WAVES;  // by a wave
+    static constexpr int W_EACH = (W_LOADS + GROUP - 1) / GROUP, A_EACH = (A_LOADS + GROUP - 1) / GROUP;  // by a wave
     static constexpr int SCALE_ROWS = BM < 64 ? 64 : BM, CHUNK = SCALE_ROWS * 16;
     static constexpr int SCALE_LOADS = SCALE_ROWS / 64;
-    static constexpr int A_RING = SW * W_BYTES, S_RING = A_RING + SA * A_BYTES, LDS = S_RING + 2 * CHUNK;
-    static_assert(SW >= 2 && SW <= SA && SA <= 4 && SCALE_LOADS <= WAVES && WAVES % 2 == 0 && LDS <= 160 * 1024,
+    static constexpr int CHUNKS = KW == 1 ? 2 : SA;
+    static constexpr int A_RING = SW * W_BYTES, S_RING = A_RING + SA * A_BYTES, RINGS = S_RING + CHUNKS * CHUNK;
+    static constexpr int JOIN = (KW - 1) * GROUP * MT * NT * 1024;  // the sums of the groups but the first
+    static constexpr int LDS = KW * RINGS > JOIN ? KW * RINGS : JOIN;
+    static_assert(SW >= 2 && SW <= SA && SA <= 4 && SCALE_LOADS <= GROUP && GROUP % 2 == 0 && WAVES <= 16 &&
+                      LDS <= 160 * 1024,
                   "tile does not fit its workgroup");
     static_assert(W_LOADS % 2 == 0 && A_LOADS % 2 == 0, "rows of a wave's loads modulo 16");
     static_assert(SA * A_EACH + SW * W_EACH < 64, "vmcnt range");
     // loads of a wave after each column of tiles, so that all are issued within half a block
-    static constexpr int EACH = W_EACH + A_EACH, SPREAD = (EACH + (MT + 1) / 2 - 1) / ((MT + 1) / 2);
-    static constexpr int LAG = MT * NT % 4 == 0 ? 4 : MT * NT % 3 == 0 ? 3 : 2;
+    static constexpr int EACH = W_EACH + A_EACH + (KW > 1 ? 1 : 0), SPREAD = (EACH + (MT + 1) / 2 - 1) / ((MT + 1) / 2);
+    static constexpr int LAG = MT * NT % 4 == 0 ? 4 : MT * NT % 3 == 0 ? 3 : MT * NT % 2 == 0 ? 2 : 1;
 };
 
-// acc[t][u] += rows of W (tile t of this wave) x rows of A (tile u).  w, a, as: uniform
+// acc[t][u] += rows of W (tile t of this wave) x rows of A (tile u); with KW > 1 only the
+// first group's waves have the sums in the end.  w, a, as: uniform
 // bases at column 0; w_off(row), a_off(row), as_off(row): 32-bit byte offsets of the
 // tile's rows (valid for every row of the tile); ws[i]: the scales of the wave's i-th
 // NT / SN tiles, one per block.  On return no load is in flight and all waves are done
@@ -44,9 +55,14 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
                                          f32x4 (&acc)[T::NT][T::MT]) {
     constexpr int SW = T::SW, SA = T::SA, MT = T::MT, NT = T::NT;
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / T::WN, wn = wave % T::WN;
-    const int nb = (K + 127) / 128, pieces = (K - 128 * (nb - 1)) / 16;  // blocks; pieces of the last
-    const uint32_t lds0 = lds_addr(smem);
+    constexpr int KW = T::KW;
+    const int kg = KW == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 6) / T::GROUP;  // this wave's group
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) - kg * T::GROUP, wm = wave / T::WN, wn = wave % T::WN;
+    const int blocks = (K + 127) / 128, pieces = (K - 128 * (blocks - 1)) / 16;  // pieces of the last block
+    const int nb = KW == 1 ? blocks : (blocks + KW - 1) / KW;                     // this group's (the last may be none)
+    auto block_of = [&](int g) __attribute__((always_inline)) { return KW == 1 ? g : min(g * KW + kg, blocks - 1); };
+    uint8_t *const ring = smem + kg * T::RINGS;
+    const uint32_t lds0 = lds_addr(smem) + kg * T::RINGS;
 
     // load instruction c fills KB c of a stage, rows 8c .. 8c + 7; a wave's take rows that
     // are equal modulo 16, so its lanes keep their pieces (where there are fewer loads
@@ -54,8 +70,8 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
     const int piece = (lane & 7) ^ bank_key<8>((8 * wave + (lane >> 3)) & 15);
     const uint32_t cut = 16 * (piece - min(piece, pieces - 1));  // what the last block's lanes step back by
     auto load_number = [&](int j, int loads) __attribute__((always_inline)) {
-        const int c = j * T::WAVES + wave;
-        return c < loads ? c : loads >= T::WAVES ? c - T::WAVES : c % loads;
+        const int c = j * T::GROUP + wave;
+        return c < loads ? c : loads >= T::GROUP ? c - T::GROUP : c % loads;
     };
     uint32_t w_at[T::W_EACH], a_at[T::A_EACH];
 #pragma unroll
@@ -63,28 +79,31 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
 #pragma unroll
     for (int j = 0; j < T::A_EACH; ++j) a_at[j] = a_off(8 * load_number(j, T::A_LOADS) + (lane >> 3)) + 16 * piece;
     auto issue_w = [&](int i, int j) __attribute__((always_inline)) {
-        dma16(w + 128 * (size_t)i, w_at[j] - (i == nb - 1 ? cut : 0u),
+        const int b = block_of(i);
+        dma16(w + 128 * (size_t)b, w_at[j] - (b == blocks - 1 ? cut : 0u),
               lds0 + (uint32_t)(i % SW) * T::W_BYTES + 1024u * load_number(j, T::W_LOADS));
     };
     auto issue_a = [&](int i, int j) __attribute__((always_inline)) {
-        dma16(a + 128 * (size_t)i, a_at[j] - (i == nb - 1 ? cut : 0u),
+        const int b = block_of(i);
+        dma16(a + 128 * (size_t)b, a_at[j] - (b == blocks - 1 ? cut : 0u),
               lds0 + T::A_RING + (uint32_t)(i % SA) * T::A_BYTES + 1024u * load_number(j, T::A_LOADS));
     };
     const int se = wave % T::SCALE_LOADS;  // (several waves bring the same rows)
     const uint32_t s_off = as_off(min(64 * se + lane, T::BM - 1));
-    auto issue_scales = [&](int chunk) __attribute__((always_inline)) {
-        dma16(as + 16 * (size_t)chunk, s_off, lds0 + T::S_RING + (uint32_t)(chunk & 1) * T::CHUNK + 1024u * se);
+    auto issue_scales = [&](int i) __attribute__((always_inline)) {  // of stage i's block and its neighbours
+        const int place = KW == 1 ? i >> 2 & 1 : i % SA;
+        dma16(as + 16 * (size_t)(block_of(i) >> 2), s_off, lds0 + T::S_RING + (uint32_t)place * T::CHUNK + 1024u * se);
     };
     float wsv[SN];  // lane l: the scale of block 64 * (b / 64) + l
     auto load_ws = [&](int b0) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < SN; ++i) {
-            wsv[i] = ws[i][min(b0 + lane, nb - 1)];
+            wsv[i] = ws[i][min(b0 + lane, blocks - 1)];
             asm volatile("" : "+v"(wsv[i]));  // waited for here, not in every block behind the rings' loads
         }
     };
-    const uint8_t *w_lds = smem + (wn * NT * 16 + r) * 128, *x_lds = smem + T::A_RING + (wm * MT * 16 + r) * 128;
-    const uint8_t *s_lds = smem + T::S_RING + (wm * MT * 16 + r) * 16;
+    const uint8_t *w_lds = ring + (wn * NT * 16 + r) * 128, *x_lds = ring + T::A_RING + (wm * MT * 16 + r) * 128;
+    const uint8_t *s_lds = ring + T::S_RING + (wm * MT * 16 + r) * 16;
     const int lo = 16 * (q ^ bank_key<8>(r)), hi = 16 * ((q + 4) ^ bank_key<8>(r));
     auto read = [&](const uint8_t *p) __attribute__((always_inline)) {
         return Fp8Frag{*reinterpret_cast<const uint4 *>(p + lo), *reinterpret_cast<const uint4 *>(p + hi)};
@@ -96,16 +115,18 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
         return read(x_lds + (uint32_t)(g % SA) * T::A_BYTES + u * 2048);
     };
     auto read_s = [&](int g, int u) __attribute__((always_inline)) {
-        return *reinterpret_cast<const float *>(s_lds + (g >> 2 & 1) * T::CHUNK + u * 256 + 4 * (g & 3));
+        const int place = KW == 1 ? g >> 2 & 1 : g % SA;
+        return *reinterpret_cast<const float *>(s_lds + place * T::CHUNK + u * 256 + 4 * (block_of(g) & 3));
     };
 
     // Issue order, which the waits count on: the first scales, W's stages 0 .. SW-1 and A's
     // 0 .. SA-1 by turns, then after the turn from block g to g + 1 W's stage g + SW and A's
     // g + SA (and scales before them).
     load_ws(0);
-    issue_scales(0);
+    if (KW == 1) issue_scales(0);
 #pragma unroll
     for (int i = 0; i < SA; ++i) {
+        if (KW > 1 && i < nb) issue_scales(i);
         if (i < SW && i < nb)
 #pragma unroll
             for (int j = 0; j < T::W_EACH; ++j) issue_w(i, j);
@@ -114,7 +135,7 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
             for (int j = 0; j < T::A_EACH; ++j) issue_a(i, j);
     }
     if (nb >= SA)
-        wait_vm<(SW - 1) * T::W_EACH + (SA - 1) * T::A_EACH>();
+        wait_vm<(SW - 1) * T::W_EACH + (SA - 1) * (T::EACH - T::W_EACH)>();
     else
         wait_vm<0>();
     ring_barrier();
@@ -135,7 +156,7 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
     // g + 1 - SW + SA (itself needed where SA = SW) and what SW - 2 turns issued.
     auto turn = [&](int g) __attribute__((always_inline)) {
         if (g + SA <= nb)
-            wait_vm<(SW - 2) * T::EACH + (SA > SW ? T::A_EACH : 0)>();
+            wait_vm<(SW - 2) * T::EACH + (SA > SW ? T::A_EACH : 0)>();  // (scales come first)
         else
             wait_vm<0>();
         ring_barrier();
@@ -156,25 +177,28 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
     };
     auto block = [&](int g, auto cut_const) __attribute__((always_inline)) {
         constexpr bool CUT = decltype(cut_const)::value != 0;
-        if ((g & 63) == 0 && g) load_ws(g);
+        const int b = block_of(g);
+        if ((b & 63) < KW && g) load_ws(b & ~63);
+        const bool none = KW > 1 && g * KW + kg >= blocks;  // no such block: the last one again, times 0
         float sw[SN];
 #pragma unroll
         for (int i = 0; i < SN; ++i)
-            sw[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsv[i]), g & 63));
+            sw[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsv[i]), b & 63));
+        const int kept = CUT && b == blocks - 1 ? pieces : 8;
         if (CUT) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) cut_frag(wf[t], q, pieces);
+            for (int t = 0; t < NT; ++t) cut_frag(wf[t], q, kept);
         }
         decltype(operand<WIDE>(wf[0])) wo[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) wo[t] = operand<WIDE>(wf[t]);
         static_for<0, MT>([&](auto u_const) __attribute__((always_inline)) {
             constexpr int u = decltype(u_const)::value;
-            if (CUT) cut_frag(xf[u % AHEAD], q, pieces);
+            if (CUT) cut_frag(xf[u % AHEAD], q, kept);
             const auto x = operand<WIDE>(xf[u % AHEAD]);
             float su[SN];
 #pragma unroll
-            for (int i = 0; i < SN; ++i) su[i] = sf[u % AHEAD] * sw[i];
+            for (int i = 0; i < SN; ++i) su[i] = none ? 0.0f : sf[u % AHEAD] * sw[i];
             // the next operands (past the last block whatever the rings hold)
             constexpr int next = u + AHEAD;
             if (next == MT) turn(g);
@@ -194,10 +218,13 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
             constexpr int step = (u + AHEAD) % MT, turned = u + AHEAD < MT ? 1 : 0;
             if constexpr (step * T::SPREAD < T::EACH) {
                 const int from = g - turned;  // the turn's block
-                if (step == 0 && from >= 0 && ((from + SA) & 3) == 0 && from + SA < nb) issue_scales((from + SA) >> 2);
+                if (KW == 1 && step == 0 && from >= 0 && ((from + SA) & 3) == 0 && from + SA < nb) issue_scales(from + SA);
 #pragma unroll
-                for (int j = step * T::SPREAD; j < (step + 1) * T::SPREAD && j < T::EACH; ++j) {
-                    if (j < T::W_EACH) {
+                for (int j0 = step * T::SPREAD; j0 < (step + 1) * T::SPREAD && j0 < T::EACH; ++j0) {
+                    const int j = KW > 1 ? j0 - 1 : j0;  // KW > 1: the scales first
+                    if (j < 0) {
+                        if (from >= 0 && from + SA < nb) issue_scales(from + SA);
+                    } else if (j < T::W_EACH) {
                         if (from >= 0 && from + SW < nb) issue_w(from + SW, j);
                     } else {
                         if (from >= 0 && from + SA < nb) issue_a(from + SA, j - T::W_EACH);
@@ -213,6 +240,20 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
     static_for<NT * MT - LAG, NT * MT>(add);
     wait_vm<0>();
     __syncthreads();
+    if constexpr (KW > 1) {
+        f32x4(*part)[64] = reinterpret_cast<f32x4(*)[64]>(smem);
+        if (kg)
+#pragma unroll
+            for (int i = 0; i < NT * MT; ++i)
+                part[((kg - 1) * T::GROUP + wave) * NT * MT + i][lane] = acc[i / MT][i % MT];
+        __syncthreads();
+        if (!kg)
+#pragma unroll
+            for (int i = 0; i < NT * MT; ++i)
+#pragma unroll
+                for (int k = 1; k < KW; ++k) acc[i / MT][i % MT] += part[((k - 1) * T::GROUP + wave) * NT * MT + i][lane];
+        __syncthreads();
+    }
 }
 
 }  // namespace moe

@@ -22,34 +22,36 @@ __device__ __forceinline__ int bank_key(int r) {
 // 6144 output took 10 us, as whole rows 4.  In as many parts of m as the ring's size
 // asks for.  Kept short: it runs once, from a cold instruction cache.  p: M, N, y and
 // y_stride (their alignment decides the width of the stores) and row(m), where row m lies.
-// STREAM: stores past the caches, for outputs that these do not hold.
+// mine: this wave holds sums (else it only helps to store).  STREAM: stores past the caches, for outputs that these do not hold.
 template <class T, int MT, int NT, typename OUT, bool STREAM = false, class ARGS, typename F32X4>
 __device__ __forceinline__ void store_tile(const ARGS &p, uint8_t *smem, int m0, int n0, int wm, int wn, int lane,
-                                           const F32X4 (&acc)[NT][MT]) {
+                                           const F32X4 (&acc)[NT][MT], bool mine = true) {
     constexpr int PITCH = T::BN * (int)sizeof(OUT) + 16;
     constexpr int FULL = T::BM * PITCH, PARTS = FULL <= T::LDS ? 1 : FULL <= 2 * T::LDS ? 2 : 4;
     static_assert(MT % PARTS == 0 && FULL <= PARTS * T::LDS, "a part of the tile fits the LDS");
     constexpr int PM = MT / PARTS, ROWS = T::BM / PARTS;  // row tiles per wave, rows of a part
     constexpr int PER16 = 16 / (int)sizeof(OUT), UNITS = T::BN / PER16, THREADS = 64 * T::WAVES;
     constexpr int AT_ONCE = ROWS * UNITS % (4 * THREADS) == 0 ? 4 : ROWS * UNITS % (2 * THREADS) == 0 ? 2 : 1;
-    static_assert(ROWS * UNITS % (AT_ONCE * THREADS) == 0, "whole rounds of stores");
+    static_assert(AT_ONCE == 1 || ROWS * UNITS % (AT_ONCE * THREADS) == 0, "whole rounds of stores");
     const int r = lane & 15, q = lane >> 4;
     // 16 bytes at a time where every row begins and ends on such a piece
     const bool wide = ((uintptr_t)p.y | p.y_stride) % 16 == 0 && p.N % PER16 == 0;
 #pragma unroll
     for (int part = 0; part < PARTS; ++part) {
         if (part) __syncthreads();
+        if (mine) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int u = 0; u < PM; ++u) {
-                const F32X4 v = acc[t][part * PM + u];
-                uint8_t *o = smem + ((wm * PM + u) * 16 + r) * PITCH + ((wn * NT + t) * 16 + 4 * q) * (int)sizeof(OUT);
-                if constexpr (sizeof(OUT) == 4)
-                    *reinterpret_cast<F32X4 *>(o) = v;
-                else
-                    *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-            }
+                for (int u = 0; u < PM; ++u) {
+                    const F32X4 v = acc[t][part * PM + u];
+                    uint8_t *o = smem + ((wm * PM + u) * 16 + r) * PITCH + ((wn * NT + t) * 16 + 4 * q) * (int)sizeof(OUT);
+                    if constexpr (sizeof(OUT) == 4)
+                        *reinterpret_cast<F32X4 *>(o) = v;
+                    else
+                        *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                }
+        }
         __syncthreads();
         // row lr of the part: wave row lr / (16 * PM), its tiles part * PM and up
         auto row_of = [&](int lr) { return m0 + lr / (16 * PM) * (16 * MT) + part * 16 * PM + lr % (16 * PM); };

@@ -19,7 +19,10 @@ using moe::f32x4;
 
 constexpr int kMaxE = 1024;
 constexpr int kMaxPairs = 16384;   // of a permutation
-constexpr int kScanPairs = 512;    // up to here a workgroup finds its expert's pairs itself
+// Up to here a workgroup finds its expert's pairs itself and no permutation is built.  Top 8
+// of 128 experts of 4096 x 1536 and a shared one, this way and by tiles: 1 token 62 and 79
+// us, 2 tokens 97 and 94, 4 tokens 165 and 125, 32 tokens 655 and 387.
+constexpr int kScanPairs = 12;
 
 struct ExpertArgs {
     moe::Fp8Act a;  // gate/up: x, a row a token; down: h
@@ -122,38 +125,126 @@ __global__ __launch_bounds__(64 * WK) void fp8_experts_rows_kernel(ExpertArgs p)
 }
 
 // ---------------------------------------------------------------- many tokens
-// The (token, expert) pairs in expert order (a permutation); a workgroup owns 64 rows of
-// one expert and 128 columns of h or 256 of y.  Rows of h: the pairs' places in that
-// order, then T * k + t; so the down projection reads neighbouring rows.
-using Tile = moe::Fp8Tile<2, 4, 2, 4, 3, 3>;
-constexpr int kGroupBits = 11;  // of a tile's number: its expert (E: the shared one); above: its first row / BM
+// The (token, expert) pairs in expert order; a workgroup owns BM rows of one expert and 128
+// columns of h or 256 of y.  Rows of h: the pairs' places in that order, then T * k + t; so
+// the down projection reads neighbouring rows.
+constexpr int kGroupBits = 11;  // of a tile's number: its expert (E: the shared one); above: which of its BM rows
+constexpr int kPrepare = 1024;  // threads of the kernel that comes first
 
-// tiles[0]: how many tiles of BM rows, tiles[1 ..]: each one's expert and rows, expert by
-// expert.  One workgroup of 1024.
-__global__ __launch_bounds__(1024) void fp8_experts_tiles_kernel(const int32_t *__restrict__ count,
-                                                                 const uint8_t *__restrict__ mask, int E, int T,
-                                                                 bool shared, int BM, int32_t *__restrict__ tiles) {
-    __shared__ int sums[16];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const int n = tid < E && (!mask || mask[tid]) ? (count[tid] + BM - 1) / BM : 0;
-    int at = n;  // inclusive sum
+// One launch before the products.  Workgroup 0 sorts the pairs by expert, stable, and lists
+// the tiles of BM rows: offset [E + 1], pair_of_row, tiles[0] how many, tiles[1 ..] each
+// one's expert and place.  Its 16 waves take neighbouring runs of pairs; lanes with the
+// same expert find each other by ballots over the number's bits, so that a pair's place
+// (its expert's offset, plus that expert's pairs of the waves before, plus its rank in its
+// own) needs neither atomics nor a second sort.  Pairs of masked experts have their places
+// but no tiles; pairs with a number outside 0 .. E-1 have none.  16384 pairs take 9 us.
+// The other workgroups quantise x: codes, or (WIDE) the codes' values in bf16, and scales.
+struct PrepareArgs {
+    const uint16_t *x;
+    uint8_t *xq;
+    float *xs;
+    int T, H, E, k, BM;
+    const int32_t *topk_idx;
+    const uint8_t *mask;
+    bool shared;
+    int32_t *offset, *pairs, *tiles;
+};
+
+__device__ __forceinline__ int wave_scan(int v) {  // inclusive sum over the lanes
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(at, o, 64);
-        if (lane >= o) at += u;
+        const int u = __shfl_up(v, o, 64);
+        if ((int)(threadIdx.x & 63) >= o) v += u;
     }
-    if (lane == 63) sums[wave] = at;
+    return v;
+}
+
+__device__ __forceinline__ void sort_pairs(const PrepareArgs &p, uint16_t *count) {  // count: [16][E]
+    __shared__ int sums[2][16];
+    constexpr int kPer = kMaxPairs / 1024;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = p.T * p.k;
+    const int run = (n + 1023) / 1024 * 64;  // pairs of a wave
+    int ex[kPer], rank[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int at = wave * run + 64 * i + lane;
+        ex[i] = 64 * i < run && at < n ? p.topk_idx[at] : -1;
+        if ((unsigned)ex[i] >= (unsigned)p.E) ex[i] = -1;
+    }
+    for (int i = tid; i < 16 * p.E; i += 1024) count[i] = 0;
     __syncthreads();
-    int before = 0, all = 0;
+    uint16_t *mine = count + wave * p.E;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (64 * i < run) {
+            uint64_t same = __ballot(ex[i] >= 0);
+#pragma unroll
+            for (int b = 0; b < 10; ++b) {
+                const uint64_t ones = __ballot(ex[i] >> b & 1);
+                same &= (ex[i] >> b & 1) ? ones : ~ones;
+            }
+            const int below = __popcll(same & ((1ull << lane) - 1));
+            if (ex[i] >= 0) {
+                const int before = mine[ex[i]];  // read by all lanes of the expert before the first of them writes
+                rank[i] = before + below;
+                if (below == 0) mine[ex[i]] = (uint16_t)(before + __popcll(same));
+            }
+        }
+    __syncthreads();
+    // one expert a thread: its pairs, its tiles
+    int pairs = 0;
+    if (tid < p.E)
+        for (int w = 0; w < 16; ++w) {
+            const int c = count[w * p.E + tid];
+            count[w * p.E + tid] = (uint16_t)pairs;
+            pairs += c;
+        }
+    const int tiles = tid < p.E && (!p.mask || p.mask[tid]) ? (pairs + p.BM - 1) / p.BM : 0;
+    const int pair_sum = wave_scan(pairs), tile_sum = wave_scan(tiles);
+    if (lane == 63) sums[0][wave] = pair_sum, sums[1][wave] = tile_sum;
+    __syncthreads();
+    int first = pair_sum - pairs, tile0 = tile_sum - tiles, all = 0;
 #pragma unroll
     for (int w = 0; w < 16; ++w) {
-        if (w < wave) before += sums[w];
-        all += sums[w];
+        if (w < wave) first += sums[0][w], tile0 += sums[1][w];
+        all += sums[1][w];
     }
-    for (int i = 0; i < n; ++i) tiles[1 + before + at - n + i] = tid | i << kGroupBits;
-    const int more = shared ? (T + BM - 1) / BM : 0;
-    for (int i = tid; i < more; i += 1024) tiles[1 + all + i] = E | i << kGroupBits;
-    if (tid == 0) tiles[0] = all + more;
+    if (tid < p.E) p.offset[tid] = first;
+    if (tid == p.E - 1) p.offset[p.E] = first + pairs;
+    for (int i = 0; i < tiles; ++i) p.tiles[1 + tile0 + i] = tid | i << kGroupBits;
+    const int more = p.shared ? (p.T + p.BM - 1) / p.BM : 0;
+    for (int i = tid; i < more; i += 1024) p.tiles[1 + all + i] = p.E | i << kGroupBits;
+    if (tid == 0) p.tiles[0] = all + more;
+    if (tid < p.E) reinterpret_cast<int *>(count + 16 * p.E)[tid] = first;
+    __syncthreads();
+    const int *offset = reinterpret_cast<const int *>(count + 16 * p.E);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (64 * i < run && ex[i] >= 0) p.pairs[offset[ex[i]] + mine[ex[i]] + rank[i]] = wave * run + 64 * i + lane;
+}
+
+template <bool WIDE>
+__global__ __launch_bounds__(kPrepare) void fp8_experts_prepare_kernel(PrepareArgs p) {
+    extern __shared__ uint16_t counts[];
+    if (blockIdx.x == 0) {
+        sort_pairs(p, counts);
+        return;
+    }
+    const int per = 16 * ((p.H + 127) / 128), u = (blockIdx.x - 1) * kPrepare + threadIdx.x;
+    if (u >= p.T * per) return;  // T * per: a multiple of 16
+    const int row = u / per, c = u - row * per;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (8 * c < p.H) moe::load8<MOE_BF16>(reinterpret_cast<const uint8_t *>(p.x + (size_t)row * p.H + 8 * c), v);
+    const float s = moe::fp8_scale(moe::row16_max(moe::top_of(v)), false);
+    const uint2 codes = moe::fp8_codes8<false>(v, s);
+    if (8 * c < p.H) {
+        if constexpr (WIDE)
+            *reinterpret_cast<uint4 *>(p.xq + ((size_t)row * p.H + 8 * c) * 2) =
+                __builtin_bit_cast(uint4, moe::widen8(codes.x, codes.y));
+        else
+            *reinterpret_cast<uint2 *>(p.xq + (size_t)row * p.H + 8 * c) = codes;
+    }
+    if ((c & 15) == 0) p.xs[(size_t)row * (moe::fp8_scale_row(p.H) / 4) + (c >> 4)] = s;
 }
 
 // Rows of y, for store_tile.
@@ -165,9 +256,8 @@ struct YRows {
     __device__ __forceinline__ uint8_t *row(int m) const { return y + (size_t)(pairs ? pairs[m] : m) * y_stride; }
 };
 
-template <bool GATEUP>
-__global__ __launch_bounds__(64 * Tile::WAVES) void fp8_experts_tile_kernel(ExpertArgs p) {
-    using T = Tile;
+template <bool GATEUP, class T>
+__global__ __launch_bounds__(64 * T::WAVES) void fp8_experts_tile_kernel(ExpertArgs p) {
     constexpr int BN = GATEUP ? T::BN / 2 : T::BN, MT = T::MT, NT = T::NT;  // columns of h or y
     __shared__ uint4 smem4[T::LDS / 16];
     uint8_t *smem = reinterpret_cast<uint8_t *>(smem4);
@@ -200,28 +290,30 @@ __global__ __launch_bounds__(64 * Tile::WAVES) void fp8_experts_tile_kernel(Expe
         const moe::Fp8Slab w1 = moe::fp8_slab(slab, H, I, 0), w3 = moe::fp8_slab(slab, H, I, 1);
         const float *const ws[2] = {w1.s + (size_t)(n0 / 128) * w1.s_row, w3.s + (size_t)(n0 / 128) * w3.s_row};
         auto token = [&](int row) { return (uint32_t)(pairs ? pairs[row_of(row)] / p.k : m0 + row_of(row)); };
-        moe::fp8_tile<T, true, 2>(
-            smem, w1.w, p.a.codes, p.a.scales, ws, K,
-            [&](int row) {
-                const int w = row / (16 * NT), t = row / 16 % NT, c = n0 + (w * (NT / 2) + t % (NT / 2)) * 16 + row % 16;
-                return (uint32_t)((t >= NT / 2 ? I : 0) + min(c, I - 1)) * (uint32_t)H;
-            },
-            [&](int row) { return token(row) * (uint32_t)p.a.stride; },
-            [&](int row) { return token(row) * (uint32_t)p.a.scale_stride; }, acc);
+        auto w_off = [&](int row) {
+            const int w = row / (16 * NT), t = row / 16 % NT, c = n0 + (w * (NT / 2) + t % (NT / 2)) * 16 + row % 16;
+            return (uint32_t)((t >= NT / 2 ? I : 0) + min(c, I - 1)) * (uint32_t)H;
+        };
+        auto a_off = [&](int row) { return token(row) * (uint32_t)p.a.stride; };
+        auto s_off = [&](int row) { return token(row) * (uint32_t)p.a.scale_stride; };
+        if constexpr (T::AW)
+            moe::fp8_tile_exact<T, 2>(smem, w1.w, p.a.codes, p.a.scales, ws, K, w_off, a_off, s_off, acc);
+        else
+            moe::fp8_tile<T, true, 2>(smem, w1.w, p.a.codes, p.a.scales, ws, K, w_off, a_off, s_off, acc);
         // h, its largest magnitude per row over the block's columns, its codes
         uint32_t(*tops)[T::WN] = reinterpret_cast<uint32_t(*)[T::WN]>(smem);
         uint8_t *codes = smem + T::BM * T::WN * 4;
-        constexpr int PITCH = BN + 16;
-        static_assert(NT == 4 && BN == 128, "eight of a block's columns a lane");
-        float h[MT][8];
+        constexpr int PITCH = BN + 16, HT = NT / 2;  // a wave's tiles of h
+        static_assert(BN == 128 && NT % 2 == 0, "a workgroup holds whole blocks of h");
+        float h[MT][4 * HT];
 #pragma unroll
         for (int u = 0; u < MT; ++u) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = n0 + (wn * 2 + j / 4) * 16 + 4 * q + j % 4;
-                h[u][j] = c < I ? moe::silu(acc[j / 4][u][j % 4]) * acc[2 + j / 4][u][j % 4] : 0.0f;
+            for (int j = 0; j < 4 * HT; ++j) {
+                const int c = n0 + (wn * HT + j / 4) * 16 + 4 * q + j % 4;
+                h[u][j] = c < I ? moe::silu(acc[j / 4][u][j % 4]) * acc[HT + j / 4][u][j % 4] : 0.0f;
             }
-            uint32_t top = moe::top8(h[u]);
+            uint32_t top = moe::top_of(h[u]);
             top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
             top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
             if (q == 0) tops[(wm * MT + u) * 16 + r][wn] = top;
@@ -230,14 +322,14 @@ __global__ __launch_bounds__(64 * Tile::WAVES) void fp8_experts_tile_kernel(Expe
 #pragma unroll
         for (int u = 0; u < MT; ++u) {
             const int m = (wm * MT + u) * 16 + r;
-            uint32_t top = 0;
+            uint32_t top = 0, c[HT];
 #pragma unroll
             for (int w = 0; w < T::WN; ++w) top = max(top, tops[m][w]);
             const float s = moe::fp8_scale(top, false);
-            const uint2 c = moe::fp8_codes8<false>(h[u], s);
-            uint8_t *o = codes + m * PITCH + wn * 32 + 4 * q;
-            *reinterpret_cast<uint32_t *>(o) = c.x;
-            *reinterpret_cast<uint32_t *>(o + 16) = c.y;
+            moe::fp8_codes<false, HT>(h[u], s, c);
+#pragma unroll
+            for (int t = 0; t < HT; ++t)
+                *reinterpret_cast<uint32_t *>(codes + m * PITCH + (wn * HT + t) * 16 + 4 * q) = c[t];
             if (wn == 0 && q == 0 && m < rows)
                 *reinterpret_cast<float *>(p.out_scales + (size_t)(first + m0 + m) * moe::fp8_scale_row(I) +
                                            4 * (size_t)(n0 / 128)) = s;
@@ -264,9 +356,13 @@ __global__ __launch_bounds__(64 * Tile::WAVES) void fp8_experts_tile_kernel(Expe
 }
 
 struct Space {
-    size_t xq, xs, h, hq, hs, count, offset, pairs, tiles, y, total;
+    size_t xq, xs, h, hq, hs, offset, pairs, tiles, y, total;
 };
 bool few(int T, int k) { return T * k <= kScanPairs; }
+
+// Rows of a tile, by the rows an expert has on average.
+int tile_rows(int T, int E, int k) { return T * k >= 24 * E ? 64 : 16; }
+
 Space layout(int T, int H, int I, int E, int k, bool shared) {
     Space w{};
     const size_t rows = (size_t)T * k + (shared ? (size_t)T : 0);
@@ -276,21 +372,33 @@ Space layout(int T, int H, int I, int E, int k, bool shared) {
         o += moe::align_up(bytes, 256);
         return at;
     };
-    w.xq = take((size_t)T * H);
     w.xs = take((size_t)T * moe::fp8_scale_row(H));
     w.hq = take(rows * I);
     w.hs = take(rows * moe::fp8_scale_row(I));
     if (few(T, k)) {
+        w.xq = take((size_t)T * H);
         w.h = take(rows * I * 4);
     } else {
-        w.count = take((size_t)E * 4);
+        const int BM = tile_rows(T, E, k);
+        w.xq = take((size_t)T * H * (BM == 64 ? 2 : 1));
         w.offset = take((size_t)(E + 1) * 4);
         w.pairs = take((size_t)T * k * 4);
-        w.tiles = take(4 * (1 + rows / Tile::BM + (size_t)E + 1));
+        w.tiles = take(4 * (1 + rows / BM + (size_t)E + 1));
     }
     w.y = take(rows * H * 4);
     w.total = o;
     return w;
+}
+
+template <bool GATEUP, class T>
+int launch_tiles(const ExpertArgs &a, int rows, hipStream_t s) {
+    // at most so many tiles of rows: every expert's last one may be short
+    const int experts = a.E < a.T * a.k ? a.E : a.T * a.k, most = rows / T::BM + experts + 1;
+    const int columns = GATEUP ? (a.I + T::BN / 2 - 1) / (T::BN / 2) : (a.H + T::BN - 1) / T::BN;
+    hipLaunchKernelGGL((fp8_experts_tile_kernel<GATEUP, T>), dim3((unsigned)((most * columns + 7) / 8 * 8)),
+                       dim3(64 * T::WAVES), 0, s, a);
+    MOE_LAUNCH_CHECK("fp8_experts_tile_kernel");
+    return MOE_OK;
 }
 
 int experts(const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_idx, int k,
@@ -304,13 +412,13 @@ int experts(const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_i
     a.table = expert_table;
     a.shared = (const uint8_t *)shared_slab;
     a.mask = expert_mask;
-    int rc = moe::fp8_quant_rows(x, MOE_BF16, (size_t)2 * H, T, H, false, ws + sp.xq, (size_t)H,
-                                 (float *)(ws + sp.xs), moe::fp8_scale_row(H), s);
-    if (rc != MOE_OK) return rc;
-    const moe::Fp8Act xa{ws + sp.xq, ws + sp.xs, (size_t)H, moe::fp8_scale_row(H)};
+    float *xs = (float *)(ws + sp.xs);
     const moe::Fp8Act ha{ws + sp.hq, ws + sp.hs, (size_t)I, moe::fp8_scale_row(I)};
-    a.a = xa;
+    a.a = {ws + sp.xq, ws + sp.xs, (size_t)H, moe::fp8_scale_row(H)};
     if (few(T, k)) {
+        int rc = moe::fp8_quant_rows(x, MOE_BF16, (size_t)2 * H, T, H, false, ws + sp.xq, (size_t)H, xs,
+                                     moe::fp8_scale_row(H), s);
+        if (rc != MOE_OK) return rc;
         const int groups = T * k + (shared ? 1 : 0);
         a.out = ws + sp.h;
         hipLaunchKernelGGL((fp8_experts_rows_kernel<true, 1, 2, 8, 2>), dim3(I / 16, groups), dim3(512), 0, s, a);
@@ -325,28 +433,25 @@ int experts(const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_i
         MOE_LAUNCH_CHECK("fp8_experts_rows_kernel<down>");
         return MOE_OK;
     }
-    int32_t *count = (int32_t *)(ws + sp.count), *offset = (int32_t *)(ws + sp.offset);
-    int32_t *pairs = (int32_t *)(ws + sp.pairs), *tiles = (int32_t *)(ws + sp.tiles);
-    rc = moe::permute_launch(topk_idx, T, k, E, count, offset, pairs, s);
-    if (rc != MOE_OK) return rc;
-    hipLaunchKernelGGL(fp8_experts_tiles_kernel, dim3(1), dim3(1024), 0, s, count, expert_mask, E, T, shared, Tile::BM,
-                       tiles);
-    MOE_LAUNCH_CHECK("fp8_experts_tiles_kernel");
-    a.offset = offset, a.pair_of_row = pairs, a.tiles = tiles;
-    // at most so many tiles of rows: every expert's last one may be short
-    const int most = rows / Tile::BM + (E < T * k ? E : T * k) + 1;
-    auto grid = [&](int n) { return dim3((unsigned)((most * n + 7) / 8 * 8)); };
+    const int BM = tile_rows(T, E, k);
+    PrepareArgs pa{x, ws + sp.xq, xs, T, H, E, k, BM, topk_idx, expert_mask, shared, (int32_t *)(ws + sp.offset),
+                   (int32_t *)(ws + sp.pairs), (int32_t *)(ws + sp.tiles)};
+    const unsigned blocks = 1 + (unsigned)(((size_t)T * 16 * moe::fp8_blocks(H) + kPrepare - 1) / kPrepare);
+    const size_t lds = (size_t)E * (16 * sizeof(uint16_t) + sizeof(int));
+    auto *prepare = BM == 64 ? fp8_experts_prepare_kernel<true> : fp8_experts_prepare_kernel<false>;
+    hipLaunchKernelGGL(prepare, dim3(blocks), dim3(kPrepare), lds, s, pa);
+    MOE_LAUNCH_CHECK("fp8_experts_prepare_kernel");
+    a.offset = pa.offset, a.pair_of_row = pa.pairs, a.tiles = pa.tiles;
     a.out = ws + sp.hq;
     a.out_scales = ws + sp.hs;
-    hipLaunchKernelGGL(fp8_experts_tile_kernel<true>, grid((I + Tile::BN / 2 - 1) / (Tile::BN / 2)),
-                       dim3(64 * Tile::WAVES), 0, s, a);
-    MOE_LAUNCH_CHECK("fp8_experts_tile_kernel<gate/up>");
+    if (BM == 64) a.a.stride = (size_t)2 * H;  // bf16
+    int rc = BM == 64 ? launch_tiles<true, moe::Fp8Tile<1, 8, 4, 2, 3, 3, 1, true>>(a, rows, s)
+                      : launch_tiles<true, moe::Fp8Tile<1, 8, 1, 2, 2, 2>>(a, rows, s);
+    if (rc != MOE_OK) return rc;
     a.a = ha;
     a.out = (uint8_t *)y;
-    hipLaunchKernelGGL(fp8_experts_tile_kernel<false>, grid((H + Tile::BN - 1) / Tile::BN), dim3(64 * Tile::WAVES), 0,
-                       s, a);
-    MOE_LAUNCH_CHECK("fp8_experts_tile_kernel<down>");
-    return MOE_OK;
+    return BM == 64 ? launch_tiles<false, moe::Fp8Tile<2, 4, 2, 4, 3, 3>>(a, rows, s)
+                    : launch_tiles<false, moe::Fp8Tile<1, 8, 1, 2, 2, 2>>(a, rows, s);
 }
 
 int check(const char *who, const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_idx, int k,

@@ -52,19 +52,29 @@ __device__ __forceinline__ uint32_t fp8_codes4(const float (&x)[4], float s, flo
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], c, true);
 }
 
-// Eight values of this lane -> eight codes, by the block's scale (NaN: codes 0).
-template <bool POW2>
-__device__ __forceinline__ uint2 fp8_codes8(const float (&x)[8], float s) {
-    float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
-    float t = s;
+// 4 W values of this lane -> as many codes, by the block's scale (NaN: codes 0).
+template <bool POW2, int W>
+__device__ __forceinline__ void fp8_codes(const float (&x)[4 * W], float s, uint32_t (&c)[W]) {
+    float t = s, up = 1.0f;
     if (!POW2 && s < 0x1p-60f) {  // keep the quotient's remainder above fp32's smallest number
-        t = s * 0x1p64f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] *= 0x1p64f, b[j] *= 0x1p64f;
+        up = 0x1p64f;
+        t = s * up;
     }
     const float inv = 1.0f / t;
-    const uint2 c = make_uint2(fp8_codes4<POW2>(a, t, inv), fp8_codes4<POW2>(b, t, inv));
-    return s == s ? c : make_uint2(0u, 0u);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        float a[4] = {x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+        if (!POW2 && up != 1.0f)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[j] *= up;
+        c[i] = s == s ? fp8_codes4<POW2>(a, t, inv) : 0u;
+    }
+}
+template <bool POW2>
+__device__ __forceinline__ uint2 fp8_codes8(const float (&x)[8], float s) {
+    uint32_t c[2];
+    fp8_codes<POW2, 2>(x, s, c);
+    return make_uint2(c[0], c[1]);
 }
 
 // Largest of a value over the 16 lanes of a row of lanes (16i .. 16i + 15).
@@ -95,10 +105,11 @@ __device__ __forceinline__ void load8(const uint8_t *p, float (&v)[8]) {
     }
 }
 
-__device__ __forceinline__ uint32_t top8(const float (&v)[8]) {
+template <int N>
+__device__ __forceinline__ uint32_t top_of(const float (&v)[N]) {
     uint32_t t = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t = max(t, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < N; ++j) t = max(t, __float_as_uint(v[j]) & 0x7FFFFFFFu);
     return t;
 }
 

@@ -22,7 +22,7 @@ __global__ __launch_bounds__(kThreads) void fp8_quant_rows_kernel(const uint8_t 
     const bool in = 8 * (int)c < K;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (in) moe::load8<TYPE>(x + row * x_stride + (size_t)c * (TYPE == MOE_FP32 ? 32 : 16), v);
-    const float s = moe::fp8_scale(moe::row16_max(moe::top8(v)), POW2);
+    const float s = moe::fp8_scale(moe::row16_max(moe::top_of(v)), POW2);
     if (in) *reinterpret_cast<uint2 *>(codes + row * codes_stride + 8 * (size_t)c) = moe::fp8_codes8<POW2>(v, s);
     if ((c & 15) == 0) *reinterpret_cast<float *>(scales + row * scales_stride + 4 * (size_t)(c >> 4)) = s;
 }
@@ -48,7 +48,7 @@ __global__ __launch_bounds__(kThreads) void fp8_quant_blocks_kernel(const uint8_
             moe::load8<TYPE>(x + (size_t)r * x_stride + (size_t)c * (TYPE == MOE_FP32 ? 4 : 2), v[i]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, moe::top8(v[i]));
+    for (int i = 0; i < 8; ++i) top = max(top, moe::top_of(v[i]));
     top = moe::row16_max(top);
     top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
     top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));

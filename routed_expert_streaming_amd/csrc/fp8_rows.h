@@ -103,7 +103,7 @@ __device__ __forceinline__ void quantise_few(uint8_t *xs, const uint8_t *x, size
         const int m = u / per, c = u - m * per;
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (8 * c < K) load8<TYPE>(x + (size_t)m * stride + (size_t)c * (TYPE == MOE_FP32 ? 32 : 16), v);
-        const float s = fp8_scale(row16_max(top8(v)), false);
+        const float s = fp8_scale(row16_max(top_of(v)), false);
         uint8_t *row = xs + m * few_row(K);
         *reinterpret_cast<uint2 *>(row + 8 * c) = fp8_codes8<false>(v, s);  // zeros behind K
         if ((c & 15) == 0) *reinterpret_cast<float *>(row + per * 8 + (c >> 4) * 4) = s;

@@ -7,10 +7,10 @@
 // ones as their rounding to bf16 leaves them.  y has nothing behind it but that rounding
 // and takes the FP8 cores.
 #include "common.h"
-#include "ffn.h"
 #include "fp8_mma.h"
 #include "fp8_quant.h"
 #include "fp8_rows.h"
+#include "fp8_tall.h"
 #include "fp8_tile.h"
 
 namespace {
@@ -256,26 +256,20 @@ struct YRows {
     __device__ __forceinline__ uint8_t *row(int m) const { return y + (size_t)(pairs ? pairs[m] : m) * y_stride; }
 };
 
+// One tile: rows rows of an expert from its m0-th on x columns n0 and up.
+struct TileOf {
+    const uint8_t *slab;
+    const int32_t *pairs;  // of these rows; NULL: tokens m0 and up
+    int first, m0, n0, rows;
+    bool shared;
+};
 template <bool GATEUP, class T>
-__global__ __launch_bounds__(64 * T::WAVES) void fp8_experts_tile_kernel(ExpertArgs p) {
+__device__ __forceinline__ void experts_tile(const ExpertArgs &p, const TileOf &at, uint8_t *smem) {
     constexpr int BN = GATEUP ? T::BN / 2 : T::BN, MT = T::MT, NT = T::NT;  // columns of h or y
-    __shared__ uint4 smem4[T::LDS / 16];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(smem4);
-    const int H = p.H, I = p.I, P = p.T * p.k, K = GATEUP ? H : I, N = GATEUP ? I : H;
-    // Each XCD takes a run of neighbouring tiles, an expert's rows fastest: the tiles that
-    // share rows of W start together and read them from its L2.  (With the columns fastest
-    // they drifted apart: 2.9 GB came from memory for 1.6 GB of W1 and W3.)
-    const int n_tiles = (N + BN - 1) / BN, tiles = p.tiles[0] * n_tiles, per = (tiles + 7) / 8;
-    const int i = blockIdx.x >> 3, tile = (blockIdx.x & 7) * per + i;
-    if (i >= per || tile >= tiles) return;
-    const int number = p.tiles[1 + tile / n_tiles], e = number & ((1 << kGroupBits) - 1);
-    const bool shared = e == p.E;
-    const int first = shared ? P : p.offset[e], all = shared ? p.T : p.offset[e + 1] - first;  // rows
-    const int m_tiles = (all + T::BM - 1) / T::BM;
-    const int local = tile - (tile / n_tiles - (number >> kGroupBits)) * n_tiles;  // of the expert's tiles
-    const int m0 = local % m_tiles * T::BM, n0 = local / m_tiles * BN, rows = all - m0;  // rows from m0 on
-    const int32_t *pairs = shared ? nullptr : p.pair_of_row + first + m0;
-    const uint8_t *slab = shared ? p.shared : (const uint8_t *)p.table[e];
+    const int H = p.H, I = p.I, P = p.T * p.k, K = GATEUP ? H : I;
+    const int first = at.first, m0 = at.m0, n0 = at.n0, rows = at.rows;
+    const uint8_t *const slab = at.slab;
+    const int32_t *const pairs = at.pairs;
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / T::WN, wn = wave % T::WN;
 
@@ -296,8 +290,8 @@ __global__ __launch_bounds__(64 * T::WAVES) void fp8_experts_tile_kernel(ExpertA
         };
         auto a_off = [&](int row) { return token(row) * (uint32_t)p.a.stride; };
         auto s_off = [&](int row) { return token(row) * (uint32_t)p.a.scale_stride; };
-        if constexpr (T::AW)
-            moe::fp8_tile_exact<T, 2>(smem, w1.w, p.a.codes, p.a.scales, ws, K, w_off, a_off, s_off, acc);
+        if constexpr (T::TALL)
+            moe::fp8_tall<T, 2>(smem, w1.w, p.a.codes, p.a.scales, ws, K, w_off, a_off, s_off, acc);
         else
             moe::fp8_tile<T, true, 2>(smem, w1.w, p.a.codes, p.a.scales, ws, K, w_off, a_off, s_off, acc);
         // h, its largest magnitude per row over the block's columns, its codes
@@ -344,14 +338,55 @@ __global__ __launch_bounds__(64 * T::WAVES) void fp8_experts_tile_kernel(ExpertA
     } else {
         const moe::Fp8Slab w2 = moe::fp8_slab(slab, H, I, 2);
         const float *const ws[1] = {w2.s + (size_t)(min(n0 + wn * NT * 16, H - 1) / 128) * w2.s_row};
-        moe::fp8_tile<T, false, 1>(
-            smem, w2.w + (size_t)n0 * I, p.a.codes + (size_t)(first + m0) * p.a.stride,
-            p.a.scales + (size_t)(first + m0) * p.a.scale_stride, ws, K,
-            [&](int row) { return (uint32_t)min(row, H - 1 - n0) * (uint32_t)I; },
-            [&](int row) { return (uint32_t)row_of(row) * (uint32_t)p.a.stride; },
-            [&](int row) { return (uint32_t)row_of(row) * (uint32_t)p.a.scale_stride; }, acc);
-        const YRows y{min(rows, T::BM), H, p.out + (shared ? (size_t)(P + m0) * H * 4 : 0), (size_t)H * 4, pairs};
+        const uint8_t *w = w2.w + (size_t)n0 * I, *h = p.a.codes + (size_t)(first + m0) * p.a.stride,
+                      *hs = p.a.scales + (size_t)(first + m0) * p.a.scale_stride;
+        auto w_off = [&](int row) { return (uint32_t)min(row, H - 1 - n0) * (uint32_t)I; };
+        auto a_off = [&](int row) { return (uint32_t)row_of(row) * (uint32_t)p.a.stride; };
+        auto s_off = [&](int row) { return (uint32_t)row_of(row) * (uint32_t)p.a.scale_stride; };
+        if constexpr (T::TALL)
+            moe::fp8_tall<T, 1>(smem, w, h, hs, ws, K, w_off, a_off, s_off, acc);
+        else
+            moe::fp8_tile<T, false, 1>(smem, w, h, hs, ws, K, w_off, a_off, s_off, acc);
+        const YRows y{rows, H, p.out + (at.shared ? (size_t)(P + m0) * H * 4 : 0), (size_t)H * 4, pairs};
         moe::store_tile<T, MT, NT, float, true>(y, smem, 0, n0, wm, wn, lane, acc);
+    }
+}
+
+// T: the tile, the tallest one of the heights where several are listed.
+template <bool GATEUP, class T>
+__global__ __launch_bounds__(64 * T::WAVES, T::TALL ? 2 : 1) void fp8_experts_tile_kernel(ExpertArgs p) {
+    constexpr int BN = GATEUP ? T::BN / 2 : T::BN;
+    __shared__ uint4 smem4[T::LDS / 16];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(smem4);
+    // Each XCD takes a run of neighbouring tiles, an expert's rows fastest: the tiles that
+    // share rows of W start together and read them from its L2.  (With the columns fastest
+    // they drifted apart: 2.9 GB came from memory for 1.6 GB of W1 and W3.)
+    const int N = GATEUP ? p.I : p.H;
+    const int n_tiles = (N + BN - 1) / BN, tiles = p.tiles[0] * n_tiles, per = (tiles + 7) / 8;
+    const int i = blockIdx.x >> 3, tile = (blockIdx.x & 7) * per + i;
+    if (i >= per || tile >= tiles) return;
+    const int number = p.tiles[1 + tile / n_tiles], e = number & ((1 << kGroupBits) - 1);
+    TileOf at;
+    at.shared = e == p.E;
+    at.first = at.shared ? p.T * p.k : p.offset[e];
+    const int all = at.shared ? p.T : p.offset[e + 1] - at.first;  // rows
+    const int m_tiles = (all + T::BM - 1) / T::BM;
+    const int height = 16 * (((all + 15) / 16 + m_tiles - 1) / m_tiles);  // alike; with none left empty
+    const int local = tile - (tile / n_tiles - (number >> kGroupBits)) * n_tiles;  // of the expert's tiles
+    at.m0 = local % m_tiles * height, at.n0 = local / m_tiles * BN, at.rows = min(height, all - at.m0);
+    at.pairs = at.shared ? nullptr : p.pair_of_row + at.first + at.m0;
+    at.slab = at.shared ? p.shared : (const uint8_t *)p.table[e];
+    if constexpr (T::TALL) {
+        if (T::MT > 8 && at.rows > 128)
+            experts_tile<GATEUP, moe::Fp8Tall<T::WN, (T::MT > 8 ? 10 : 4), T::EXACT>>(p, at, smem);
+        else if (T::MT > 6 && at.rows > 96)
+            experts_tile<GATEUP, moe::Fp8Tall<T::WN, (T::MT > 6 ? 8 : 4), T::EXACT>>(p, at, smem);
+        else if (T::MT > 4 && at.rows > 64)
+            experts_tile<GATEUP, moe::Fp8Tall<T::WN, (T::MT > 4 ? 6 : 4), T::EXACT>>(p, at, smem);
+        else
+            experts_tile<GATEUP, moe::Fp8Tall<T::WN, 4, T::EXACT>>(p, at, smem);
+    } else {
+        experts_tile<GATEUP, T>(p, at, smem);
     }
 }
 
@@ -361,7 +396,7 @@ struct Space {
 bool few(int T, int k) { return T * k <= kScanPairs; }
 
 // Rows of a tile, by the rows an expert has on average.
-int tile_rows(int T, int E, int k) { return T * k >= 24 * E ? 64 : 16; }
+int tile_rows(int T, int E, int k) { return T * k >= 64 * E ? 160 : T * k >= 24 * E ? 64 : 16; }
 
 Space layout(int T, int H, int I, int E, int k, bool shared) {
     Space w{};
@@ -380,7 +415,7 @@ Space layout(int T, int H, int I, int E, int k, bool shared) {
         w.h = take(rows * I * 4);
     } else {
         const int BM = tile_rows(T, E, k);
-        w.xq = take((size_t)T * H * (BM == 64 ? 2 : 1));
+        w.xq = take((size_t)T * H * (BM > 16 ? 2 : 1));
         w.offset = take((size_t)(E + 1) * 4);
         w.pairs = take((size_t)T * k * 4);
         w.tiles = take(4 * (1 + rows / BM + (size_t)E + 1));
@@ -438,20 +473,22 @@ int experts(const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_i
                    (int32_t *)(ws + sp.pairs), (int32_t *)(ws + sp.tiles)};
     const unsigned blocks = 1 + (unsigned)(((size_t)T * 16 * moe::fp8_blocks(H) + kPrepare - 1) / kPrepare);
     const size_t lds = (size_t)E * (16 * sizeof(uint16_t) + sizeof(int));
-    auto *prepare = BM == 64 ? fp8_experts_prepare_kernel<true> : fp8_experts_prepare_kernel<false>;
+    auto *prepare = BM > 16 ? fp8_experts_prepare_kernel<true> : fp8_experts_prepare_kernel<false>;
     hipLaunchKernelGGL(prepare, dim3(blocks), dim3(kPrepare), lds, s, pa);
     MOE_LAUNCH_CHECK("fp8_experts_prepare_kernel");
     a.offset = pa.offset, a.pair_of_row = pa.pairs, a.tiles = pa.tiles;
     a.out = ws + sp.hq;
     a.out_scales = ws + sp.hs;
-    if (BM == 64) a.a.stride = (size_t)2 * H;  // bf16
-    int rc = BM == 64 ? launch_tiles<true, moe::Fp8Tile<1, 8, 4, 2, 3, 3, 1, true>>(a, rows, s)
-                      : launch_tiles<true, moe::Fp8Tile<1, 8, 1, 2, 2, 2>>(a, rows, s);
+    if (BM > 16) a.a.stride = (size_t)2 * H;  // bf16
+    int rc = BM == 160  ? launch_tiles<true, moe::Fp8Tall<8, 10, true>>(a, rows, s)
+             : BM == 64 ? launch_tiles<true, moe::Fp8Tall<8, 4, true>>(a, rows, s)
+                        : launch_tiles<true, moe::Fp8Tile<1, 8, 1, 2, 2, 2>>(a, rows, s);
     if (rc != MOE_OK) return rc;
     a.a = ha;
     a.out = (uint8_t *)y;
-    return BM == 64 ? launch_tiles<false, moe::Fp8Tile<2, 4, 2, 4, 3, 3>>(a, rows, s)
-                    : launch_tiles<false, moe::Fp8Tile<1, 8, 1, 2, 2, 2>>(a, rows, s);
+    return BM == 160  ? launch_tiles<false, moe::Fp8Tall<4, 10, false>>(a, rows, s)
+           : BM == 64 ? launch_tiles<false, moe::Fp8Tall<4, 4, false>>(a, rows, s)
+                      : launch_tiles<false, moe::Fp8Tile<1, 8, 1, 2, 2, 2>>(a, rows, s);
 }
 
 int check(const char *who, const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_idx, int k,

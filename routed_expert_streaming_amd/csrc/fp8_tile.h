@@ -18,16 +18,15 @@
 
 namespace moe {
 
-template <int WM_, int WN_, int MT_, int NT_, int SW_, int SA_, int KW_ = 1, bool AW_ = false>
+template <int WM_, int WN_, int MT_, int NT_, int SW_, int SA_, int KW_ = 1>
 struct Fp8Tile {
     static constexpr int WM = WM_, WN = WN_, MT = MT_, NT = NT_;
+    static constexpr bool TALL = false;
     static constexpr int SW = SW_, SA = SA_;  // stages of W's rows and of A's
     static constexpr int KW = KW_, GROUP = WM * WN;  // groups of waves along K, waves of one
     static constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, WAVES = GROUP * KW;
-    static constexpr bool AW = AW_;
-    static constexpr int A_ROW = AW ? 256 : 128, A_PIECES = A_ROW / 16;
-    static constexpr int W_BYTES = BN * 128, A_BYTES = BM * A_ROW;
-    static constexpr int W_LOADS = BN / 8, A_LOADS = A_BYTES / 1024;  // load instructions of a stage, 1 KB each
+    static constexpr int W_BYTES = BN * 128, A_BYTES = BM * 128;
+    static constexpr int W_LOADS = BN / 8, A_LOADS = BM / 8;  // load instructions of a stage, 1 KB each
     static constexpr int W_EACH = (W_LOADS + GROUP - 1) / GROUP, A_EACH = (A_LOADS + GROUP - 1) / GROUP;  // by a wave
     static constexpr int SCALE_ROWS = BM < 64 ? 64 : BM, CHUNK = SCALE_ROWS * 16;
     static constexpr int SCALE_LOADS = SCALE_ROWS / 64;
@@ -38,8 +37,6 @@ struct Fp8Tile {
     static_assert(SW >= 2 && SW <= SA && SA <= 4 && SCALE_LOADS <= GROUP && GROUP % 2 == 0 && WAVES <= 16 &&
                       LDS <= 160 * 1024,
                   "tile does not fit its workgroup");
-    static_assert(W_LOADS % 2 == 0 && A_LOADS % (AW ? 4 : 2) == 0 && GROUP % (AW ? 4 : 2) == 0,
-                  "rows of a wave's loads modulo 16");
     static_assert(SA * A_EACH + SW * W_EACH < 64, "vmcnt range");
     // loads of a wave after each column of tiles, so that all are issued within half a block
     static constexpr int EACH = W_EACH + A_EACH + (KW > 1 ? 1 : 0), SPREAD = (EACH + (MT + 1) / 2 - 1) / ((MT + 1) / 2);
@@ -146,7 +143,6 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
     // eight waves' reads in turn took longer than a column's products.
     constexpr int AHEAD = MT >= 4 ? 2 : 1;
     static_assert(MT % AHEAD == 0, "an operand's place");
-    static_assert(!T::AW, "codes");
     Fp8Frag wf[NT], xf[AHEAD];
     float sf[AHEAD];
 #pragma unroll
@@ -258,200 +254,6 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
                 for (int k = 1; k < KW; ++k) acc[i / MT][i % MT] += part[((k - 1) * T::GROUP + wave) * NT * MT + i][lane];
         __syncthreads();
     }
-}
-
-// The same for exact products (T::AW): a holds the codes' values in bf16, 256 bytes a
-// block, and the wave's own 16 NT rows of W are converted once, by it alone (WM = 1).
-// Products and the other instructions are mixed finely, because a wave issues in order and
-// two waves a SIMD do not fill each other's gaps: between two matrix products stand an
-// addition to the sums, and for half of a block the conversion of the next block's W.  So
-// W is read from LDS one block ahead: the turn from block g to g + 1 needs its stage g + 2.
-// (Converted when needed, in one go, and with each product's four parts in a chain, a block
-// of 64 x 256 took 1.55 us.)
-template <class T, int SN, class WOff, class AOff, class SOff>
-__device__ __forceinline__ void fp8_tile_exact(uint8_t *smem, const uint8_t *w, const uint8_t *a, const uint8_t *as,
-                                               const float *const (&ws)[SN], int K, WOff w_off, AOff a_off,
-                                               SOff as_off, f32x4 (&acc)[T::NT][T::MT]) {
-    constexpr int S = T::SW, MT = T::MT, NT = T::NT;
-    static_assert(T::AW && T::WM == 1 && T::KW == 1 && T::SW == 3 && T::SA == 3 && MT == 4 && SN == NT, "the shape below");
-    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int nb = (K + 127) / 128, pieces = (K - 128 * (nb - 1)) / 16;  // blocks; pieces of the last (of codes)
-    const uint32_t lds0 = lds_addr(smem);
-    static_assert(T::W_LOADS % T::GROUP == 0 && T::A_LOADS % T::GROUP == 0, "whole loads a wave");
-
-    const int piece = (lane & 7) ^ bank_key<8>((8 * wave + (lane >> 3)) & 15);
-    const int piece_a = (lane & 15) ^ bank_key<16>((4 * wave + (lane >> 4)) & 15);
-    const uint32_t cut = 16 * (piece - min(piece, pieces - 1)), cut_a = 16 * (piece_a - min(piece_a, 2 * pieces - 1));
-    uint32_t w_at[T::W_EACH], a_at[T::A_EACH];
-#pragma unroll
-    for (int j = 0; j < T::W_EACH; ++j) w_at[j] = w_off(8 * (j * T::GROUP + wave) + (lane >> 3)) + 16 * piece;
-#pragma unroll
-    for (int j = 0; j < T::A_EACH; ++j) a_at[j] = a_off(4 * (j * T::GROUP + wave) + (lane >> 4)) + 16 * piece_a;
-    auto issue_w = [&](int i, int j) __attribute__((always_inline)) {
-        dma16(w + 128 * (size_t)i, w_at[j] - (i == nb - 1 ? cut : 0u),
-              lds0 + (uint32_t)(i % S) * T::W_BYTES + 1024u * (j * T::GROUP + wave));
-    };
-    auto issue_a = [&](int i, int j) __attribute__((always_inline)) {
-        dma16(a + 256 * (size_t)i, a_at[j] - (i == nb - 1 ? cut_a : 0u),
-              lds0 + T::A_RING + (uint32_t)(i % S) * T::A_BYTES + 1024u * (j * T::GROUP + wave));
-    };
-    const int se = wave % T::SCALE_LOADS;
-    const uint32_t s_off = as_off(min(64 * se + lane, T::BM - 1));
-    auto issue_scales = [&](int i) __attribute__((always_inline)) {  // of stage i's block and the next three
-        dma16(as + 16 * (size_t)(i >> 2), s_off, lds0 + T::S_RING + (uint32_t)(i >> 2 & 1) * T::CHUNK + 1024u * se);
-    };
-    float wsv[SN];  // lane l: the scale of block 64 * (b / 64) + l
-    auto load_ws = [&](int b0) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < SN; ++i) {
-            wsv[i] = ws[i][min(b0 + lane, nb - 1)];
-            asm volatile("" : "+v"(wsv[i]));
-        }
-    };
-    const uint8_t *w_lds = smem + (wave * NT * 16 + r) * 128, *x_lds = smem + T::A_RING + r * 256;
-    const uint8_t *s_lds = smem + T::S_RING + r * 16;
-    const int lo = 16 * (q ^ bank_key<8>(r)), hi = 16 * ((q + 4) ^ bank_key<8>(r));
-    int x_piece[4];  // the columns of codes' pieces q and q + 4: pieces 2q, 2q + 1 and 8 further
-#pragma unroll
-    for (int s = 0; s < 4; ++s) x_piece[s] = 16 * ((2 * q + (s & 1) + 8 * (s >> 1)) ^ bank_key<16>(r));
-    auto read_w = [&](int g, int t) __attribute__((always_inline)) {
-        const uint8_t *p = w_lds + (uint32_t)(g % S) * T::W_BYTES + t * 2048;
-        return Fp8Frag{*reinterpret_cast<const uint4 *>(p + lo), *reinterpret_cast<const uint4 *>(p + hi)};
-    };
-    auto read_x = [&](int g, int u) __attribute__((always_inline)) {
-        const uint8_t *p = x_lds + (uint32_t)(g % S) * T::A_BYTES + u * 4096;
-        WideFrag f;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) f.v[s] = *reinterpret_cast<const bf16x8 *>(p + x_piece[s]);
-        return f;
-    };
-    auto read_s = [&](int g, int u) __attribute__((always_inline)) {
-        return *reinterpret_cast<const float *>(s_lds + (g >> 2 & 1) * T::CHUNK + u * 256 + 4 * (g & 3));
-    };
-    // part s of a row's codes in bf16
-    auto widen_part = [&](const Fp8Frag &f, int s) __attribute__((always_inline)) {
-        return s == 0   ? widen8(f.lo.x, f.lo.y)
-               : s == 1 ? widen8(f.lo.z, f.lo.w)
-               : s == 2 ? widen8(f.hi.x, f.hi.y)
-                        : widen8(f.hi.z, f.hi.w);
-    };
-
-    // Issue order: the first scales, W's and A's stages 0 .. 2 by turns, W's 3, then after the
-    // turn from block g [scales] W's g + 4 and A's g + 3.
-    load_ws(0);
-    issue_scales(0);
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-        if (i < nb) {
-#pragma unroll
-            for (int j = 0; j < T::W_EACH; ++j) issue_w(i, j);
-#pragma unroll
-            for (int j = 0; j < T::A_EACH; ++j) issue_a(i, j);
-        }
-    if (nb >= S)
-        wait_vm<2 * T::W_EACH + 3 * T::A_EACH>();
-    else
-        wait_vm<0>();
-    ring_barrier();
-    Fp8Frag raw[NT];
-    WideFrag wide[2][NT];  // block g's W in [g & 1]
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        raw[t] = read_w(0, t);
-        if (nb == 1) cut_frag(raw[t], q, pieces);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) wide[0][t].v[s] = widen_part(raw[t], s);
-    }
-    ring_barrier();  // every wave has read W's stage 0
-    if (S < nb)
-#pragma unroll
-        for (int j = 0; j < T::W_EACH; ++j) issue_w(S, j);
-    if (S < nb)
-        wait_vm<2 * T::EACH>();
-    else
-        wait_vm<0>();
-    ring_barrier();
-#pragma unroll
-    for (int t = 0; t < NT; ++t) raw[t] = read_w(1, t);
-    WideFrag xf[2] = {read_x(0, 0), read_x(0, 1)};
-    float sf[2] = {read_s(0, 0), read_s(0, 1)};
-
-    f32x4 done[NT];  // the last column of tiles' products, still to be added
-    float done_s[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) done[t] = f32x4{0.f, 0.f, 0.f, 0.f}, done_s[t] = 0.0f;
-    auto block = [&](int g, auto p_const) __attribute__((always_inline)) {
-        constexpr int P = decltype(p_const)::value;
-        if ((g & 63) == 0 && g) load_ws(g);
-        float sw[SN];
-#pragma unroll
-        for (int i = 0; i < SN; ++i)
-            sw[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsv[i]), g & 63));
-        if (pieces < 8 && g + 1 == nb - 1)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) cut_frag(raw[t], q, pieces);
-        static_for<0, MT>([&](auto u_const) __attribute__((always_inline)) {
-            constexpr int u = decltype(u_const)::value;
-            if (pieces < 8 && g == nb - 1) cut_frag(xf[u & 1], q, pieces);
-            const WideFrag x = xf[u & 1];
-            float su[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) su[t] = sf[u & 1] * sw[t];
-            // the next operands (past the last block whatever the rings hold)
-            if (u == 2) {
-                if (g + S < nb)
-                    wait_vm<T::EACH>();
-                else
-                    wait_vm<0>();
-                ring_barrier();
-#pragma unroll
-                for (int t = 0; t < NT; ++t) raw[t] = read_w(g + 2, t);
-            }
-            xf[u & 1] = u < 2 ? read_x(g, u + 2) : read_x(g + 1, u - 2);
-            sf[u & 1] = u < 2 ? read_s(g, u + 2) : read_s(g + 1, u - 2);
-            f32x4 v[NT];
-            static_for<0, 4 * NT>([&](auto i_const) __attribute__((always_inline)) {
-                constexpr int i = decltype(i_const)::value, t = i % NT, s = i / NT;
-                v[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide[P][t].v[s], x.v[s],
-                                                               s ? v[t] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-                f32x4 &c = acc[t][(u + MT - 1) % MT];
-                c[s] = fmaf(done[t][s], done_s[t], c[s]);
-                if (u < 2 && i % 2 == 1) {  // units 4u .. 4u + 3 of the next block's W
-                    constexpr int n = u * 2 * NT + i / 2;
-                    wide[P ^ 1][n % NT].v[n / NT] = widen_part(raw[n % NT], n / NT);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            });
-#pragma unroll
-            for (int t = 0; t < NT; ++t) done[t] = v[t], done_s[t] = su[t];
-            // the loads that the last turn made room for
-            constexpr int step = (u + 2) % MT, turned = u < 2 ? 1 : 0, SPREAD = (T::EACH + 2) / 3;
-            if constexpr (step * SPREAD < T::EACH) {
-                const int from = g - turned;
-                if (step == 0 && ((from + S) & 3) == 0 && from + S < nb) issue_scales(from + S);
-#pragma unroll
-                for (int j = step * SPREAD; j < (step + 1) * SPREAD && j < T::EACH; ++j) {
-                    if (j < T::W_EACH) {
-                        if (from >= 0 && from + S + 1 < nb) issue_w(from + S + 1, j);
-                    } else {
-                        if (from >= 0 && from + S < nb) issue_a(from + S, j - T::W_EACH);
-                    }
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        });
-    };
-    int g = 0;
-    for (; g + 1 < nb; g += 2) {
-        block(g, IntC<0>{});
-        block(g + 1, IntC<1>{});
-    }
-    if (g < nb) block(g, IntC<0>{});
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t][MT - 1] = fma4(done[t], done_s[t], acc[t][MT - 1]);
-    wait_vm<0>();
-    __syncthreads();
 }
 
 }  // namespace moe

@@ -6,6 +6,8 @@
 // cut would move codes of h, and the outputs were then 1.3 times as far from the exact
 // ones as their rounding to bf16 leaves them.  y has nothing behind it but that rounding
 // and takes the FP8 cores.
+#include <algorithm>
+
 #include "common.h"
 #include "fp8_mma.h"
 #include "fp8_quant.h"
@@ -19,18 +21,21 @@ using moe::f32x4;
 
 constexpr int kMaxE = 1024;
 constexpr int kMaxPairs = 16384;   // of a permutation
-// Up to here a workgroup finds its expert's pairs itself and no permutation is built.  Top 8
-// of 128 experts of 4096 x 1536 and a shared one, this way and by tiles: 1 token 62 and 79
-// us, 2 tokens 97 and 94, 4 tokens 165 and 125, 32 tokens 655 and 387.
-constexpr int kScanPairs = 12;
+// Up to here, and up to kFewRows tokens, a workgroup finds its expert's pairs itself: no
+// permutation, no launch for a quantisation.  Top 8 of 128 experts of 4096 x 1536 and a
+// shared one, this way and by tiles: 1 token 48 and 80 us, 2 tokens 75 and 89, 3 tokens 102
+// and 109, 4 tokens 127 and 125.
+constexpr int kScanPairs = 32;
+constexpr int kFewBytes = 44 * 1024;  // of LDS for their rows, beside up to 16 KB for the sums
 
 struct ExpertArgs {
-    moe::Fp8Act a;  // gate/up: x, a row a token; down: h
+    moe::Fp8Act a;      // tile kernels.  gate/up: x, a row a token; down: h
+    const uint8_t *in;  // few tokens.  gate/up: x in bf16; down: h in fp32
     int T, H, I, E, k;
     const int32_t *topk_idx;
     const void *const *table;
     const uint8_t *shared, *mask;
-    uint8_t *out;        // rows kernels: fp32 h [rows, I] or y [rows, H]; tile kernels: codes of h, or y
+    uint8_t *out;         // few tokens: fp32 h [rows, I] or y [rows, H]; tile kernels: codes of h, or y
     uint8_t *out_scales;  // tile kernel, gate/up: h's
     const int32_t *offset, *pair_of_row, *tiles;  // tile kernels
 };
@@ -46,34 +51,36 @@ struct Group {
     int rows;
 };
 __device__ __forceinline__ Group find_group(const ExpertArgs &p, int32_t *list) {
+    static_assert(kScanPairs <= 64, "a ballot");
     const int P = p.T * p.k, g = blockIdx.y, lane = threadIdx.x & 63;
     if (g >= P) return {p.shared, nullptr, p.T};
     const int e = p.topk_idx[g];
     if ((unsigned)e >= (unsigned)p.E || (p.mask && !p.mask[e])) return {nullptr, nullptr, 0};
-    int n = 0;
-    for (int b = 0; b < P; b += 64) {
-        const bool mine = b + lane < P && p.topk_idx[b + lane] == e;
-        const uint64_t m = __ballot(mine);
-        if (n == 0 && m && b + __ffsll((long long)m) - 1 < g) return {nullptr, nullptr, 0};  // not the first
-        if (mine && threadIdx.x < 64) list[n + __popcll(m & ((1ull << lane) - 1))] = b + lane;
-        n += __popcll(m);
-    }
+    const bool mine = lane < P && p.topk_idx[lane] == e;
+    const uint64_t m = __ballot(mine);
+    if (__ffsll((long long)m) - 1 < g) return {nullptr, nullptr, 0};  // not the first
+    if (mine && threadIdx.x < 64) list[__popcll(m & ((1ull << lane) - 1))] = lane;
     __syncthreads();
-    return {(const uint8_t *)p.table[e], list, n};
+    return {(const uint8_t *)p.table[e], list, (int)__popcll(m)};
 }
 
 // GATEUP: blockIdx.x is 16 columns of h, tile 0 their rows of W1 and tile 1 of W3; down:
-// 16 * NT rows of W2.
-template <bool GATEUP, int MT, int NT, int WK, int U>
-__global__ __launch_bounds__(64 * WK) void fp8_experts_rows_kernel(ExpertArgs p) {
+// 16 * NT rows of W2.  A workgroup quantises its rows (x in bf16, h in fp32) itself while
+// its first weights are on their way; at_once rows fit the LDS.  Weights bound it: 113 MB of
+// W1 and W3 in 27 us, 57 MB of W2 in 16.  Steps of one block (U) and few waves on a short K
+// leave more workgroups a CU: with two blocks a step 59 us a token, so 48.
+template <bool GATEUP, int NT, int WK, int U>
+__global__ __launch_bounds__(64 * WK) void fp8_experts_few_kernel(ExpertArgs p, int at_once) {
     static_assert(!GATEUP || NT == 2, "a tile of each matrix");
-    __shared__ f32x4 part[WK][NT * MT][64];
+    extern __shared__ uint4 few_smem[];
+    __shared__ f32x4 part[WK][NT][64];
     __shared__ int32_t list[kScanPairs];
+    uint8_t *const xs = reinterpret_cast<uint8_t *>(few_smem);
     const Group g = find_group(p, list);
-    if (g.rows == 0) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int K = GATEUP ? p.H : p.I, N = GATEUP ? p.I : p.H, n0 = blockIdx.x * 16 * (GATEUP ? 1 : NT);
+    if (g.rows == 0) return;
     const uint8_t *w[NT];
     const float *ws[NT];
 #pragma unroll
@@ -84,42 +91,37 @@ __global__ __launch_bounds__(64 * WK) void fp8_experts_rows_kernel(ExpertArgs p)
         ws[t] = m.s + (size_t)(n / 128) * m.s_row;
     }
     auto row_of = [&](int m) { return g.pairs ? g.pairs[m] : p.T * p.k + m; };
-    for (int m0 = 0; m0 < g.rows; m0 += 16 * MT) {
-        const uint8_t *a[MT];
-        const float *as[MT];
+    for (int m0 = 0; m0 < g.rows; m0 += at_once) {
+        const int rows = min(at_once, g.rows - m0);
+        f32x4 acc[NT];
 #pragma unroll
-        for (int u = 0; u < MT; ++u) {
-            const int m = min(m0 + 16 * u + r, g.rows - 1);
-            const int row = GATEUP ? (g.pairs ? g.pairs[m] / p.k : m) : row_of(m);
-            a[u] = p.a.codes + (size_t)row * p.a.stride;
-            as[u] = reinterpret_cast<const float *>(p.a.scales + (size_t)row * p.a.scale_stride);
-        }
-        f32x4 acc[NT][MT];
+        for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (m0) __syncthreads();  // the last rows and their sums are read
+        moe::multiply_few<GATEUP, NT, U, WK>(
+            wave, K, q, w, ws, xs + min(r, rows - 1) * moe::few_row(K), acc, [&]() {
+                for (int m = 0; m < rows; ++m) {
+                    const int row = GATEUP ? (g.pairs ? g.pairs[m0 + m] / p.k : m0 + m) : row_of(m0 + m);
+                    moe::quantise_few<GATEUP ? MOE_BF16 : MOE_FP32>(
+                        xs + m * moe::few_row(K), p.in + (size_t)row * K * (GATEUP ? 2 : 4), 0, 1, K, threadIdx.x,
+                        64 * WK);
+                }
+                __syncthreads();
+            });
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int u = 0; u < MT; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-        moe::multiply_rows<GATEUP, MT, NT, U, WK>(wave, K, q, w, ws, a, as, acc);
-        if (m0) __syncthreads();  // the last rows' sums are read
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int u = 0; u < MT; ++u) part[wave][t * MT + u][lane] = acc[t][u];
+        for (int t = 0; t < NT; ++t) part[wave][t][lane] = acc[t];
         __syncthreads();
-        constexpr int ITEMS = GATEUP ? MT : NT * MT;
-#pragma unroll
-        for (int i0 = 0; i0 < ITEMS; i0 += WK) {
-            const int i = i0 + wave;
-            if (i >= ITEMS) break;
-            const int m = m0 + 16 * (i % MT) + r, n = n0 + 16 * (i / MT) + 4 * q;
-            f32x4 v = moe::joined<WK, NT * MT>(part, i, lane);
+        constexpr int ITEMS = GATEUP ? 1 : NT;
+        for (int i = wave; i < ITEMS; i += WK) {
+            const int n = n0 + 16 * i + 4 * q;
+            f32x4 v = moe::joined<WK, NT>(part, i, lane);
             if constexpr (GATEUP) {
-                const f32x4 up = moe::joined<WK, NT * MT>(part, MT + i, lane);
+                const f32x4 up = moe::joined<WK, NT>(part, 1, lane);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = moe::silu(v[j]) * up[j];
             }
-            if (m < g.rows && n < N)  // N % 32 == 0: all four columns exist
-                reinterpret_cast<float4 *>(p.out)[((size_t)row_of(m) * N + n) / 4] = make_float4(v[0], v[1], v[2], v[3]);
+            if (r < rows && n < N)  // N % 32 == 0: all four columns exist
+                reinterpret_cast<float4 *>(p.out)[((size_t)row_of(m0 + r) * N + n) / 4] =
+                    make_float4(v[0], v[1], v[2], v[3]);
         }
     }
 }
@@ -393,7 +395,7 @@ __global__ __launch_bounds__(64 * T::WAVES, T::TALL ? 2 : 1) void fp8_experts_ti
 struct Space {
     size_t xq, xs, h, hq, hs, offset, pairs, tiles, y, total;
 };
-bool few(int T, int k) { return T * k <= kScanPairs; }
+bool few(int T, int k) { return T <= moe::kFewRows && T * k <= kScanPairs; }
 
 // Rows of a tile, by the rows an expert has on average.
 int tile_rows(int T, int E, int k) { return T * k >= 64 * E ? 160 : T * k >= 24 * E ? 64 : 16; }
@@ -407,15 +409,14 @@ Space layout(int T, int H, int I, int E, int k, bool shared) {
         o += moe::align_up(bytes, 256);
         return at;
     };
-    w.xs = take((size_t)T * moe::fp8_scale_row(H));
-    w.hq = take(rows * I);
-    w.hs = take(rows * moe::fp8_scale_row(I));
     if (few(T, k)) {
-        w.xq = take((size_t)T * H);
         w.h = take(rows * I * 4);
     } else {
         const int BM = tile_rows(T, E, k);
         w.xq = take((size_t)T * H * (BM > 16 ? 2 : 1));
+        w.xs = take((size_t)T * moe::fp8_scale_row(H));
+        w.hq = take(rows * I);
+        w.hs = take(rows * moe::fp8_scale_row(I));
         w.offset = take((size_t)(E + 1) * 4);
         w.pairs = take((size_t)T * k * 4);
         w.tiles = take(4 * (1 + rows / BM + (size_t)E + 1));
@@ -436,6 +437,17 @@ int launch_tiles(const ExpertArgs &a, int rows, hipStream_t s) {
     return MOE_OK;
 }
 
+template <bool GATEUP, int NT, int WK, int U>
+int launch_few(const ExpertArgs &a, bool shared, hipStream_t s) {
+    const int row = moe::few_row(GATEUP ? a.H : a.I), N = GATEUP ? a.I : a.H, columns = GATEUP ? 16 : 16 * NT;
+    const int at_once = std::min(a.T, kFewBytes / row);  // at least 2: 16384 columns take 17 KB
+    hipLaunchKernelGGL((fp8_experts_few_kernel<GATEUP, NT, WK, U>),
+                       dim3((N + columns - 1) / columns, a.T * a.k + (shared ? 1 : 0)), dim3(64 * WK),
+                       (size_t)at_once * row, s, a, at_once);
+    MOE_LAUNCH_CHECK("fp8_experts_few_kernel");
+    return MOE_OK;
+}
+
 int experts(const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_idx, int k,
             const void *const *expert_table, const void *shared_slab, const uint8_t *expert_mask, float *y,
             uint8_t *ws, const Space &sp, hipStream_t s) {
@@ -447,27 +459,18 @@ int experts(const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_i
     a.table = expert_table;
     a.shared = (const uint8_t *)shared_slab;
     a.mask = expert_mask;
+    if (few(T, k)) {
+        a.in = (const uint8_t *)x;
+        a.out = ws + sp.h;
+        int rc = launch_few<true, 2, 8, 1>(a, shared, s);
+        if (rc != MOE_OK) return rc;
+        a.in = ws + sp.h;
+        a.out = (uint8_t *)y;
+        return launch_few<false, 2, 4, 1>(a, shared, s);
+    }
     float *xs = (float *)(ws + sp.xs);
     const moe::Fp8Act ha{ws + sp.hq, ws + sp.hs, (size_t)I, moe::fp8_scale_row(I)};
     a.a = {ws + sp.xq, ws + sp.xs, (size_t)H, moe::fp8_scale_row(H)};
-    if (few(T, k)) {
-        int rc = moe::fp8_quant_rows(x, MOE_BF16, (size_t)2 * H, T, H, false, ws + sp.xq, (size_t)H, xs,
-                                     moe::fp8_scale_row(H), s);
-        if (rc != MOE_OK) return rc;
-        const int groups = T * k + (shared ? 1 : 0);
-        a.out = ws + sp.h;
-        hipLaunchKernelGGL((fp8_experts_rows_kernel<true, 1, 2, 8, 2>), dim3(I / 16, groups), dim3(512), 0, s, a);
-        MOE_LAUNCH_CHECK("fp8_experts_rows_kernel<gate/up>");
-        rc = moe::fp8_quant_rows(ws + sp.h, MOE_FP32, (size_t)4 * I, rows, I, false, ws + sp.hq, (size_t)I,
-                                 (float *)(ws + sp.hs), moe::fp8_scale_row(I), s);
-        if (rc != MOE_OK) return rc;
-        a.a = ha;
-        a.out = (uint8_t *)y;
-        hipLaunchKernelGGL((fp8_experts_rows_kernel<false, 1, 2, 8, 2>), dim3((H + 31) / 32, groups), dim3(512), 0, s,
-                           a);
-        MOE_LAUNCH_CHECK("fp8_experts_rows_kernel<down>");
-        return MOE_OK;
-    }
     const int BM = tile_rows(T, E, k);
     PrepareArgs pa{x, ws + sp.xq, xs, T, H, E, k, BM, topk_idx, expert_mask, shared, (int32_t *)(ws + sp.offset),
                    (int32_t *)(ws + sp.pairs), (int32_t *)(ws + sp.tiles)};

@@ -119,7 +119,10 @@ int moe_router_topk_layers(const uint16_t *x, int n_layers, int T, int H, const 
  *   topk_idx[t,:] = the k largest c, ties to the lower expert index, in descending order;
  *   topk_w[t,i]   = fp32( scale * p_i / (renormalise ? sum of the k chosen p : 1) )   (a sum of zero gives zeros).
  * n_layers independent routers in one call, laid out as in moe_router_topk_layers (bias and
- * balance [n_layers, E] fp32 or NULL).  n_groups = top_groups = 1 for no groups.  A NaN
+ * balance [n_layers, E] fp32 or NULL).  The choice and its order are those of the formulas
+ * in every call; with more than a few tokens the weights come from logits that are summed
+ * in fp32 (off by at most 2e-5 times the norms of x[t,:] and w[e,:], in practice by 1e-7 of
+ * them; moe_router_topk's are exact), so their last bits may depend on T and n_layers.  n_groups = top_groups = 1 for no groups.  A NaN
  * score ranks first; a balance of -infinity leaves its expert to the last.
  * 1 <= k <= min(64, top_groups * E / n_groups), E <= 1024, n_groups <= 64 and a divisor of
  * E, H a multiple of 32 up to 16384, n_layers <= 65535 (MOE_E_SHAPE); MOE_E_ARG for a NULL
@@ -183,7 +186,7 @@ typedef struct moe_cache_desc {
     int inter;
     int slots_per_layer;
     int format; /* slab format: 0 = moe_expert_bytes slabs, 1 = MXFP4 (moe_expert_bytes_mx),
-                   2 = super-blocks (moe_expert_bytes_sb) */
+                   2 = super-blocks (moe_expert_bytes_sb), 4 = FP8 blocks (moe_expert_bytes_fp8) */
 } moe_cache_desc;
 
 /* Validates the description (slots <= experts), checks every host slab is pinned
@@ -600,8 +603,8 @@ int moe_fp8_quant(const void *x, int x_type, int64_t x_stride, int rows, int K, 
  * moe_fp8_quant, 1 x 128, MOE_FP8_SCALE_AMAX; a_scales is not read); w [N, K] codes,
  * w_scales [ceil(N/128), ceil(K/128)]; bias [N] fp32 or NULL; y [M, N] bf16 or fp32.
  * A NaN code (0x7F, 0xFF) or scale makes every output it enters NaN.  A row of y does not
- * depend on the other rows of a, but its last bits may depend on M and N (which kernel
- * runs).  M and N from 0 (a no-op) to 2^26, K a multiple of 16 up to 2^27, operands' rows
+ * depend on the other rows of a, but its last bits may depend on M, N and a_type (which
+ * kernel runs).  M and N from 0 (a no-op) to 2^26, K a multiple of 16 up to 2^27, operands' rows
  * at most 2^28 bytes apart, y's at least a row.
  * workspace: moe_fp8_matmul_workspace_bytes(M, N, K, a_type) bytes (contents don't care,
  * 16-byte aligned; calls sharing it must not overlap in time; NULL when 0).
@@ -623,8 +626,12 @@ int moe_fp8_matmul(const void *a, int a_type, int64_t a_stride, const float *a_s
  * scales of W1 and W3 [ceil(I/128), ceil(H/128)] and of W2 [ceil(H/128), ceil(I/128)],
  * zeros to a multiple of 16 bytes: moe_expert_bytes_fp8(H, I) bytes (0 for other sizes),
  * 16-byte aligned.
- * T*k <= 16384, E <= 1024, H, I <= 16384 (MOE_E_SHAPE); pairs whose expert number is
- * outside 0 .. E-1 with T*k <= 512 are left out (their rows of y stay as they were).
+ * T*k <= 16384, E <= 1024, H, I <= 16384 (MOE_E_SHAPE).  Pairs whose expert number is
+ * outside 0 .. E-1 are left out like masked ones: their rows of y stay as they were (the
+ * combine call would add what its workspace holds there, so it needs valid numbers).  A
+ * token may name an expert twice.  Rows of y do not depend on each other, but their last
+ * bits may depend on T, k and E (which kernels run).  A cache of such slabs sets format =
+ * MOE_FP8 in its descriptor.
  * MOE_E_ARG for T < 0, NULL pointers, or x, shared_slab, y, out or workspace not 16-byte
  * aligned; MOE_E_NOMEM for a workspace below moe_fp8_expert_ffn_workspace_bytes; T = 0 is
  * a no-op.  The combine call needs every routed expert's slab and has no mask. */

@@ -255,6 +255,196 @@ class MxLinear:
         return y.reshape(*shape, self.N)
 
 
+def quantise_fp8(w: torch.Tensor, block_rows: int = 128, scale_rule: int = L.MOE_FP8_SCALE_AMAX,
+                 codes: torch.Tensor | None = None, scales: torch.Tensor | None = None):
+    """(codes [rows, K] uint8, scales [ceil(rows / block_rows), ceil(K / 128)] fp32) of w [rows, K] (bf16, fp16 or
+    fp32, K a multiple of 16; views as quantise_mx takes them) in blocks of block_rows (128: weights, 1: activations)
+    x 128.  codes, scales: where to write them, contiguous and of these shapes.  The scales of activations are made
+    with rows of a multiple of four columns, as the product takes them.  Runs on torch's current stream of w's
+    device."""
+    _check_matrix(w, "quantise_fp8")
+    rows, K = w.shape
+    if block_rows not in (1, 128):
+        raise ValueError(f"quantise_fp8: block_rows {block_rows}")
+    blocks, scale_rows = (K + 127) // 128, -(-rows // block_rows)
+    for t, dtype, shape in ((codes, torch.uint8, (rows, K)), (scales, torch.float32, (scale_rows, blocks))):
+        if t is not None and (t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous()
+                              or t.device != w.device):
+            raise ValueError(f"quantise_fp8: codes or scales must be {dtype} {shape}, contiguous, on {w.device}")
+    with torch.cuda.device(w.device):
+        w = _readable_rows(w)
+        if codes is None:
+            codes = torch.empty((rows, K), dtype=torch.uint8, device=w.device)
+        if scales is None:
+            width = blocks if block_rows == 128 else (blocks + 3) // 4 * 4
+            scales = torch.empty((scale_rows, width), dtype=torch.float32, device=w.device)[:, :blocks]
+        L.moe_fp8_quant(w, _ELEMENT[w.dtype], w.stride(0) * w.element_size(), rows, K, block_rows, scale_rule, codes, K,
+                        scales, 4 * scales.stride(0), torch.cuda.current_stream())
+    return codes, scales
+
+
+def pack_fp8_expert(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, slab: torch.Tensor | None = None,
+                    scale_rule: int = L.MOE_FP8_SCALE_AMAX) -> torch.Tensor:
+    """One expert's FP8 slab (cache format MOE_FP8) from its gate w1 [I,H], up w3 [I,H] and down w2 [H,I] matrices on
+    the GPU.  slab: where to write it (uint8, moe_expert_bytes_fp8(H, I) contiguous bytes, on the matrices' device or
+    the host), or None for a new tensor.  A call that is refused has written nothing."""
+    for w in (w1, w3, w2):
+        _check_matrix(w, "pack_fp8_expert")
+        if w.device != w1.device:
+            raise ValueError(f"pack_fp8_expert: matrices on {w1.device} and {w.device}")
+    I, H = w1.shape
+    if tuple(w3.shape) != (I, H) or tuple(w2.shape) != (H, I):
+        raise ValueError(f"pack_fp8_expert: shapes {tuple(w1.shape)}, {tuple(w3.shape)}, {tuple(w2.shape)}")
+    nbytes = L.moe_expert_bytes_fp8(H, I)
+    if not nbytes:
+        raise ValueError(f"pack_fp8_expert: H={H}, I={I} must be multiples of 32")
+    if slab is None:
+        slab = torch.empty(nbytes, dtype=torch.uint8, device=w1.device)
+    on_host = slab.device.type == "cpu"
+    if (slab.dtype != torch.uint8 or slab.numel() != nbytes or not slab.is_contiguous()
+            or not (on_host or (slab.device == w1.device and slab.data_ptr() % 16 == 0))):
+        raise ValueError(f"pack_fp8_expert: the slab must be {nbytes} contiguous bytes (uint8), 16-byte aligned, on "
+                         f"{w1.device} or the host")
+    slab = slab.view(-1)
+    if on_host:
+        slab.copy_(pack_fp8_expert(w1, w3, w2, None, scale_rule))  # waits for the copy
+        return slab
+    hb, ib = (H + 127) // 128, (I + 127) // 128
+    at, scale_at = 0, 3 * H * I
+    for w, shape, blocks in ((w1, (I, H), (ib, hb)), (w3, (I, H), (ib, hb)), (w2, (H, I), (hb, ib))):
+        scales = slab[scale_at:scale_at + 4 * ib * hb].view(torch.float32).view(blocks)
+        quantise_fp8(w, 128, scale_rule, slab[at:at + H * I].view(shape), scales)
+        at, scale_at = at + H * I, scale_at + 4 * ib * hb
+    slab[scale_at:].zero_()
+    return slab
+
+
+class Fp8Linear:
+    """A dense layer with FP8 weights in blocks of 128 x 128 (moe_fp8_matmul): y = x W^T + bias.
+
+    weight [N, K]: quantised once, here; or codes and scales of a checkpoint, as quantise_fp8 returns them:
+    Fp8Linear((codes, scales)).  out_dtype: torch.bfloat16 or torch.float32 (exact products)."""
+
+    def __init__(self, weight, bias: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                 scale_rule: int = L.MOE_FP8_SCALE_AMAX):
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"Fp8Linear: out_dtype {out_dtype}")
+        if isinstance(weight, torch.Tensor):
+            codes, scales = quantise_fp8(weight, 128, scale_rule)
+        else:
+            codes, scales = weight
+            if (codes.dim() != 2 or codes.element_size() != 1 or codes.shape[1] % 16 or scales.dtype != torch.float32
+                    or tuple(scales.shape) != (-(-codes.shape[0] // 128), -(-codes.shape[1] // 128))
+                    or codes.device.type != "cuda" or scales.device != codes.device):
+                raise ValueError("Fp8Linear: needs codes [N, K] of one byte, K a multiple of 16, and fp32 scales "
+                                 "[ceil(N / 128), ceil(K / 128)] on one GPU")
+            codes, scales = _readable_rows(codes.view(torch.uint8).contiguous()), scales.contiguous()
+        self.N, self.K = codes.shape
+        self.codes, self.scales = codes, scales
+        self.bias = None if bias is None else bias.to(codes.device, torch.float32).contiguous()
+        if self.bias is not None and tuple(self.bias.shape) != (self.N,):
+            raise ValueError(f"Fp8Linear: bias {tuple(self.bias.shape)} for {self.N} outputs")
+        self.out_dtype = out_dtype
+
+    def __call__(self, x) -> torch.Tensor:
+        """x [..., K] bf16 (quantised in blocks of 1 x 128 on the way), or (codes, scales) of quantise_fp8 with
+        block_rows 1, [M, K]; on torch's current stream of the weights' device.  No gradients."""
+        a, a_scales = (x, None) if isinstance(x, torch.Tensor) else x
+        if a.device != self.codes.device or (a_scales is not None and a_scales.device != a.device):
+            raise ValueError(f"Fp8Linear: x on {a.device}, weights on {self.codes.device}")
+        blocks = (self.K + 127) // 128
+        with torch.cuda.device(a.device):
+            if a_scales is None:
+                if a.dtype != torch.bfloat16 or a.shape[-1] != self.K:
+                    raise ValueError(f"Fp8Linear: x must be bf16 [..., {self.K}], got {a.dtype} {tuple(a.shape)}")
+                shape, a_type = a.shape[:-1], L.MOE_BF16
+                a = _readable_rows(a.reshape(-1, self.K).contiguous())
+                scale_stride = 0
+            else:
+                if (a.dim() != 2 or a.element_size() != 1 or a.shape[1] != self.K or not a.is_contiguous()
+                        or a_scales.dtype != torch.float32 or tuple(a_scales.shape) != (a.shape[0], blocks)):
+                    raise ValueError(f"Fp8Linear: needs contiguous codes [M, {self.K}] and fp32 scales [M, {blocks}]")
+                shape, a_type, a = (a.shape[0],), L.MOE_FP8, _readable_rows(a.view(torch.uint8))
+                if a_scales.data_ptr() % 16 or (a.shape[0] > 1 and (a_scales.stride(0) % 4 or a_scales.stride(0) < blocks)) or (
+                        blocks > 1 and a_scales.stride(1) != 1):
+                    rows = torch.empty((a.shape[0], (blocks + 3) // 4 * 4), dtype=torch.float32, device=a.device)
+                    a_scales = rows[:, :blocks].copy_(a_scales)
+                scale_stride = 4 * a_scales.stride(0)
+            M = a.shape[0]
+            y = torch.empty((M, self.N), dtype=self.out_dtype, device=a.device)
+            # a workspace of the call's own: two calls in flight, or two graphs, share nothing
+            need = L.moe_fp8_matmul_workspace_bytes(M, self.N, self.K, a_type)
+            ws = torch.empty(need, dtype=torch.uint8, device=a.device) if need else None
+            L.moe_fp8_matmul(a, a_type, self.K * a.element_size(), a_scales, scale_stride, self.codes, self.K,
+                             self.scales, 4 * blocks, M, self.N, self.K, self.bias, y, _ELEMENT[y.dtype],
+                             y.element_size() * self.N, ws, need, torch.cuda.current_stream())
+        return y.reshape(*shape, self.N)
+
+
+class Fp8MoELayer:
+    """A layer of routed experts with FP8 weights, all resident: a router by scores (moe_router_scored), the experts'
+    feed-forward and its weighted combine (moe_fp8_expert_ffn_combine).
+
+    router [E, H], bias and balance [E] (or None): made fp32; experts: E triples (w1 [I,H], w3 [I,H], w2 [H,I]) on
+    the GPU, packed once, here; shared: such a triple for every token, or None; routing: a moe_routing, k experts a
+    token."""
+
+    def __init__(self, router: torch.Tensor, experts, k: int, routing: L.moe_routing,
+                 bias: torch.Tensor | None = None, balance: torch.Tensor | None = None, shared=None,
+                 scale_rule: int = L.MOE_FP8_SCALE_AMAX):
+        self.E, self.H = router.shape
+        self.k, self.routing = k, routing
+        if len(experts) != self.E:
+            raise ValueError(f"Fp8MoELayer: {len(experts)} experts for a router of {self.E}")
+        self.I = experts[0][0].shape[0]
+        dev = router.device
+        for w1, w3, w2 in list(experts) + ([] if shared is None else [shared]):
+            if tuple(w1.shape) != (self.I, self.H) or w1.device != dev:
+                raise ValueError(f"Fp8MoELayer: an expert of {tuple(w1.shape)} on {w1.device}, not "
+                                 f"{(self.I, self.H)} on {dev}")
+        self.router = router.to(torch.float32).contiguous()
+        self.bias, self.balance = (None if b is None else b.to(dev, torch.float32).contiguous() for b in (bias, balance))
+        for b in (self.bias, self.balance):
+            if b is not None and tuple(b.shape) != (self.E,):
+                raise ValueError(f"Fp8MoELayer: {tuple(b.shape)} for {self.E} experts")
+        nbytes = L.moe_expert_bytes_fp8(self.H, self.I)
+        if not nbytes:
+            raise ValueError(f"Fp8MoELayer: H={self.H}, I={self.I} must be multiples of 32")
+        self.pool = torch.empty((self.E, nbytes), dtype=torch.uint8, device=dev)
+        for e, w in enumerate(experts):
+            pack_fp8_expert(*w, slab=self.pool[e], scale_rule=scale_rule)
+        self.shared = None if shared is None else pack_fp8_expert(*shared, scale_rule=scale_rule)
+        self.table = torch.tensor([self.pool[e].data_ptr() for e in range(self.E)], dtype=torch.int64, device=dev)
+
+    def route(self, x: torch.Tensor):
+        """(experts [T,k] int32, weights [T,k] fp32) of x [T,H] bf16."""
+        T = x.shape[0]
+        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.H or x.device != self.router.device:
+            raise ValueError(f"Fp8MoELayer: x must be bf16 [T, {self.H}] on {self.router.device}")
+        with torch.cuda.device(x.device):
+            x = _readable_rows(x.contiguous())
+            idx = torch.empty((T, self.k), dtype=torch.int32, device=x.device)
+            w = torch.empty((T, self.k), dtype=torch.float32, device=x.device)
+            need = L.moe_router_scored_workspace_bytes(1, T, self.E, self.H)
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+            L.moe_router_scored(x, 1, T, self.H, self.router, self.bias, self.balance, self.E, self.k, self.routing,
+                                idx, w, ws, need, torch.cuda.current_stream())
+        return idx, w
+
+    def __call__(self, x: torch.Tensor) -> torch.Tensor:
+        """x [T, H] bf16 -> [T, H] bf16, on torch's current stream of the weights' device.  No gradients."""
+        idx, w = self.route(x)
+        with torch.cuda.device(x.device):
+            x = _readable_rows(x.contiguous())
+            T = x.shape[0]
+            out = torch.empty((T, self.H), dtype=torch.bfloat16, device=x.device)
+            need = L.moe_fp8_expert_ffn_workspace_bytes(T, self.H, self.I, self.E, self.k, self.shared is not None)
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+            L.moe_fp8_expert_ffn_combine(x, T, self.H, self.I, self.E, idx, w, self.k, self.table, self.shared, out,
+                                         ws, need, torch.cuda.current_stream())
+        return out
+
+
 class MoEStack:
     """L routed-expert MoE layers of one configuration on one GPU.
 
@@ -267,12 +457,18 @@ class MoEStack:
     host cores computing them from the pinned pool (assign_lanes; lane_pick, if
     set, overrides the choice: lane_pick(layer, misses) -> experts for the CPU).
     link_GBps: host-to-device rate the cost model assumes for a streamed expert.
+    routing: None for the softmax router over the chosen logits (moe_router_topk), or a
+    moe_routing for routing by scores (moe_router_scored); balance [layers, E], what it adds
+    to the scores for the choice, or None.
     """
 
     def __init__(self, cfg: synth.Config, *, layers: int | None = None, cap: float | None = None,
                  device: int = 0, threads: int = 0, path: int = L.MOE_FFN_AUTO, split_copies: bool = True,
-                 cpu_lane: int = 0, link_GBps: float = 55.0):
+                 cpu_lane: int = 0, link_GBps: float = 55.0, routing: L.moe_routing | None = None,
+                 balance: torch.Tensor | None = None):
         L.lib()
+        if balance is not None and routing is None:
+            raise ValueError("MoEStack: balance needs a routing")
         self.cfg = cfg
         self.L = layers or cfg.layers
         self.T, self.H, self.I, self.E, self.k = cfg.tokens, cfg.hidden, cfg.inter, cfg.experts, cfg.top_k
@@ -298,6 +494,11 @@ class MoEStack:
             self.wr[l].copy_(torch.from_numpy(synth.router_w(cfg.seed, l, E, H, threads)))
             if self.bias is not None:
                 self.bias[l].copy_(torch.from_numpy(synth.router_bias(cfg, l)))
+
+        self.routing = routing
+        self.balance = None if balance is None else balance.to(self.dev, torch.float32).contiguous()
+        if self.balance is not None and tuple(self.balance.shape) != (Lyr, E):
+            raise ValueError(f"MoEStack: balance {tuple(self.balance.shape)}, not {(Lyr, E)}")
 
         # shared experts: always resident
         self.shared = None
@@ -348,7 +549,8 @@ class MoEStack:
             if self.copy_stream2 is not None:
                 L.moe_cache_split_copies(self.cache, self.copy_stream2)
         # workspaces and outputs
-        self.router_ws_bytes = L.moe_router_layers_workspace_bytes(Lyr, T, E)
+        self.router_ws_bytes = (L.moe_router_layers_workspace_bytes(Lyr, T, E) if routing is None else
+                                max(L.moe_router_scored_workspace_bytes(n, T, E, H) for n in (1, Lyr)))
         self.router_ws = torch.zeros(self.router_ws_bytes, dtype=torch.uint8, device=self.dev)
         self.ffn_ws_bytes = L.moe_expert_ffn_workspace_bytes(T, H, I, E, k, self.has_shared)
         self.ffn_ws = torch.empty(self.ffn_ws_bytes, dtype=torch.uint8, device=self.dev)
@@ -420,16 +622,25 @@ class MoEStack:
         return torch.cuda.current_stream(self.dev)
 
     def route(self, x: torch.Tensor, l: int):
-        L.moe_router_topk(x[l], self.T, self.H, self.wr[l], None if self.bias is None else self.bias[l], self.E,
-                          self.k, self.idx[l], self.w[l], self.router_ws, self.router_ws_bytes, self.stream)
+        self.route_with(x[l], l, self.idx[l], self.w[l])
 
     def route_with(self, x_l: torch.Tensor, l: int, idx: torch.Tensor, w: torch.Tensor):
         """Router of layer l applied to the hidden states x_l [T,H] (any layer's)."""
-        L.moe_router_topk(x_l, self.T, self.H, self.wr[l], None if self.bias is None else self.bias[l], self.E,
-                          self.k, idx, w, self.router_ws, self.router_ws_bytes, self.stream)
+        bias = None if self.bias is None else self.bias[l]
+        if self.routing is not None:
+            L.moe_router_scored(x_l, 1, self.T, self.H, self.wr[l], bias,
+                                None if self.balance is None else self.balance[l], self.E, self.k, self.routing, idx,
+                                w, self.router_ws, self.router_ws_bytes, self.stream)
+            return
+        L.moe_router_topk(x_l, self.T, self.H, self.wr[l], bias, self.E, self.k, idx, w, self.router_ws,
+                          self.router_ws_bytes, self.stream)
 
     def route_all(self, x: torch.Tensor):
         """Routers of every layer in one call."""
+        if self.routing is not None:
+            L.moe_router_scored(x, self.L, self.T, self.H, self.wr, self.bias, self.balance, self.E, self.k,
+                                self.routing, self.idx, self.w, self.router_ws, self.router_ws_bytes, self.stream)
+            return
         L.moe_router_topk_layers(x, self.L, self.T, self.H, self.wr, self.bias, self.E, self.k, self.idx, self.w,
                                  self.router_ws, self.router_ws_bytes, self.stream)
 
@@ -487,7 +698,11 @@ class MoEStack:
         """Router, gate/up, down and combine of layer l in one call (every expert resident).
         The call reads the router weights of the layer that runs next (the first
         after the last) into the device caches while it runs: they are static, so
-        this does not depend on the next layer's input."""
+        this does not depend on the next layer's input.  With a routing: two calls."""
+        if self.routing is not None:
+            self.route(x, l)
+            self.ffn_combine(x, l, out)
+            return
         nxt = self.wr[(l + 1) % self.L]
         call = [L.moe_route_ffn_combine, L.moe_mx_route_ffn_combine, L.moe_sb_route_ffn_combine][self.fmt]
         call(x[l], self.T, self.H, self.I, self.wr[l], None if self.bias is None else self.bias[l],

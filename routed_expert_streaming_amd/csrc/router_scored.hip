@@ -399,10 +399,7 @@ __global__ __launch_bounds__(256, 2) void router_choose_kernel(Logits from, cons
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             l[j] = (float)(v[j] + (bias ? (double)bias[min(lane + 64 * j, c.E - 1)] : 0.0));
-            // and the rounding of the definition's logit and of this one; rows of zeros are exact
-            off[j] = wn[j] > 0.0f ? moe::router_split_error(from.sp.columns) * sqrtf(xn) * sqrtf(wn[j]) +
-                                        0x1p-22f * fabsf(l[j])
-                                  : wn[j] == 0.0f ? 0.0f : INFINITY;
+            off[j] = moe::router_split_error(from.sp.columns, xn, wn[j], l[j]);
         }
     } else {
 #pragma unroll

@@ -4,8 +4,8 @@
 
 namespace moe {
 
-// logit[t,e] = sum of its parts (fp64), off by at most
-//   split_error(columns of a part) * sqrt(sum of xn[.][t]) * sqrt(sum of wn[.][e])
+// logit[t,e] = fp32(sum of its parts in fp64), off by at most
+//   router_split_error(columns of a part, sum of xn[.][t], sum of wn[.][e], logit)
 struct RouterSplit {
     int parts, columns;            // of H: parts of `columns` columns, a multiple of 64
     size_t partial, xn, wn, total;  // byte offsets of one layer's fp32 [parts][T][E], [parts][T], [parts][E]; bytes
@@ -14,16 +14,22 @@ RouterSplit router_split_layout(int layers, int T, int E, int H);
 int router_split(const uint16_t *x, int layers, int T, int H, const float *w_router, int E, const RouterSplit &sp,
                  void *workspace, hipStream_t s);
 
-// Relative to sqrt(sum x^2) sqrt(sum w^2), which is at least the sum of the terms'
-// magnitudes.  What v_mfma_f32_16x16x32_bf16 keeps (measured): of each 8 products (8
-// neighbouring columns) the bits down to 2^-23 of the largest one's exponent; with the sums
-// of eights and the addend rounded to fp32 it is off by at most (7 + 5) * 2^-24 of the
-// magnitudes of its terms and its addend.  Per 64 columns the large plane takes two of them
-// (12 * 2^-23 in all) and the small planes four on sums below 2^-7 of it; 16 leaves a
-// third to spare.  Then one addition per 64 columns of the part (2^-24); 1.01 for the
-// norms' own rounding.
-__host__ __device__ inline float router_split_error(int columns) {
-    return 1.01f * (16.0f + 0.5f * (float)(columns / 64 + 1)) * 0x1p-23f;
+// Relative to |x| |w|, which is at least the sum of the terms' magnitudes.  What
+// v_mfma_f32_16x16x32_bf16 keeps (measured): of each 8 products (8 neighbouring columns)
+// the bits down to 2^-23 of the largest one's exponent; with the sums of eights and the
+// addend rounded to fp32 it is off by at most (7 + 5) * 2^-24 of the magnitudes of its
+// terms and its addend.  Per 64 columns the large plane takes two of them (12 * 2^-23 in
+// all) and the small planes four on sums below 2^-7 of it; 16 leaves a third to spare.
+// Then one addition per 64 columns of the part (2^-24); 1.01 for the norms' own rounding,
+// and the roundings of the definition's logit and of this one.
+//
+// Squares below 2^-150 vanish from the norms: of up to 16384 numbers below 2^-75, together
+// at most 2^-68.  With that added the bound also covers the planes' bits below bf16's range
+// (2^-133 of each weight, 2^-126 |x| in all).  Sums that may pass fp32's range are unknown.
+__device__ __forceinline__ float router_split_error(int columns, float xn, float wn, float logit) {
+    const float size = (sqrtf(xn) + 0x1p-67f) * (sqrtf(wn) + 0x1p-67f);
+    const float relative = 1.01f * (16.0f + 0.5f * (float)(columns / 64 + 1)) * 0x1p-23f;
+    return size < 0x1p125f ? relative * size + 0x1p-22f * fabsf(logit) : INFINITY;  // not a number: unknown
 }
 
 }  // namespace moe

@@ -9,7 +9,9 @@ constexpr int kThreads = 256;
 
 // 1 x 128: 16 neighbouring lanes hold a block, eight values each, so that its maximum
 // is four lane exchanges away.  Lanes of a last block that end behind the row have
-// nothing.  units: lanes of all rows; per: of one (16 a block).
+// nothing.  units: lanes of all rows; per: of one (16 a block).  2048 x 6144 bf16: 10 us,
+// 3.8 TB/s (a large copy 4.7); 6 of them are instructions: about ten for a value's exact
+// rounding.  Stores past the caches took 4% less alone, but the product reads the codes next.
 template <int TYPE, bool POW2>
 __global__ __launch_bounds__(kThreads) void fp8_quant_rows_kernel(const uint8_t *__restrict__ x, size_t x_stride,
                                                                   uint32_t units, uint32_t per, int K,
@@ -28,7 +30,8 @@ __global__ __launch_bounds__(kThreads) void fp8_quant_rows_kernel(const uint8_t 
 }
 
 // 128 x 128: one workgroup a block, held in registers between the maximum and the codes;
-// thread t has columns 8 * (t % 16) .. + 7 of rows t / 16, + 16, ...
+// thread t has columns 8 * (t % 16) .. + 7 of rows t / 16, + 16, ...  1533 x 2080 fp32 (204
+// blocks on 256 CUs): 5.0 us, 3.2 TB/s.
 template <int TYPE, bool POW2>
 __global__ __launch_bounds__(kThreads) void fp8_quant_blocks_kernel(const uint8_t *__restrict__ x, size_t x_stride,
                                                                     int rows, int K, uint8_t *__restrict__ codes,

@@ -9,6 +9,11 @@
 // score or the sum of its two largest) is found by as many lanes as fit the wave, from
 // the scores in LDS; the groups are then ranked by counting, and the top-k runs over
 // order-preserving 64-bit codes in registers.
+//
+// What bounds it: latency.  One token of 4096 x 128: 3.6 us of logits (a launch, a row of w
+// a workgroup) and 5.2 of choice; 16 layers of 32 tokens of 6144 x 256: 20 of logits (5 TB/s
+// of w) and 27; 2048 tokens: 30 and 44.  A winner takes 0.65 us (two reductions of 32 bits
+// over the wave for one of 64), a pass 7.5; what is not told apart takes another pass or two.
 #include <cmath>
 
 #include "common.h"

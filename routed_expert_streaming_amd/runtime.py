@@ -255,6 +255,9 @@ class MxLinear:
         return y.reshape(*shape, self.N)
 
 
+_CODES = (torch.uint8, torch.float8_e4m3fn)  # what E4M3 codes may come as
+
+
 def quantise_fp8(w: torch.Tensor, block_rows: int = 128, scale_rule: int = L.MOE_FP8_SCALE_AMAX,
                  codes: torch.Tensor | None = None, scales: torch.Tensor | None = None):
     """(codes [rows, K] uint8, scales [ceil(rows / block_rows), ceil(K / 128)] fp32) of w [rows, K] (bf16, fp16 or
@@ -333,10 +336,10 @@ class Fp8Linear:
             codes, scales = quantise_fp8(weight, 128, scale_rule)
         else:
             codes, scales = weight
-            if (codes.dim() != 2 or codes.element_size() != 1 or codes.shape[1] % 16 or scales.dtype != torch.float32
+            if (codes.dim() != 2 or codes.dtype not in _CODES or codes.shape[1] % 16 or scales.dtype != torch.float32
                     or tuple(scales.shape) != (-(-codes.shape[0] // 128), -(-codes.shape[1] // 128))
                     or codes.device.type != "cuda" or scales.device != codes.device):
-                raise ValueError("Fp8Linear: needs codes [N, K] of one byte, K a multiple of 16, and fp32 scales "
+                raise ValueError("Fp8Linear: needs E4M3 codes [N, K], K a multiple of 16, and fp32 scales "
                                  "[ceil(N / 128), ceil(K / 128)] on one GPU")
             codes, scales = _readable_rows(codes.view(torch.uint8).contiguous()), scales.contiguous()
         self.N, self.K = codes.shape
@@ -361,7 +364,7 @@ class Fp8Linear:
                 a = _readable_rows(a.reshape(-1, self.K).contiguous())
                 scale_stride = 0
             else:
-                if (a.dim() != 2 or a.element_size() != 1 or a.shape[1] != self.K or not a.is_contiguous()
+                if (a.dim() != 2 or a.dtype not in _CODES or a.shape[1] != self.K or not a.is_contiguous()
                         or a_scales.dtype != torch.float32 or tuple(a_scales.shape) != (a.shape[0], blocks)):
                     raise ValueError(f"Fp8Linear: needs contiguous codes [M, {self.K}] and fp32 scales [M, {blocks}]")
                 shape, a_type, a = (a.shape[0],), L.MOE_FP8, _readable_rows(a.view(torch.uint8))

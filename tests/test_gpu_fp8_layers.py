@@ -60,9 +60,13 @@ def test_linear(out):
         assert torch.equal(lin(view), lin(view.contiguous().clone()))
     again = Fp8Linear((lin.codes.view(torch.float8_e4m3fn), lin.scales), bias, out_dtype=out)
     assert torch.equal(again(wide[:, :K]), lin(wide[:, :K]))
-    for bad in (wide, wide[:, :K].float(), wide[:, :K].cpu(), (lin.codes[:3, :128], lin.scales[:1])):
+    for bad in (wide, wide[:, :K].float(), wide[:, :K].cpu(), (lin.codes[:3, :128], lin.scales[:1]),
+                (a[0].view(torch.int8), a[1])):
         with pytest.raises(ValueError):
             lin(bad)
+    for other in (torch.float8_e5m2, torch.float8_e4m3fnuz, torch.int8):  # bytes of another meaning
+        with pytest.raises(ValueError):
+            Fp8Linear((lin.codes.view(other), lin.scales))
 
 
 def test_pack_places_every_block():

@@ -10,10 +10,10 @@
 // the scores in LDS; the groups are then ranked by counting, and the top-k runs over
 // order-preserving 64-bit codes in registers.
 //
-// What bounds it: latency.  One token of 4096 x 128: 3.6 us of logits (a launch, a row of w
-// a workgroup) and 5.2 of choice; 16 layers of 32 tokens of 6144 x 256: 20 of logits (5 TB/s
-// of w) and 27; 2048 tokens: 30 and 44.  A winner takes 0.65 us (two reductions of 32 bits
-// over the wave for one of 64), a pass 7.5; what is not told apart takes another pass or two.
+// What bounds it: latency.  One token of 4096 x 128: 3.7 us of logits (a launch, a row of w
+// a workgroup) and 5.1 of choice; 16 layers of 32 tokens of 6144 x 256: 20 of logits (5 TB/s
+// of w) and 24; 2048 tokens: 30 and 36.  A 64-bit winner takes 0.65 us (two reductions of 32
+// bits over the wave); 13 to 17 us is the choice where nothing has to be summed again.
 #include <cmath>
 
 #include "common.h"
@@ -63,6 +63,22 @@ __device__ __forceinline__ void merge2(double &a, double &b, double c, double d)
     a = fmax(a, c);
     b = fmax(low, fmax(b, d));
 }
+__device__ __forceinline__ void merge2(float &a, float &b, float c, float d) {
+    const float low = fminf(a, c);
+    a = fmaxf(a, c);
+    b = fmaxf(low, fmaxf(b, d));
+}
+
+// A lane's value, in every lane; lane: the same in all.
+__device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ __forceinline__ float from_lane(float v, int lane) {
+    return __uint_as_float(from_lane(__float_as_uint(v), lane));
+}
+__device__ __forceinline__ double from_lane(double v, int lane) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    return __longlong_as_double(
+        (long long)((uint64_t)from_lane((uint32_t)(u >> 32), lane) << 32 | from_lane((uint32_t)u, lane)));
+}
 
 // Where a token's logits come from.
 struct Logits {
@@ -76,10 +92,10 @@ struct Logits {
 };
 
 // This wave's quarter of two logits as the definition has them: products and sums in fp64.
-// (Six loads of each row in flight: the quarter of rows of 6144 is one memory latency.)
+// (Three loads of each row in flight; six took the same time and twice the code.)
 __device__ __forceinline__ void exact_quarters(const uint16_t *const (&x)[2], const float *const (&w)[2], int H,
                                                double (&sum)[2]) {
-    constexpr int AT_ONCE = 6;
+    constexpr int AT_ONCE = 3;
     double a[2] = {0.0, 0.0};
     for (int h0 = 4 * threadIdx.x; h0 < H; h0 += 1024 * AT_ONCE) {
         uint2 xv[2][AT_ONCE];
@@ -120,12 +136,12 @@ __device__ __forceinline__ float wave_max_positive(float v) {
 // -- the logits behind them are summed again in fp64, and the choice is made again.  A
 // logit that is not finite, or whose bound is not, is summed again first.
 // The four waves of the workgroup do those sums together, two at a time, a quarter of the
-// columns each (asked: the bits of what is asked for, quarters: two rounds' sums, summed:
-// the logits [4][E]); there: this wave has a token.
+// columns each (asked: the experts that each asks for [4][E], asks: how many, -1 where it is
+// done, quarters: two rounds' sums, summed: the logits [4][E]); there: this wave has a token.
 template <int PER, bool SPLIT>
 __device__ __forceinline__ void choose(float (&l)[PER], float (&off)[PER], bool there, const Choice &c,
                                        const float *balance, const uint16_t *x, const float *w, const float *bias,
-                                       int H, double *cs, double *sel, uint64_t (*asked)[16],
+                                       int H, double *cs, double *sel, uint16_t *asked, int *asks,
                                        double (*quarters)[2][4], float *summed,
                                        int32_t *idx_out, float *w_out) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -293,48 +309,183 @@ __device__ __forceinline__ void choose(float (&l)[PER], float (&off)[PER], bool 
         }
         return step;
     };
+    // SPLIT's way for nearly every token, in 32 bits: scores with their rounding added to what
+    // they may be off by; the groups (those at the border once more, with the logits that make
+    // their worth summed again); the winners with all that are not told from them, which are
+    // then ordered by 64-bit scores of their logits, summed again where need be.  Lane i: the
+    // i-th of `entries`.  Left to the above: logits or scores that are not finite, groups that
+    // are not told apart in 32 bits then either, more than 64 entries, softmax's 64-bit zeros.
+    // (6144 x 256, 16 layers of 32 tokens: 27 us by the above alone, 24 so; 2048 tokens 44 and 36.)
+    int entries = 0, entry = 0;
+    float entry_l = 0.0f, top_l = 0.0f;
+    uint64_t redo = 0;  // entries whose logits are summed again
+    enum { START, GROUPS, RANKED, SLOW } way = START;
+    auto quick = [&](uint32_t &again) __attribute__((always_inline)) {
+        float key[PER], far = 0.0f, far_logit = 0.0f, size = 1.0f;
+        bool odd = false;
+        if (!sigmoid) {
+            uint32_t most = 0;
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (lane + 64 * j < c.E) most = max(most, moe::topk_ord(l[j]));
+            top_l = moe::topk_logit(moe::topk_wave_max(most));
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int e = lane + 64 * j;
+            const float d = off[j], v = expf(sigmoid ? -l[j] : l[j] - top_l), q = sigmoid ? 1.0f / (1.0f + v) : v;
+            key[j] = q;
+            if (e >= c.E) continue;
+            if (balance) key[j] += balance[e];
+            far = fmaxf(far, sigmoid ? 0.25f * d : d <= 1.0f ? q * (d + d * d) : 1e30f);
+            far_logit = fmaxf(far_logit, d);
+            odd |= !(fabsf(l[j]) < 1e30f && d < 1e30f) || !(fabsf(key[j]) < 1e30f || key[j] == -INFINITY);
+            if (key[j] > -INFINITY) size = fmaxf(size, fabsf(key[j]));
+        }
+        if (__any(odd)) return SLOW;
+        // a score is within 2^-21 of itself (the exponential, 1 +, 1 /), at most 1; and the sum's rounding
+        const float rounding = 0x1p-21f * wave_max_positive(size);
+        far = 1.001f * wave_max_positive(far) + rounding;
+        far_logit = 1.001f * wave_max_positive(far_logit) + 0x1p-21f;
+        uint64_t in = ~0ull;
+        if (drop) {
+            float *keys = reinterpret_cast<float *>(cs);
+            wave_sync();
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (lane + 64 * j < c.E) keys[lane + 64 * j] = key[j];
+            wave_sync();
+            const int g = lane / per;
+            float a = -INFINITY, b = -INFINITY;
+            if (g < c.groups)
+                for (int i = lane % per; i < n; i += per) merge2(a, b, keys[g * n + i], -INFINITY);
+            for (int o = 1; o < per; o <<= 1) {
+                const float c1 = __shfl_xor(a, o, 64), c2 = __shfl_xor(b, o, 64);
+                merge2(a, b, c1, c2);
+            }
+            const float value = c.top2 ? a + b : a;
+            const uint32_t worth = moe::topk_ord(value);
+            int rank = 0;
+            for (int h = 0; h < c.groups; ++h) {
+                const uint32_t other = from_lane(worth, h * per);
+                rank += other > worth || (other == worth && h < g);
+            }
+            const bool stays = g < c.groups && rank < c.top_groups;
+            in = __ballot(stays);
+            const float gap = (c.top2 ? 4.01f : 2.01f) * (way == START ? far : rounding);
+            const float in_least = moe::topk_logit(~moe::topk_wave_max(stays ? ~worth : 0u));
+            const float out_most = moe::topk_logit(moe::topk_wave_max(g < c.groups && !stays ? worth : 0u));
+            const uint64_t close =
+                __ballot(g < c.groups && !(stays ? value - out_most > gap : in_least - value > gap));
+            if (close) {
+                if (way != START) return SLOW;
+                // of those groups the experts that may be among the ones that make the worth
+                if (lane % per == 0 && g < c.groups) sel[g] = (c.top2 ? b : a) - 2.01f * far;
+                wave_sync();
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const int e = lane + 64 * j, ge = e / n;
+                    if (e < c.E && (close >> (ge * per) & 1) && off[j] > 0.0f && !(key[j] < sel[ge])) again |= 1u << j;
+                }
+                return GROUPS;
+            }
+        }
+        uint32_t ord[PER];  // softmax: by the logits
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int e = lane + 64 * j;
+            ord[j] = e < c.E && (!drop || (in >> (e / n * per) & 1)) ? moe::topk_ord(sigmoid ? key[j] : l[j]) : 0u;
+        }
+        const float apart = 2.01f * (sigmoid ? far : far_logit);
+        float before = 0.0f;
+        uint64_t sums = 0;  // entries whose logits are sums with a bound
+        for (int i = 0;; ++i) {
+            uint32_t best = 0;
+            int best_j = 0;
+            float best_l = 0.0f, best_off = 0.0f;
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (ord[j] > best) best = ord[j], best_j = j, best_l = l[j], best_off = off[j];
+            const uint32_t top = moe::topk_wave_max(best);
+            if (top == 0) break;
+            const float now = moe::topk_logit(top);
+            const bool close = i > 0 && !(before - now > apart);
+            if (i >= c.k && !close) break;
+            if (i >= 64 || (!sigmoid && now - top_l < -600.0f)) return SLOW;
+            const int at = __ffsll((long long)__ballot(best == top)) - 1, at_j = __builtin_amdgcn_readlane(best_j, at);
+            const float at_l = from_lane(best_l, at);
+            if (from_lane(best_off, at) > 0.0f) sums |= 1ull << i;
+            if (close) redo |= 3ull << (i - 1);
+            if (lane == i) entry = at + 64 * at_j, entry_l = at_l;
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (j == at_j && lane == at) ord[j] = 0u;
+            before = now;
+            entries = i + 1;
+        }
+        redo &= sums;
+        for (uint64_t m = redo; m; m &= m - 1) {
+            const int e = __builtin_amdgcn_readlane(entry, __ffsll((long long)m) - 1);
+            if (lane == (e & 63)) again |= 1u << (e >> 6);
+        }
+        return RANKED;
+    };
     if constexpr (!SPLIT) {
         uint32_t again = 0;
         if (there) once(again);
     } else {
         for (bool open = there;;) {
             uint32_t again = 0;
-            if (open) open = once(again);
-            if (!open) again = 0;
-            if (!__syncthreads_or(open)) break;
+            if (open && way == RANKED) {
+                open = false;
+            } else if (open) {
+                if (way != SLOW) way = quick(again);
+                if (way == SLOW) {
+                    again = 0;
+                    open = once(again);
+                    if (!open) again = 0;
+                } else if (way == RANKED) {
+                    open = redo != 0;
+                }
+            }
+            int mine = 0;  // this wave's experts, one after the other
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 const uint64_t m = __ballot(again >> j & 1);
-                if (lane == 0) asked[wave][j] = m;
+                if (again >> j & 1) asked[wave * c.E + mine + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(lane + 64 * j);
+                mine += __popcll(m);
             }
+            if (lane == 0) asks[wave] = open ? mine : -1;
             __syncthreads();
-            int have = 0, round = 0, token[2] = {}, expert[2] = {};
-            auto sum_them = [&]() __attribute__((always_inline)) {
-                const uint16_t *const xs[2] = {x + (size_t)token[0] * H, x + (size_t)token[1] * H};
-                const float *const wr[2] = {w + (size_t)expert[0] * H, w + (size_t)expert[1] * H};
+            int upto[4], any = 0;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int m = __builtin_amdgcn_readfirstlane(asks[v]);
+                any |= m >= 0;
+                upto[v] = (v ? upto[v - 1] : 0) + (m > 0 ? m : 0);
+            }
+            if (!any) break;
+            for (int at = 0, round = 0; at < upto[3]; at += 2, ++round) {
+                int pair[2];  // of [4][E]; the last one again where there are no more
+                const uint16_t *xs[2];
+                const float *wr[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int i = min(at + k, upto[3] - 1), v = (i >= upto[0]) + (i >= upto[1]) + (i >= upto[2]);
+                    const int first = v == 0 ? 0 : v == 1 ? upto[0] : v == 2 ? upto[1] : upto[2];
+                    const int e = __builtin_amdgcn_readfirstlane(asked[v * c.E + i - first]);
+                    pair[k] = v * c.E + e, xs[k] = x + (size_t)v * H, wr[k] = w + (size_t)e * H;
+                }
                 double v[2];
                 exact_quarters(xs, wr, H, v);
                 double(*q)[4] = quarters[round & 1];
                 if (lane < 2) q[lane][wave] = lane ? v[1] : v[0];
                 __syncthreads();
                 if (threadIdx.x < 2) {
-                    const int k = threadIdx.x, e = k ? expert[1] : expert[0];
-                    summed[(k ? token[1] : token[0]) * c.E + e] =
-                        (float)(((q[k][0] + q[k][1]) + (q[k][2] + q[k][3])) + (bias ? (double)bias[e] : 0.0));
+                    const int k = threadIdx.x, at_pair = k ? pair[1] : pair[0];
+                    summed[at_pair] = (float)(((q[k][0] + q[k][1]) + (q[k][2] + q[k][3])) +
+                                              (bias ? (double)bias[at_pair % c.E] : 0.0));
                 }
-                have = 0;
-                ++round;
-            };
-            for (int v = 0; v < 4; ++v)
-                for (int j = 0; j < PER; ++j)
-                    for (uint64_t m = asked[v][j]; m; m &= m - 1) {
-                        token[1] = token[0], expert[1] = expert[0];
-                        token[0] = v, expert[0] = 64 * j + __ffsll((long long)m) - 1;
-                        if (++have == 2) sum_them();
-                    }
-            if (have) {
-                token[1] = token[0], expert[1] = expert[0];
-                sum_them();
             }
             __syncthreads();
 #pragma unroll
@@ -343,6 +494,31 @@ __device__ __forceinline__ void choose(float (&l)[PER], float (&off)[PER], bool 
         }
     }
     if (!there) return;
+    if (SPLIT && way == RANKED) {
+        if (redo >> lane & 1) entry_l = summed[wave * c.E + entry];
+        const double v = exp(sigmoid ? -(double)entry_l : (double)entry_l - (double)top_l);
+        double p = sigmoid ? 1.0 / (1.0 + v) : v;
+        const double key = balance && lane < entries ? p + (double)balance[entry] : p;
+        int rank = 0;
+        for (int i = 0; i < entries; ++i) {
+            const double other = from_lane(key, i);
+            rank += other > key || (other == key && __builtin_amdgcn_readlane(entry, i) < entry);
+        }
+        if (!sigmoid && !c.renorm) {  // the sum of all: 32-bit terms, as precise as the logits are
+            double sum = 0.0;
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (lane + 64 * j < c.E) sum += (double)expf(l[j] - top_l);
+            p /= wave_sum_f64(sum);
+        }
+        wave_sync();
+        if (lane < entries && rank < c.k) {
+            sel[rank] = p;
+            asked[wave * c.E + rank] = (uint16_t)entry;
+        }
+        wave_sync();
+        slot = lane < c.k ? asked[wave * c.E + lane] : 0;
+    }
     wave_sync();
     double wt = lane < c.k ? sel[lane] : 0.0;
     if (c.renorm) {
@@ -420,11 +596,12 @@ __global__ __launch_bounds__(256, 2) void router_choose_kernel(Logits from, cons
     }
     const int scores = c.top_groups < c.groups ? c.E : 0;
     double *sel = lds + 4 * scores + 64 * wave;
-    uint64_t(*asked)[16] = reinterpret_cast<uint64_t(*)[16]>(lds + 4 * scores + 256);
+    double(*quarters)[2][4] = reinterpret_cast<double(*)[2][4]>(lds + 4 * scores + 256);
+    float *summed = reinterpret_cast<float *>(quarters + 2);
+    int *asks = reinterpret_cast<int *>(summed + 4 * c.E);
     choose<PER, KIND == Logits::SPLIT>(l, off, mine < T, c, balance, from.x + ((size_t)blockIdx.y * T + 4 * blockIdx.x) * from.H,
                                        from.w + (size_t)blockIdx.y * c.E * from.H, bias, from.H, lds + wave * scores, sel,
-                                       asked, reinterpret_cast<double(*)[2][4]>(asked + 4),
-                                       reinterpret_cast<float *>(lds + 4 * scores + 256 + 64 + 16), idx + row * c.k,
+                                       reinterpret_cast<uint16_t *>(asks + 4), asks, quarters, summed, idx + row * c.k,
                                        w + row * c.k);
 }
 
@@ -433,7 +610,7 @@ int launch_choose(const Logits &from, int layers, const float *balance, const Ch
                   hipStream_t s) {
     const dim3 grid((from.T + 3) / 4, layers), block(256);
     const size_t lds = ((c.top_groups < c.groups ? (size_t)4 * c.E : 0) + 256) * sizeof(double) +
-                       (KIND == Logits::SPLIT ? (64 + 16) * sizeof(double) + (size_t)4 * c.E * sizeof(float) : 0);
+                       (KIND == Logits::SPLIT ? 16 * sizeof(double) + (size_t)4 * c.E * 6 + 16 : 0);
     auto *kernel = c.E <= 64    ? router_choose_kernel<1, KIND>
                    : c.E <= 128 ? router_choose_kernel<2, KIND>
                    : c.E <= 256 ? router_choose_kernel<4, KIND>

@@ -131,7 +131,6 @@ __global__ __launch_bounds__(64 * WK) void fp8_experts_few_kernel(ExpertArgs p, 
 // columns of h or 256 of y.  Rows of h: the pairs' places in that order, then T * k + t; so
 // the down projection reads neighbouring rows.
 constexpr int kGroupBits = 11;  // of a tile's number: its expert (E: the shared one); above: which of its BM rows
-constexpr int kRun = 16;         // neighbouring tiles that an XCD takes at a time
 constexpr int kPrepare = 1024;  // threads of the kernel that comes first
 
 // One launch before the products.  Workgroup 0 sorts the pairs by expert, stable, and lists
@@ -365,15 +364,13 @@ __global__ __launch_bounds__(64 * T::WAVES, T::TALL ? 2 : 1) void fp8_experts_ti
     constexpr int BN = GATEUP ? T::BN / 2 : T::BN;
     __shared__ uint4 smem4[T::LDS / 16];
     uint8_t *smem = reinterpret_cast<uint8_t *>(smem4);
-    // The XCDs take runs of neighbouring tiles in turn, an expert's rows fastest: the tiles
-    // that share rows of W start together and read them from its L2.  (With the columns
-    // fastest they drifted apart: 2.9 GB came from memory for 1.6 GB of W1 and W3.  With one
-    // long run an XCD the last one had the shared expert's tiles, the tallest: gate/up 655
-    // us, so 630.)
+    // Each XCD takes a run of neighbouring tiles, an expert's rows fastest: the tiles that
+    // share rows of W start together and read them from its L2.  (With the columns fastest
+    // they drifted apart: 2.9 GB came from memory for 1.6 GB of W1 and W3.)
     const int N = GATEUP ? p.I : p.H;
-    const int n_tiles = (N + BN - 1) / BN, tiles = p.tiles[0] * n_tiles;
-    const int i = blockIdx.x >> 3, tile = ((i / kRun) * 8 + (blockIdx.x & 7)) * kRun + i % kRun;
-    if (tile >= tiles) return;
+    const int n_tiles = (N + BN - 1) / BN, tiles = p.tiles[0] * n_tiles, per = (tiles + 7) / 8;
+    const int i = blockIdx.x >> 3, tile = (blockIdx.x & 7) * per + i;
+    if (i >= per || tile >= tiles) return;
     const int number = p.tiles[1 + tile / n_tiles], e = number & ((1 << kGroupBits) - 1);
     TileOf at;
     at.shared = e == p.E;
@@ -441,8 +438,7 @@ int launch_tiles(const ExpertArgs &a, int rows, hipStream_t s) {
     // at most so many tiles of rows: every expert's last one may be short
     const int experts = a.E < a.T * a.k ? a.E : a.T * a.k, most = rows / T::BM + experts + 1;
     const int columns = GATEUP ? (a.I + T::BN / 2 - 1) / (T::BN / 2) : (a.H + T::BN - 1) / T::BN;
-    hipLaunchKernelGGL((fp8_experts_tile_kernel<GATEUP, T>),
-                       dim3((unsigned)((most * columns + 8 * kRun - 1) / (8 * kRun) * (8 * kRun))),
+    hipLaunchKernelGGL((fp8_experts_tile_kernel<GATEUP, T>), dim3((unsigned)((most * columns + 7) / 8 * 8)),
                        dim3(64 * T::WAVES), 0, s, a);
     MOE_LAUNCH_CHECK("fp8_experts_tile_kernel");
     return MOE_OK;

@@ -174,7 +174,7 @@ void launch_tile(const MatArgs &p, hipStream_t s) {
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * T::WAVES), 0, s, p, m_tiles, n_tiles);
 }
 
-// A few rows of bf16 activations, quantised by each workgroup (16 rows of W) for itself.
+// Up to 16 rows of bf16 activations, quantised by each workgroup (16 rows of W) for itself.
 template <bool WIDE, int WK, int U>
 __global__ __launch_bounds__(64 * WK) void fp8_matmul_few_kernel(MatArgs p) {
     extern __shared__ uint4 few_smem[];
@@ -259,12 +259,17 @@ Kind plan(bool wide, int M, int N, int K, bool near) {
 // Rows further apart than this take the rows kernels: a tile's lane offsets are 32 bits.
 constexpr int64_t kTileStride = 8 << 20;
 
-// Which activations the kernel quantises itself: up to kFewRows rows that leave LDS room
-// for two workgroups a CU, and few enough workgroups to do so again and again (1 x 4096 x
-// 4096: two launches 8.1 us, one 6.2).
+// Which activations the kernel quantises itself: one tile of rows that leave LDS room for two
+// workgroups a CU, where every workgroup doing so takes less than a launch for all of them.
+// Kernels alone, two launches and one, us: 1 x 4096 x 4096 8.1 and 6.8; 1 x 12288 x 12288 45
+// and 36; 8 x 4096 x 1024 6.3 and 4.6; 16 x 4096 x 1024 6.4 and 6.2, x 12288 9.0 and 11.9;
+// 4 x 4096 x 4096 9.2 and 9.3, x 12288 14 and 18; 3 x 12288 x 6144 17 and 19.
 constexpr int kFewBytes = 52 << 10, kFewWgs = 1024;
+constexpr int64_t kFewValues = 11 << 10, kFewValuesNarrow = 18 << 10;  // of A; for a round of workgroups
 bool few(bool quantise, int M, int N, int K) {
-    return quantise && M <= moe::kFewRows && (int64_t)M * moe::few_row(K) <= kFewBytes && N <= 16 * kFewWgs;
+    const int64_t values = (int64_t)M * K;
+    return quantise && M <= 16 && (int64_t)M * moe::few_row(K) <= kFewBytes && N <= 16 * kFewWgs &&
+           (M == 1 || values <= (N <= 4096 ? kFewValuesNarrow : kFewValues));
 }
 
 // WIDE: products of codes converted to bf16, for fp32 outputs.

@@ -87,10 +87,9 @@ __device__ __forceinline__ void multiply_rows(int wave, int K, int q, const uint
 }
 
 // ---------------------------------------------------------------- a few rows, quantised here
-// Up to kFewRows rows of unquantised activations that fit LDS whole: the workgroup
-// quantises them itself, while its first weights are on their way, which saves a launch
-// for one token.  Row m: its codes at xs + m * few_row(K), then its scales.
-constexpr int kFewRows = 4;
+// Up to 16 rows of unquantised activations that fit LDS whole: the workgroup quantises them
+// itself, while its first weights are on their way, which saves a launch.  Row m: its codes at xs + m * few_row(K), then its scales.
+constexpr int kFewRows = 4;  // tokens of the experts
 __host__ __device__ inline int few_row(int K) {
     const int blocks = (K + 127) / 128;
     return blocks * 128 + (blocks + 3) / 4 * 16 + 16;  // (the last 16: other banks for the next row)

@@ -244,13 +244,17 @@ def test_matmul_quantises_bf16(M, N, K):
         L.moe_fp8_matmul(a, kind, stride, sc, 4 * srow, wd, K, swd, 4 * fp8kit.blocks(K), M, N, K, None, y, L.MOE_FP32,
                          4 * N, ws, need, s)
         out.append(y.cpu().numpy())
-    assert np.array_equal(out[0], out[1], equal_nan=True)
+    # beyond 16 rows the same kernel multiplies the same codes; up to there one that quantises them itself adds the blocks'
+    # sums in another order (one chain of fused additions, or parts that are joined): each is within sum_error
+    if M > 16:
+        assert np.array_equal(out[0], out[1], equal_nan=True)
     rc, rs = fp8kit.quantise(x[:, :K].double().numpy())
     va, vw = fp8kit.values(rc, rs, 1), fp8kit.values(w, sw, 128)
     want, mag = va @ vw.T, np.abs(va) @ np.abs(vw).T
     ok = ~np.isnan(want)
-    assert np.array_equal(ok, ~np.isnan(out[0]))
-    assert (np.abs(out[0] - want) <= (fp8kit.sum_error(K) + 2.0 ** -24) * mag + 2.0 ** -24 * np.abs(want))[ok].all()
+    for y in out:
+        assert np.array_equal(ok, ~np.isnan(y))
+        assert (np.abs(y - want) <= (fp8kit.sum_error(K) + 2.0 ** -24) * mag + 2.0 ** -24 * np.abs(want))[ok].all()
 
 
 def test_matmul_streams_and_graphs():

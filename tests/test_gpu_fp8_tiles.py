@@ -45,6 +45,31 @@ def test_bounds(M, N, K):
         assert (np.abs(got - want) <= err + half * (np.abs(want) + err)).all()
 
 
+@pytest.mark.parametrize("y_type", [L.MOE_BF16, L.MOE_FP32])
+@pytest.mark.parametrize("M,N,K", [(1, 33, 16), (1, 4100, 8400), (2, 257, 4096), (3, 130, 6144), (5, 1000, 2048), (8, 72, 1040),
+                                   (11, 8200, 912), (16, 300, 400), (16, 4096, 1024), (16, 4112, 1040), (9, 64, 2064)])
+def test_activations_of_a_few_rows(M, N, K, y_type):
+    """bf16 activations, quantised in the product's kernel or before it."""
+    rng = np.random.default_rng(M * N + K)
+    w, sw = random_operand(rng, N, K, 128)
+    x = torch.randn((M, K + 8), generator=torch.Generator().manual_seed(K)).to(torch.bfloat16)[:, :K]
+    bias = rng.standard_normal(N).astype(np.float32)
+    y = torch.full((M + 1, N), 5.0, dtype=DTYPE[y_type], device="cuda")
+    need = L.moe_fp8_matmul_workspace_bytes(M, N, K, L.MOE_BF16)
+    ws = torch.full((need + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    xd = torch.full((M, K + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    xd[:, :K] = x.cuda()
+    L.moe_fp8_matmul(xd, L.MOE_BF16, 2 * (K + 8), None, 0, dev(w), K, dev(sw), 4 * sw.shape[1], M, N, K, dev(bias), y, y_type,
+                     N * y.element_size(), ws, need, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert (y[M] == 5.0).all() and (ws[need:] == 0xA5).all()
+    va, vw = fp8kit.values(*fp8kit.quantise(x.double().numpy()), 1), fp8kit.values(w, sw, 128)
+    want, mag = va @ vw.T + bias, np.abs(va) @ np.abs(vw).T + np.abs(bias)
+    err = (fp8kit.sum_error(K) + fp8kit.cores_error(y_type == L.MOE_BF16) + 2.0 ** -24) * mag
+    half = 2.0 ** -8 if y_type == L.MOE_BF16 else 2.0 ** -24
+    assert (np.abs(y[:M].double().cpu().numpy() - want) <= err + half * (np.abs(want) + err)).all()
+
+
 def apart(c, stride):
     """Rows of c as a view of rows stride bytes apart."""
     buf = torch.empty(((c.shape[0] - 1) * stride + c.shape[1] * c.element_size(),), dtype=torch.uint8, device="cuda")

@@ -60,16 +60,7 @@ __device__ __forceinline__ f32x4 mfma_fp8(const WideFrag &w, const WideFrag &a) 
     for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[s], a.v[s], c, 0, 0, 0);
     return c;
 }
-__device__ __forceinline__ void cut_frag(WideFrag &f, int q, int pieces) {
-    const bf16x8 zero = __builtin_bit_cast(bf16x8, make_uint4(0u, 0u, 0u, 0u));
-    if (q >= pieces) f.v[0] = f.v[1] = zero;
-    if (q + 4 >= pieces) f.v[2] = f.v[3] = zero;
-}
 // The operand as the products take it.
-template <bool WIDE>
-__device__ __forceinline__ WideFrag operand(const WideFrag &f) {
-    return f;
-}
 template <bool WIDE>
 __device__ __forceinline__ auto operand(const Fp8Frag &f) {
     if constexpr (WIDE)

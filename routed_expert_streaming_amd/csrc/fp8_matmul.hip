@@ -256,7 +256,8 @@ Kind plan(bool wide, int M, int N, int K, bool near) {
     return best;
 }
 
-// Rows further apart than this take the rows kernels: a tile's lane offsets are 32 bits.
+// Rows (of A, of its scales, of W) further apart than this take the rows kernels: a tile's
+// lane offsets are 32 bits.
 constexpr int64_t kTileStride = 8 << 20;
 
 // Which activations the kernel quantises itself: one tile of rows that leave LDS room for two
@@ -386,7 +387,8 @@ extern "C" int moe_fp8_matmul(const void *a, int a_type, int64_t a_stride, const
         if (rc != MOE_OK) return rc;
         p.a = {codes, (const uint8_t *)scales, (size_t)K, moe::fp8_scale_row(K)};
     }
-    const bool near = (M == 1 || p.a.stride < (size_t)kTileStride) && (N == 1 || p.w_stride < (size_t)kTileStride);
+    const size_t far = (size_t)kTileStride;
+    const bool near = (M == 1 || (p.a.stride < far && p.a.scale_stride < far)) && (N == 1 || p.w_stride < far);
     const Kind kind = here ? FEW : plan(p.y_f32, M, N, K, near);
     return p.y_f32 ? run<true>(p, kind, s) : run<false>(p, kind, s);
 }

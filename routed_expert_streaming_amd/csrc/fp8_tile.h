@@ -47,9 +47,10 @@ struct Fp8Tile {
 // first group's waves have the sums in the end.  w, a, as: uniform
 // bases at column 0; w_off(row), a_off(row), as_off(row): 32-bit byte offsets of the
 // tile's rows (valid for every row of the tile); ws[i]: the scales of the wave's i-th
-// NT / SN tiles, one per block.  On return no load is in flight and all waves are done
-// with the LDS.
-template <class T, bool WIDE, int SN, class WOff, class AOff, class SOff>
+// NT / SN tiles, one per block.  ENDS: A's rows of scales end where their values do, so
+// nothing behind them is read (else they are readable up to a multiple of 16 bytes).
+// On return no load is in flight and all waves are done with the LDS.
+template <class T, bool WIDE, int SN, bool ENDS = false, class WOff, class AOff, class SOff>
 __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const uint8_t *a, const uint8_t *as,
                                          const float *const (&ws)[SN], int K, WOff w_off, AOff a_off, SOff as_off,
                                          f32x4 (&acc)[T::NT][T::MT]) {
@@ -91,8 +92,18 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
     const int se = wave % T::SCALE_LOADS;  // (several waves bring the same rows)
     const uint32_t s_off = as_off(min(64 * se + lane, T::BM - 1));
     auto issue_scales = [&](int i) __attribute__((always_inline)) {  // of stage i's block and its neighbours
-        const int place = KW == 1 ? i >> 2 & 1 : i % SA;
-        dma16(as + 16 * (size_t)(block_of(i) >> 2), s_off, lds0 + T::S_RING + (uint32_t)place * T::CHUNK + 1024u * se);
+        const int place = KW == 1 ? i >> 2 & 1 : i % SA, first = block_of(i) & ~3;
+        const uint32_t at = T::S_RING + (uint32_t)place * T::CHUNK + 1024u * se;
+        if (ENDS && first + 4 > blocks) {
+            // fewer than four: value by value.  The waves' waits stay right without the load that they
+            // count here, because these values are waited for, and with them every load before them.
+            const float *from = reinterpret_cast<const float *>(as + s_off);
+            float *to = reinterpret_cast<float *>(ring + at + 16 * lane);
+#pragma unroll 1
+            for (int b = first; b < blocks; ++b) to[b - first] = from[b];
+        } else {
+            dma16(as + 4 * (size_t)first, s_off, lds0 + at);
+        }
     };
     float wsv[SN];  // lane l: the scale of block 64 * (b / 64) + l
     auto load_ws = [&](int b0) __attribute__((always_inline)) {

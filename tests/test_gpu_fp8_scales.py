@@ -34,3 +34,26 @@ def test_scale_rows_far_apart(M, N, K, stride, y_type):
     got = product(a, buf, stride, w, sw, y_type)
     want = fp8kit.values(a, sa, 1) @ fp8kit.values(w, sw, 128).T
     assert np.array_equal(got, torch.from_numpy(want).to(DTYPE[y_type]).double().numpy())
+
+
+# one for each kernel that a product may take; blocks of 128 columns that are no multiple of four
+ENDS = [(1, 16, 128), (1, 130, 1040), (7, 300, 272), (16, 64, 2080), (17, 130, 144), (33, 260, 640), (17, 5000, 1168),
+        (33, 5000, 272), (100, 5000, 784), (33, 5000, 144), (300, 6144, 144), (300, 6144, 1168), (2000, 2080, 144),
+        (1500, 6144, 144), (2560, 4864, 144)]
+
+
+@pytest.mark.parametrize("y_type", [L.MOE_BF16, L.MOE_FP32])
+@pytest.mark.parametrize("M,N,K", ENDS)
+def test_scale_rows_that_end_with_their_values(M, N, K, y_type):
+    """The last row of scales is ceil(K / 128) values and no more; what lies behind it is not the product's."""
+    rng = np.random.default_rng(M + N + K)
+    a, sa = small_operand(rng, M, K, 1)
+    w, sw = small_operand(rng, N, K, 128)
+    blocks = fp8kit.blocks(K)
+    assert blocks % 4
+    row = (blocks + 3) // 4 * 4
+    buf = torch.full(((M - 1) * row + blocks,), float("nan"), device="cuda")
+    buf.as_strided((M, blocks), (row, 1)).copy_(dev(sa))
+    got = torch.from_numpy(product(a, buf, 4 * row, w, sw, y_type))
+    va, vw = (dev(fp8kit.values(*o)) for o in ((a, sa, 1), (w, sw, 128)))
+    assert torch.equal(got, (va @ vw.T).to(DTYPE[y_type]).double().cpu())  # (sums of whole multiples of 1/4: exact)

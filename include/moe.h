@@ -129,8 +129,9 @@ int moe_router_topk_layers(const uint16_t *x, int n_layers, int T, int H, const 
  * pointer, a negative T or n_layers, an unknown score or rule, a scale that is not finite,
  * or x, w_router or workspace not 16-byte aligned.  T = 0 or n_layers = 0 is a no-op.
  * workspace: moe_router_scored_workspace_bytes(n_layers, T, E, H) bytes (contents don't
- * care; calls sharing it must not overlap in time).  The description is read before the
- * call returns. */
+ * care; calls sharing it must not overlap in time), which never falls as n_layers or T
+ * grows: one of the longest call's serves all.  The description is read before the call
+ * returns. */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
 typedef struct moe_routing {
@@ -607,7 +608,8 @@ int moe_fp8_quant(const void *x, int x_type, int64_t x_stride, int rows, int K, 
  * kernel runs).  M and N from 0 (a no-op) to 2^26, K a multiple of 16 up to 2^27, operands' rows
  * at most 2^28 bytes apart, y's at least a row.
  * workspace: moe_fp8_matmul_workspace_bytes(M, N, K, a_type) bytes (contents don't care,
- * 16-byte aligned; calls sharing it must not overlap in time; NULL when 0).
+ * 16-byte aligned; calls sharing it must not overlap in time; NULL when 0; never falls as
+ * M grows).
  * MOE_E_SHAPE for sizes or strides beyond these; MOE_E_ARG for negative sizes, unknown
  * types, NULL pointers, a, w or a_scales (pointers or strides) that are not multiples of 16
  * bytes, w_scales, y, bias or workspace not aligned; MOE_E_NOMEM for a small workspace.  y
@@ -633,8 +635,8 @@ int moe_fp8_matmul(const void *a, int a_type, int64_t a_stride, const float *a_s
  * bits may depend on T, k and E (which kernels run).  A cache of such slabs sets format =
  * MOE_FP8 in its descriptor.
  * MOE_E_ARG for T < 0, NULL pointers, or x, shared_slab, y, out or workspace not 16-byte
- * aligned; MOE_E_NOMEM for a workspace below moe_fp8_expert_ffn_workspace_bytes; T = 0 is
- * a no-op.  The combine call needs every routed expert's slab and has no mask. */
+ * aligned; MOE_E_NOMEM for a workspace below moe_fp8_expert_ffn_workspace_bytes (which
+ * never falls as T grows); T = 0 is a no-op.  The combine call needs every routed expert's slab and has no mask. */
 size_t moe_expert_bytes_fp8(int hidden, int inter);
 size_t moe_fp8_expert_ffn_workspace_bytes(int T, int H, int I, int E, int k, int has_shared);
 int moe_fp8_expert_ffn(const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_idx, int k,

@@ -400,13 +400,16 @@ __global__ __launch_bounds__(64 * T::WAVES, T::TALL ? 2 : 1) void fp8_experts_ti
 struct Space {
     size_t xq, xs, h, hq, hs, offset, pairs, tiles, y, total;
 };
-bool few(int T, int k) { return T <= moe::kFewRows && T * k <= kScanPairs; }
+bool few(int T, int k) { return T <= moe::kFewRows && (int64_t)T * k <= kScanPairs; }
 
 // Rows of a tile, by the rows an expert has on average.  Tiles of 16 rows leave two
 // workgroups a CU and keep up with memory (32 tokens, top 8 of 128 experts of 4096 x 1536:
 // 2.1 GB of weights in 380 us); tall ones read and convert each row of W once for all of an
 // expert's rows (2048 tokens: gate/up 650 us, down 280; in tiles of 64 rows 850 and 370).
-int tile_rows(int T, int E, int k) { return T * k >= 64 * E ? 160 : T * k >= 24 * E ? 64 : 16; }
+int tile_rows(int T, int E, int k) {
+    const int64_t pairs = (int64_t)T * k;
+    return pairs >= (int64_t)64 * E ? 160 : pairs >= (int64_t)24 * E ? 64 : 16;
+}
 
 Space layout(int T, int H, int I, int E, int k, bool shared) {
     Space w{};
@@ -427,11 +430,17 @@ Space layout(int T, int H, int I, int E, int k, bool shared) {
         w.hs = take(rows * moe::fp8_scale_row(I));
         w.offset = take((size_t)(E + 1) * 4);
         w.pairs = take((size_t)T * k * 4);
-        w.tiles = take(4 * (1 + rows / BM + (size_t)E + 1));
+        w.tiles = take(4 * (1 + rows / 16 + (size_t)E + 1));  // (16: the size grows with T)
     }
     w.y = take(rows * H * 4);
     w.total = o;
     return w;
+}
+
+// Enough for every call of fewer tokens too: a few rows' h is in fp32.
+size_t workspace_of(int T, int H, int I, int E, int k, bool shared) {
+    const int some = std::min(std::min(T, moe::kFewRows), kScanPairs / k);  // the most tokens that `few` takes
+    return std::max(layout(T, H, I, E, k, shared).total, some ? layout(some, H, I, E, k, shared).total : 0);
 }
 
 template <bool GATEUP, class T>
@@ -513,9 +522,10 @@ int check(const char *who, const uint16_t *x, int T, int H, int I, int E, const 
     if (!x || !topk_idx || !expert_table || !out || !workspace) return moe::fail(MOE_E_ARG, "%s: NULL pointer", who);
     if (((uintptr_t)x | (uintptr_t)shared_slab | (uintptr_t)out | (uintptr_t)workspace) % 16)
         return moe::fail(MOE_E_ARG, "%s: x, slabs, output and workspace must be 16-byte aligned", who);
+    const size_t need = workspace_of(T, H, I, E, k, shared_slab != nullptr);
+    if (workspace_bytes < need)
+        return moe::fail(MOE_E_NOMEM, "%s: workspace %zu < %zu bytes", who, workspace_bytes, need);
     *sp = layout(T, H, I, E, k, shared_slab != nullptr);
-    if (workspace_bytes < sp->total)
-        return moe::fail(MOE_E_NOMEM, "%s: workspace %zu < %zu bytes", who, workspace_bytes, sp->total);
     return MOE_OK;
 }
 
@@ -528,7 +538,7 @@ extern "C" size_t moe_expert_bytes_fp8(int hidden, int inter) {
 
 extern "C" size_t moe_fp8_expert_ffn_workspace_bytes(int T, int H, int I, int E, int k, int has_shared) {
     if (T < 0 || H <= 0 || I <= 0 || E <= 0 || k <= 0) return 0;
-    return layout(T, H, I, E, k, has_shared != 0).total;
+    return workspace_of(T, H, I, E, k, has_shared != 0);
 }
 
 extern "C" int moe_fp8_expert_ffn(const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_idx, int k,

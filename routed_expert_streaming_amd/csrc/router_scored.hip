@@ -14,6 +14,7 @@
 // a workgroup) and 5.1 of choice; 16 layers of 32 tokens of 6144 x 256: 20 of logits (5 TB/s
 // of w) and 24; 2048 tokens: 30 and 36.  A 64-bit winner takes 0.65 us (two reductions of 32
 // bits over the wave); 13 to 17 us is the choice where nothing has to be summed again.
+#include <algorithm>
 #include <cmath>
 
 #include "common.h"
@@ -636,8 +637,11 @@ bool split_pays(int layers, int T) { return T > (layers > 1 ? 8 : 16); }
 
 extern "C" size_t moe_router_scored_workspace_bytes(int n_layers, int T, int E, int H) {
     if (n_layers <= 0 || T <= 0 || E <= 0 || E > kMaxE || H <= 0) return 0;
-    const size_t exact = exact_bytes(T, E), split = moe::router_split_layout(n_layers, T, E, H).total;
-    return (size_t)n_layers * (split_pays(n_layers, T) && split > exact ? split : exact);
+    // enough for every call of fewer tokens or layers too, whichever way their logits come
+    size_t exact = exact_bytes(T, E);
+    if (T > kSmallT) exact = std::max(exact, exact_bytes(kSmallT, E));
+    exact *= (size_t)n_layers;
+    return split_pays(n_layers, T) ? std::max(exact, moe::router_split_most(n_layers, T, E, H)) : exact;
 }
 
 extern "C" int moe_router_scored(const uint16_t *x, int n_layers, int T, int H, const float *w_router,

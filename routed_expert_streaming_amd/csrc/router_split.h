@@ -11,6 +11,8 @@ struct RouterSplit {
     size_t partial, xn, wn, total;  // byte offsets of one layer's fp32 [parts][T][E], [parts][T], [parts][E]; bytes
 };
 RouterSplit router_split_layout(int layers, int T, int E, int H);
+// Bytes that every call of at most so many layers and tokens finds room in, all its layers.
+size_t router_split_most(int layers, int T, int E, int H);
 int router_split(const uint16_t *x, int layers, int T, int H, const float *w_router, int E, const RouterSplit &sp,
                  void *workspace, hipStream_t s);
 

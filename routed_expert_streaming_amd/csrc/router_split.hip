@@ -13,6 +13,8 @@
 // instructions for two weights, beside six products of 16 cycles for every eight a lane).
 // 2048 x 6144 x 256: 30 us, 0.64 PFLOP/s of bf16 products; the fp64 matrix cores took 209.
 // 16 layers of 32 tokens: 20 us, 5 TB/s of weights.
+#include <algorithm>
+
 #include "common.h"
 #include "lds_dma.h"
 #include "router_split.h"
@@ -196,15 +198,15 @@ __global__ __launch_bounds__(64 * kWaves) void router_split_kernel(const uint16_
 
 namespace moe {
 
+static constexpr int64_t kCUs = 256;
+static int most_parts(int H) { return std::max(1, std::min((H + kCols - 1) / kCols / 4, 16)); }
+
 RouterSplit router_split_layout(int layers, int T, int E, int H) {
     RouterSplit sp{};
     // as many parts as make one workgroup a CU, of at least four stages, at most 16
     const int64_t tiles = (int64_t)layers * ((E + kBN - 1) / kBN) * (T <= 32 ? 1 : (T + 127) / 128);
     const int stages = (H + kCols - 1) / kCols;
-    int parts = (int)(256 / (tiles < 256 ? tiles : 256));
-    parts = parts < stages / 4 ? parts : stages / 4;
-    parts = parts < 16 ? parts : 16;
-    parts = parts > 1 ? parts : 1;
+    const int parts = std::max(1, std::min((int)(kCUs / std::min(tiles, kCUs)), most_parts(H)));
     sp.columns = (stages + parts - 1) / parts * kCols;
     sp.parts = (H + sp.columns - 1) / sp.columns;
     size_t o = 0;
@@ -216,6 +218,15 @@ RouterSplit router_split_layout(int layers, int T, int E, int H) {
     o += align_up((size_t)sp.parts * E * 4, 256);
     sp.total = o;
     return sp;
+}
+
+// Fewer tokens or layers may be summed in more parts.  Two or more parts are chosen where
+// parts * layers * tiles of experts * tiles of at most 128 tokens are at most kCUs.
+size_t router_split_most(int layers, int T, int E, int H) {
+    const int64_t cap = most_parts(H), all = (int64_t)layers * T, room = kCUs / ((E + kBN - 1) / kBN);
+    const int64_t rows = std::max(all, std::min(cap * all, 128 * room));  // parts x layers x tokens
+    const int64_t parts = std::max((int64_t)layers, std::min(cap * layers, room));
+    return 4 * ((size_t)rows * (E + 1) + (size_t)parts * E) + (size_t)layers * 3 * 256;  // (rounded up by arrays)
 }
 
 int router_split(const uint16_t *x, int layers, int T, int H, const float *w_router, int E, const RouterSplit &sp,

@@ -553,7 +553,7 @@ class MoEStack:
                 L.moe_cache_split_copies(self.cache, self.copy_stream2)
         # workspaces and outputs
         self.router_ws_bytes = (L.moe_router_layers_workspace_bytes(Lyr, T, E) if routing is None else
-                                max(L.moe_router_scored_workspace_bytes(n, T, E, H) for n in (1, Lyr)))
+                                L.moe_router_scored_workspace_bytes(Lyr, T, E, H))
         self.router_ws = torch.zeros(self.router_ws_bytes, dtype=torch.uint8, device=self.dev)
         self.ffn_ws_bytes = L.moe_expert_ffn_workspace_bytes(T, H, I, E, k, self.has_shared)
         self.ffn_ws = torch.empty(self.ffn_ws_bytes, dtype=torch.uint8, device=self.dev)

@@ -256,6 +256,7 @@ class MxLinear:
 
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)  # what E4M3 codes may come as
+_FP8_PAIRS = 16384  # (token, expert) pairs of one moe_fp8_expert_ffn_combine call
 
 
 def quantise_fp8(w: torch.Tensor, block_rows: int = 128, scale_rule: int = L.MOE_FP8_SCALE_AMAX,
@@ -435,16 +436,20 @@ class Fp8MoELayer:
         return idx, w
 
     def __call__(self, x: torch.Tensor) -> torch.Tensor:
-        """x [T, H] bf16 -> [T, H] bf16, on torch's current stream of the weights' device.  No gradients."""
+        """x [T, H] bf16 -> [T, H] bf16, on torch's current stream of the weights' device.  More than 16384 (token,
+        expert) pairs are several calls.  No gradients."""
         idx, w = self.route(x)
         with torch.cuda.device(x.device):
             x = _readable_rows(x.contiguous())
-            T = x.shape[0]
-            out = torch.empty((T, self.H), dtype=torch.bfloat16, device=x.device)
-            need = L.moe_fp8_expert_ffn_workspace_bytes(T, self.H, self.I, self.E, self.k, self.shared is not None)
+            out = torch.empty_like(x)
+            most = _FP8_PAIRS // self.k  # tokens of a call
+            need = L.moe_fp8_expert_ffn_workspace_bytes(min(x.shape[0], most), self.H, self.I, self.E, self.k,
+                                                        self.shared is not None)
             ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-            L.moe_fp8_expert_ffn_combine(x, T, self.H, self.I, self.E, idx, w, self.k, self.table, self.shared, out,
-                                         ws, need, torch.cuda.current_stream())
+            for t in range(0, x.shape[0], most):  # one after the other on the stream: they share the workspace
+                n = min(most, x.shape[0] - t)
+                L.moe_fp8_expert_ffn_combine(x[t:], n, self.H, self.I, self.E, idx[t:], w[t:], self.k, self.table,
+                                             self.shared, out[t:], ws, need, torch.cuda.current_stream())
         return out
 
 

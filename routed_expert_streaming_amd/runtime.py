@@ -287,28 +287,50 @@ def quantise_fp8(w: torch.Tensor, block_rows: int = 128, scale_rule: int = L.MOE
     return codes, scales
 
 
-def pack_fp8_expert(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, slab: torch.Tensor | None = None,
+def _check_codes(weight, what: str):
+    """(codes, scales) of a checkpoint's matrix."""
+    codes, scales = weight
+    if (codes.dim() != 2 or codes.dtype not in _CODES or codes.shape[1] % 16 or scales.dtype != torch.float32
+            or tuple(scales.shape) != (-(-codes.shape[0] // 128), -(-codes.shape[1] // 128))
+            or codes.device.type != "cuda" or scales.device != codes.device):
+        raise ValueError(f"{what}: needs E4M3 codes [N, K], K a multiple of 16, and fp32 scales "
+                         "[ceil(N / 128), ceil(K / 128)] on one GPU")
+    return codes.view(torch.uint8), scales
+
+
+def _values_of(w) -> torch.Tensor:
+    """The matrix, or the codes of a checkpoint's (codes, scales): what has its shape and device."""
+    return w if isinstance(w, torch.Tensor) else w[0]
+
+
+def pack_fp8_expert(w1, w3, w2, slab: torch.Tensor | None = None,
                     scale_rule: int = L.MOE_FP8_SCALE_AMAX) -> torch.Tensor:
     """One expert's FP8 slab (cache format MOE_FP8) from its gate w1 [I,H], up w3 [I,H] and down w2 [H,I] matrices on
-    the GPU.  slab: where to write it (uint8, moe_expert_bytes_fp8(H, I) contiguous bytes, on the matrices' device or
-    the host), or None for a new tensor.  A call that is refused has written nothing."""
+    the GPU: each bf16, fp16 or fp32, quantised by scale_rule, or codes and scales of a checkpoint as quantise_fp8
+    returns them, taken as they are.  slab: where to write it (uint8, moe_expert_bytes_fp8(H, I) contiguous bytes, on
+    the matrices' device or the host), or None for a new tensor.  A call that is refused has written nothing."""
+    device = _values_of(w1).device
     for w in (w1, w3, w2):
-        _check_matrix(w, "pack_fp8_expert")
-        if w.device != w1.device:
-            raise ValueError(f"pack_fp8_expert: matrices on {w1.device} and {w.device}")
-    I, H = w1.shape
-    if tuple(w3.shape) != (I, H) or tuple(w2.shape) != (H, I):
-        raise ValueError(f"pack_fp8_expert: shapes {tuple(w1.shape)}, {tuple(w3.shape)}, {tuple(w2.shape)}")
+        if isinstance(w, torch.Tensor):
+            _check_matrix(w, "pack_fp8_expert")
+        else:
+            _check_codes(w, "pack_fp8_expert")
+        if _values_of(w).device != device:
+            raise ValueError(f"pack_fp8_expert: matrices on {device} and {_values_of(w).device}")
+    given = [tuple(_values_of(w).shape) for w in (w1, w3, w2)]
+    I, H = given[0]
+    if given != [(I, H), (I, H), (H, I)]:
+        raise ValueError(f"pack_fp8_expert: shapes {given}")
     nbytes = L.moe_expert_bytes_fp8(H, I)
     if not nbytes:
         raise ValueError(f"pack_fp8_expert: H={H}, I={I} must be multiples of 32")
     if slab is None:
-        slab = torch.empty(nbytes, dtype=torch.uint8, device=w1.device)
+        slab = torch.empty(nbytes, dtype=torch.uint8, device=device)
     on_host = slab.device.type == "cpu"
     if (slab.dtype != torch.uint8 or slab.numel() != nbytes or not slab.is_contiguous()
-            or not (on_host or (slab.device == w1.device and slab.data_ptr() % 16 == 0))):
+            or not (on_host or (slab.device == device and slab.data_ptr() % 16 == 0))):
         raise ValueError(f"pack_fp8_expert: the slab must be {nbytes} contiguous bytes (uint8), 16-byte aligned, on "
-                         f"{w1.device} or the host")
+                         f"{device} or the host")
     slab = slab.view(-1)
     if on_host:
         slab.copy_(pack_fp8_expert(w1, w3, w2, None, scale_rule))  # waits for the copy
@@ -316,8 +338,12 @@ def pack_fp8_expert(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, slab: 
     hb, ib = (H + 127) // 128, (I + 127) // 128
     at, scale_at = 0, 3 * H * I
     for w, shape, blocks in ((w1, (I, H), (ib, hb)), (w3, (I, H), (ib, hb)), (w2, (H, I), (hb, ib))):
-        scales = slab[scale_at:scale_at + 4 * ib * hb].view(torch.float32).view(blocks)
-        quantise_fp8(w, 128, scale_rule, slab[at:at + H * I].view(shape), scales)
+        codes, scales = slab[at:at + H * I].view(shape), slab[scale_at:scale_at + 4 * ib * hb].view(torch.float32).view(blocks)
+        if isinstance(w, torch.Tensor):
+            quantise_fp8(w, 128, scale_rule, codes, scales)
+        else:
+            for to, part in zip((codes, scales), _check_codes(w, "pack_fp8_expert")):
+                to.copy_(part)
         at, scale_at = at + H * I, scale_at + 4 * ib * hb
     slab[scale_at:].zero_()
     return slab
@@ -336,13 +362,8 @@ class Fp8Linear:
         if isinstance(weight, torch.Tensor):
             codes, scales = quantise_fp8(weight, 128, scale_rule)
         else:
-            codes, scales = weight
-            if (codes.dim() != 2 or codes.dtype not in _CODES or codes.shape[1] % 16 or scales.dtype != torch.float32
-                    or tuple(scales.shape) != (-(-codes.shape[0] // 128), -(-codes.shape[1] // 128))
-                    or codes.device.type != "cuda" or scales.device != codes.device):
-                raise ValueError("Fp8Linear: needs E4M3 codes [N, K], K a multiple of 16, and fp32 scales "
-                                 "[ceil(N / 128), ceil(K / 128)] on one GPU")
-            codes, scales = _readable_rows(codes.view(torch.uint8).contiguous()), scales.contiguous()
+            codes, scales = _check_codes(weight, "Fp8Linear")
+            codes, scales = _readable_rows(codes.contiguous()), scales.contiguous()
         self.N, self.K = codes.shape
         self.codes, self.scales = codes, scales
         self.bias = None if bias is None else bias.to(codes.device, torch.float32).contiguous()
@@ -390,8 +411,8 @@ class Fp8MoELayer:
     feed-forward and its weighted combine (moe_fp8_expert_ffn_combine).
 
     router [E, H], bias and balance [E] (or None): made fp32; experts: E triples (w1 [I,H], w3 [I,H], w2 [H,I]) on
-    the GPU, packed once, here; shared: such a triple for every token, or None; routing: a moe_routing, k experts a
-    token."""
+    the GPU as pack_fp8_expert takes them, packed once, here; shared: such a triple for every token, or None; routing:
+    a moe_routing, k experts a token."""
 
     def __init__(self, router: torch.Tensor, experts, k: int, routing: L.moe_routing,
                  bias: torch.Tensor | None = None, balance: torch.Tensor | None = None, shared=None,
@@ -400,9 +421,10 @@ class Fp8MoELayer:
         self.k, self.routing = k, routing
         if len(experts) != self.E:
             raise ValueError(f"Fp8MoELayer: {len(experts)} experts for a router of {self.E}")
-        self.I = experts[0][0].shape[0]
+        self.I = _values_of(experts[0][0]).shape[0]
         dev = router.device
-        for w1, w3, w2 in list(experts) + ([] if shared is None else [shared]):
+        for expert in list(experts) + ([] if shared is None else [shared]):
+            w1 = _values_of(expert[0])
             if tuple(w1.shape) != (self.I, self.H) or w1.device != dev:
                 raise ValueError(f"Fp8MoELayer: an expert of {tuple(w1.shape)} on {w1.device}, not "
                                  f"{(self.I, self.H)} on {dev}")

@@ -38,8 +38,4 @@ double *router_partials_buf(void *workspace, int T, int E);
 int router_partials(const uint16_t *x, int T, int H, const float *w_router, int E, double *partial, hipStream_t s,
                     int layers = 1, size_t ws_stride = 0);
 
-// Logits [T][E] of more than 32 tokens on the fp64 matrix cores.
-int router_logits_rows(const uint16_t *x, int T, int H, const float *w_router, const float *bias, int E, float *logits,
-                       hipStream_t s);
-
 }  // namespace moe

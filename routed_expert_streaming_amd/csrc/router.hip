@@ -15,6 +15,7 @@
 //    then a top-k kernel with one wavefront per token.
 #include "common.h"
 #include "router.h"
+#include "router_rows.h"
 #include "topk.h"
 
 namespace {

@@ -19,6 +19,7 @@
 
 #include "common.h"
 #include "router.h"
+#include "router_rows.h"
 #include "router_split.h"
 #include "topk.h"
 

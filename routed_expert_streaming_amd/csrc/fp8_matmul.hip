@@ -18,8 +18,8 @@ using moe::f32x4;
 constexpr int kMaxRows = 1 << 26;        // M and N
 constexpr int kMaxK = 1 << 27;
 constexpr int64_t kMaxStride = 1 << 28;
-// bytes of y from which a tile kernel writes past the caches (2048 x 6144 x 6144: 3.5 us
-// less, which the caches took to write back at the kernel's end)
+// bytes of a bf16 y from which a tile kernel writes past the caches (2048 x 6144 x 6144: 3.5
+// us less, which the caches took to write back at the kernel's end)
 constexpr int64_t kStreamFrom = 4 << 20;
 
 struct MatArgs {
@@ -32,19 +32,19 @@ struct MatArgs {
     const float *bias;
     uint8_t *y;
     size_t y_stride;
-    bool y_f32;
     bool ends;  // the caller's rows of scales, which may end inside 16 bytes
     __device__ __forceinline__ uint8_t *row(int m) const { return y + (size_t)m * y_stride; }
 };
 
-// Four outputs n .. n+3 of row m (those below N), bias added, rounded once.
+// Four outputs n .. n+3 of row m (those below N), bias added, rounded once.  F32: y's type.
+template <bool F32>
 __device__ __forceinline__ void store4(const MatArgs &p, int m, int n, const f32x4 v) {
     if (m >= p.M) return;
     uint8_t *row = p.y + (size_t)m * p.y_stride;
     float f[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[j] = v[j] + (p.bias && n + j < p.N ? p.bias[n + j] : 0.0f);
-    if (p.y_f32) {
+    if constexpr (F32) {
         float *o = (float *)row + n;
         if (n + 3 < p.N && (uintptr_t)o % 16 == 0) {
             *reinterpret_cast<float4 *>(o) = make_float4(f[0], f[1], f[2], f[3]);
@@ -100,8 +100,8 @@ __global__ __launch_bounds__(64 * WK) void fp8_matmul_rows_kernel(MatArgs p) {
     for (int i0 = 0; i0 < NT * MT; i0 += WK) {
         const int i = i0 + wave;
         if (i >= NT * MT) break;
-        store4(p, m0 + 16 * (i % MT) + r, n0 + 16 * (i / MT) + 4 * q,
-               moe::joined<WK, NT * MT>(part, i, lane));
+        store4<WIDE>(p, m0 + 16 * (i % MT) + r, n0 + 16 * (i / MT) + 4 * q,
+                     moe::joined<WK, NT * MT>(part, i, lane));
     }
 }
 
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(64 * T::WAVES) void fp8_matmul_tile_kernel(MatArgs 
 #pragma unroll
                 for (int u = 0; u < MT; ++u) acc[t][u][j] += c;
             }
-    if (p.y_f32)
+    if constexpr (WIDE)
         moe::store_tile<T, MT, NT, float>(p, smem, m0, n0, wm, wn, lane, acc, all < T::GROUP);
     else
         moe::store_tile<T, MT, NT, uint16_t, STREAM>(p, smem, m0, n0, wm, wn, lane, acc, all < T::GROUP);
@@ -172,9 +172,10 @@ template <bool WIDE, class T>
 void launch_tile(const MatArgs &p, hipStream_t s) {
     const int m_tiles = (p.M + T::BM - 1) / T::BM, n_tiles = (p.N + T::BN - 1) / T::BN;
     const unsigned grid = (unsigned)(((int64_t)m_tiles * n_tiles + 7) / 8 * 8);
-    const bool stream = (int64_t)p.M * p.N * 2 >= kStreamFrom;
-    auto *kernel = p.ends ? (stream ? fp8_matmul_tile_kernel<WIDE, T, true, true> : fp8_matmul_tile_kernel<WIDE, T, false, true>)
-                          : (stream ? fp8_matmul_tile_kernel<WIDE, T, true, false> : fp8_matmul_tile_kernel<WIDE, T, false, false>);
+    auto *kernel = p.ends ? fp8_matmul_tile_kernel<WIDE, T, false, true> : fp8_matmul_tile_kernel<WIDE, T, false, false>;
+    if constexpr (!WIDE)
+        if ((int64_t)p.M * p.N * 2 >= kStreamFrom)
+            kernel = p.ends ? fp8_matmul_tile_kernel<WIDE, T, true, true> : fp8_matmul_tile_kernel<WIDE, T, true, false>;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * T::WAVES), 0, s, p, m_tiles, n_tiles);
 }
 
@@ -196,7 +197,7 @@ __global__ __launch_bounds__(64 * WK) void fp8_matmul_few_kernel(MatArgs p) {
     });
     part[wave][0][lane] = acc[0];
     __syncthreads();
-    if (wave == 0) store4(p, r, n0 + 4 * q, moe::joined<WK, 1>(part, 0, lane));
+    if (wave == 0) store4<WIDE>(p, r, n0 + 4 * q, moe::joined<WK, 1>(part, 0, lane));
 }
 
 // Which kernel a product takes: the least estimated time, in us.  A round of as many
@@ -277,7 +278,7 @@ bool few(bool quantise, int M, int N, int K) {
            (M == 1 || values <= (N <= 4096 ? kFewValuesNarrow : kFewValues));
 }
 
-// WIDE: products of codes converted to bf16, for fp32 outputs.
+// WIDE: fp32 outputs, from products of codes converted to bf16.
 template <bool WIDE>
 int run(const MatArgs &p, Kind kind, hipStream_t s) {
     switch (kind) {
@@ -381,7 +382,6 @@ extern "C" int moe_fp8_matmul(const void *a, int a_type, int64_t a_stride, const
     p.bias = bias;
     p.y = (uint8_t *)y;
     p.y_stride = M > 1 ? (size_t)y_stride : 0;
-    p.y_f32 = y_type == MOE_FP32;
     p.ends = !quantise && moe::fp8_blocks(K) % 4 != 0;
     const bool here = few(quantise, M, N, K);
     if (quantise && !here) {
@@ -394,6 +394,7 @@ extern "C" int moe_fp8_matmul(const void *a, int a_type, int64_t a_stride, const
     }
     const size_t far = (size_t)kTileStride;
     const bool near = (M == 1 || (p.a.stride < far && p.a.scale_stride < far)) && (N == 1 || p.w_stride < far);
-    const Kind kind = here ? FEW : plan(p.y_f32, M, N, K, near);
-    return p.y_f32 ? run<true>(p, kind, s) : run<false>(p, kind, s);
+    const bool wide = y_type == MOE_FP32;
+    const Kind kind = here ? FEW : plan(wide, M, N, K, near);
+    return wide ? run<true>(p, kind, s) : run<false>(p, kind, s);
 }

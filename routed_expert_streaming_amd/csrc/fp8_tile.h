@@ -174,7 +174,8 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
     };
     // A product's result enters the sums when LAG more products have been issued, so that
     // no addition waits for its own product.  (The pin keeps that order: left to itself
-    // the compiler gathers the products and spills.)
+    // the compiler gathers the products and spills.  256 x 256 tiles still spill 8 of their 256
+    // registers, 20 bytes a lane.)
     constexpr int LAG = T::LAG;
     static_assert(NT * MT % LAG == 0, "a product's place");
     f32x4 done[LAG];

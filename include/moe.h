@@ -125,9 +125,10 @@ int moe_router_topk_layers(const uint16_t *x, int n_layers, int T, int H, const 
  * them; moe_router_topk's are exact), so their last bits may depend on T and n_layers.  n_groups = top_groups = 1 for no groups.  A NaN
  * score ranks first; a balance of -infinity leaves its expert to the last.
  * 1 <= k <= min(64, top_groups * E / n_groups), E <= 1024, n_groups <= 64 and a divisor of
- * E, H a multiple of 32 up to 16384, n_layers <= 65535 (MOE_E_SHAPE); MOE_E_ARG for a NULL
- * pointer, a negative T or n_layers, an unknown score or rule, a scale that is not finite,
- * or x, w_router or workspace not 16-byte aligned.  T = 0 or n_layers = 0 is a no-op.
+ * E (each of two experts at least where MOE_GROUP_TOP2 drops some), H a multiple of 32 up to
+ * 16384, T <= 2^26 - 4, n_layers <= 65535 (MOE_E_SHAPE); MOE_E_ARG for a NULL pointer, a
+ * negative T or n_layers, an unknown score or rule, a scale that is not finite, or x,
+ * w_router or workspace not 16-byte aligned.  T = 0 or n_layers = 0 is a no-op.
  * workspace: moe_router_scored_workspace_bytes(n_layers, T, E, H) bytes (contents don't
  * care; calls sharing it must not overlap in time), which never falls as n_layers or T
  * grows: one of the longest call's serves all.  The description is read before the call

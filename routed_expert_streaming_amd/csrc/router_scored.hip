@@ -28,6 +28,7 @@ namespace {
 constexpr int kSmallT = 32;  // up to here the logits come from router_partials
 constexpr int kMaxE = moe::kTopkMaxE;
 constexpr int kMaxGroups = 64;
+constexpr int kMaxT = (1 << 26) - 4;  // 64 threads a token: a grid of fewer than 2^32
 
 struct Choice {
     int E, k, score, groups, top_groups, top2, renorm;
@@ -637,7 +638,7 @@ bool split_pays(int layers, int T) { return T > (layers > 1 ? 8 : 16); }
 }  // namespace
 
 extern "C" size_t moe_router_scored_workspace_bytes(int n_layers, int T, int E, int H) {
-    if (n_layers <= 0 || T <= 0 || E <= 0 || E > kMaxE || H <= 0) return 0;
+    if (n_layers <= 0 || T <= 0 || T > kMaxT || E <= 0 || E > kMaxE || H <= 0) return 0;
     // enough for every call of fewer tokens or layers too, whichever way their logits come
     size_t exact = exact_bytes(T, E);
     if (T > kSmallT) exact = std::max(exact, exact_bytes(kSmallT, E));
@@ -674,7 +675,8 @@ extern "C" int moe_router_scored(const uint16_t *x, int n_layers, int T, int H, 
     if (T == 0 || n_layers == 0) return MOE_OK;
     if (!x || !w_router || !topk_idx || !topk_w || !workspace)
         return moe::fail(MOE_E_ARG, "router_scored: NULL pointer");
-    if (n_layers > 65535) return moe::fail(MOE_E_SHAPE, "router_scored: n_layers=%d above 65535", n_layers);
+    if (n_layers > 65535 || T > kMaxT)
+        return moe::fail(MOE_E_SHAPE, "router_scored: n_layers=%d above 65535 or T=%d above %d", n_layers, T, kMaxT);
     if (((uintptr_t)x | (uintptr_t)w_router) % 16 || (uintptr_t)workspace % 16)
         return moe::fail(MOE_E_ARG, "router_scored: x, w_router and workspace must be 16-byte aligned");
     const size_t need = moe_router_scored_workspace_bytes(n_layers, T, E, H);

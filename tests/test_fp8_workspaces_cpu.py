@@ -42,3 +42,13 @@ def test_experts(H, I, E, k, shared):
 def test_product(N, K, kind):
     size = [L.moe_fp8_matmul_workspace_bytes(M, N, K, kind) for M in range(1, 600)]
     assert all(a <= b for a, b in zip(size, size[1:]))
+
+
+def test_router_refuses_more_tokens_than_a_grid_holds():
+    how = L.moe_routing(L.MOE_SCORE_SIGMOID, 1, 1, L.MOE_GROUP_MAX, 1, 1.0)
+    for T in ((1 << 26) - 3, 1 << 26, (1 << 31) - 1):
+        with pytest.raises(L.MoEError) as ei:
+            L.moe_router_scored(0x1000, 1, T, 32, 0x1000, None, None, 4, 1, how, 0x1000, 0x1000, 0x1000, 0)
+        assert ei.value.status == L.MOE_E_SHAPE
+        assert L.moe_router_scored_workspace_bytes(1, T, 4, 32) == 0
+    assert L.moe_router_scored_workspace_bytes(1, (1 << 26) - 4, 4, 32) > 0

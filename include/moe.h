@@ -122,8 +122,9 @@ int moe_router_topk_layers(const uint16_t *x, int n_layers, int T, int H, const 
  * balance [n_layers, E] fp32 or NULL).  The choice and its order are those of the formulas
  * in every call; with more than a few tokens the weights come from logits that are summed
  * in fp32 (off by at most 2e-5 times the norms of x[t,:] and w[e,:], in practice by 1e-7 of
- * them; moe_router_topk's are exact), so their last bits may depend on T and n_layers.  n_groups = top_groups = 1 for no groups.  A NaN
- * score ranks first; a balance of -infinity leaves its expert to the last.
+ * them; moe_router_topk's are exact), so their last bits may depend on T and n_layers.
+ * n_groups = top_groups = 1 for no groups.  A NaN score ranks first; a balance of -infinity
+ * leaves its expert to the last.
  * 1 <= k <= min(64, top_groups * E / n_groups), E <= 1024, n_groups <= 64 and a divisor of
  * E (each of two experts at least where MOE_GROUP_TOP2 drops some), H a multiple of 32 up to
  * 16384, T <= 2^26 - 4, n_layers <= 65535 (MOE_E_SHAPE); MOE_E_ARG for a NULL pointer, a
@@ -596,7 +597,8 @@ enum { MOE_FP8_SCALE_AMAX = 0, MOE_FP8_SCALE_POW2 = 1 };
 int moe_fp8_quant(const void *x, int x_type, int64_t x_stride, int rows, int K, int block_rows, int scale_rule,
                   uint8_t *codes, int64_t codes_stride, float *scales, int64_t scales_stride, void *stream);
 /* y[m,n] = sum over blocks b of K of a_scales[m,b] * w_scales[n / 128, b] * (sum over k in b of A[m,k] * W[n,k])
- *          + bias[n],  sums in fp32, rounded once.
+ *          + bias[n],  sums in fp32, rounded once.  The product of the two scales is made first,
+ * in fp32, and has to lie in its range (beyond it is 0 or infinity).
  * With y in fp32 the products are exact.  With y in bf16 they run on the FP8 matrix cores,
  * which keep of each 8 products (8 neighbouring columns) the bits down to 2^-13 of the
  * largest one: a sum is off by at most 7 * 2^-13 of its terms' magnitudes, in practice by

@@ -405,7 +405,11 @@ bool few(int T, int k) { return T <= moe::kFewRows && (int64_t)T * k <= kScanPai
 // Rows of a tile, by the rows an expert has on average.  Tiles of 16 rows leave two
 // workgroups a CU and keep up with memory (32 tokens, top 8 of 128 experts of 4096 x 1536:
 // 2.1 GB of weights in 380 us); tall ones read and convert each row of W once for all of an
-// expert's rows (2048 tokens: gate/up 650 us, down 280; in tiles of 64 rows 850 and 370).
+// expert's rows.  Those experts, a call in a graph, us in tiles of 16, 64 and up to 160 rows:
+//   rows an expert    8    16    24    32    48    64    96   128
+//   16              447   497   575   680   865  1056  1436  1833
+//   64              494   503   503   515   559   680   848  1005
+//   160             493   493   507   517   542   603   702   833
 int tile_rows(int T, int E, int k) {
     const int64_t pairs = (int64_t)T * k;
     return pairs >= (int64_t)64 * E ? 160 : pairs >= (int64_t)24 * E ? 64 : 16;

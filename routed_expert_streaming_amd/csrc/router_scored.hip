@@ -7,13 +7,15 @@
 //
 // One wavefront a token; lane l holds experts l, l + 64, ...  A group's worth (its largest
 // score or the sum of its two largest) is found by as many lanes as fit the wave, from
-// the scores in LDS; the groups are then ranked by counting, and the top-k runs over
-// order-preserving 64-bit codes in registers.
+// the scores in LDS; the groups are then ranked by counting.  Where every logit is exact
+// the top-k runs over order-preserving 64-bit codes in registers, a winner after the other
+// (0.65 us each: two reductions of 32 bits over the wave).  Where the logits come with a
+// bound on their error, nearly every token is chosen by 32-bit scores with margins, and
+// only what these tell apart too little is summed and scored again in 64 bits.
 //
 // What bounds it: latency.  One token of 4096 x 128: 3.7 us of logits (a launch, a row of w
-// a workgroup) and 5.1 of choice; 16 layers of 32 tokens of 6144 x 256: 20 of logits (5 TB/s
-// of w) and 24; 2048 tokens: 30 and 36.  A 64-bit winner takes 0.65 us (two reductions of 32
-// bits over the wave); 13 to 17 us is the choice where nothing has to be summed again.
+// a workgroup) and 5.1 of choice.  16 layers of 32 tokens of 6144 x 256: 20 of logits (5 TB/s
+// of w) and 24 of choice, 9 of them sums made again; 2048 tokens: 31 and 35, 18 of them.
 #include <algorithm>
 #include <cmath>
 
@@ -629,10 +631,16 @@ size_t exact_bytes(int T, int E) {
     return T <= kSmallT ? (size_t)T * E * moe::kMaxSlices * sizeof(double)
                         : moe::align_up((size_t)T * E * sizeof(float), 256);
 }
-// Where the logits come from the split sums: from a dozen tokens on.  One layer of 4096 x
-// 128 and of 6144 x 256, us with exact sums and split: 8 tokens 16 against 23, 21 against
-// 30; 16: 23 against 24, 30 against 36; 32: 38 against 26, 51 against 38.  Eight layers
-// of 4096 x 128: 8 tokens 24 against 30, 16: 37 against 33.
+// Where the logits come from the split sums.  Calls of sigmoid scores with a balance, in a
+// graph, us with exact sums and split:
+//   tokens                    4         8         9        12        16        17        32
+//   1 layer, 4096 x 128    11  19    15  19    16  19    19  19    23  20    24  20    37  21
+//   1 layer, 6144 x 256    16  24    20  25    21  25    24  26    28  26    29  27    51  29
+//   1 layer, 1024 x 64     10  13    14  14    15  15    18  15    22  15    23  15    37  15
+//   8 layers, 4096 x 128   16  23    23  24    25  24    30  24    36  25    37  26    61  25
+//   16 layers, 6144 x 256  52  40    74  41    80  41    96  42   118  44   123  43   214  45
+// So the split would pay from 9 to 13 tokens of one layer on, and from fewer of many large
+// layers; the rule keeps the weights of up to 16 tokens (8 of several layers) exact.
 bool split_pays(int layers, int T) { return T > (layers > 1 ? 8 : 16); }
 
 }  // namespace
@@ -686,7 +694,9 @@ extern "C" int moe_router_scored(const uint16_t *x, int n_layers, int T, int H, 
                    routing->scale};
     hipStream_t s = (hipStream_t)stream;
     Logits from{Logits::PARTIALS, (const char *)workspace, exact_bytes(T, E), {}, x, w_router, bias, T, H};
-    // (a softmax next to a balance needs every logit exact: the split would tell too little apart)
+    // A softmax next to a balance takes exact sums: the split's bound is on ratios of its scores,
+    // and beside a balance their sum's error counts too.  2048 x 6144 x 256: 205 us (51 without
+    // the balance); 16 layers of 32 tokens: 216 (42).
     if (split_pays(n_layers, T) && !(balance && routing->score == MOE_SCORE_SOFTMAX)) {
         from.kind = Logits::SPLIT;
         from.sp = moe::router_split_layout(n_layers, T, E, H);

@@ -91,16 +91,16 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
     };
     const int se = wave % T::SCALE_LOADS;  // (several waves bring the same rows)
     const uint32_t s_off = as_off(min(64 * se + lane, T::BM - 1));
+    // ENDS: the row's last scales where they are fewer than four, kept from the start (a load of them
+    // in their turn would be waited for behind the rings': 0.3 us of a short product).  They take a
+    // load's place, so the waits do not count on the scales' loads.
+    constexpr int NO_SCALES = ENDS && KW > 1 ? 1 : 0;
+    float last[3] = {0.f, 0.f, 0.f};
     auto issue_scales = [&](int i) __attribute__((always_inline)) {  // of stage i's block and its neighbours
         const int place = KW == 1 ? i >> 2 & 1 : i % SA, first = block_of(i) & ~3;
         const uint32_t at = T::S_RING + (uint32_t)place * T::CHUNK + 1024u * se;
         if (ENDS && first + 4 > blocks) {
-            // fewer than four: value by value.  The waves' waits stay right without the load that they
-            // count here, because these values are waited for, and with them every load before them.
-            const float *from = reinterpret_cast<const float *>(as + s_off);
-            float *to = reinterpret_cast<float *>(ring + at + 16 * lane);
-#pragma unroll 1
-            for (int b = first; b < blocks; ++b) to[b - first] = from[b];
+            *reinterpret_cast<f32x4 *>(ring + at + 16 * lane) = f32x4{last[0], last[1], last[2], 0.f};
         } else {
             dma16(as + 4 * (size_t)first, s_off, lds0 + at);
         }
@@ -133,7 +133,16 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
     // Issue order, which the waits count on: the first scales, W's stages 0 .. SW-1 and A's
     // 0 .. SA-1 by turns, then after the turn from block g to g + 1 W's stage g + SW and A's
     // g + SA (and scales before them).
+    if (ENDS) {
+        const float *from = reinterpret_cast<const float *>(as + s_off) + (blocks & ~3);
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            if ((blocks & ~3) + j < blocks) last[j] = from[j];
+    }
     load_ws(0);
+    if (ENDS)
+#pragma unroll
+        for (int j = 0; j < 3; ++j) asm volatile("" : "+v"(last[j]));
     if (KW == 1) issue_scales(0);
 #pragma unroll
     for (int i = 0; i < SA; ++i) {
@@ -146,7 +155,7 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
             for (int j = 0; j < T::A_EACH; ++j) issue_a(i, j);
     }
     if (nb >= SA)
-        wait_vm<(SW - 1) * T::W_EACH + (SA - 1) * (T::EACH - T::W_EACH)>();
+        wait_vm<(SW - 1) * T::W_EACH + (SA - 1) * (T::EACH - T::W_EACH - NO_SCALES)>();
     else
         wait_vm<0>();
     ring_barrier();
@@ -167,7 +176,7 @@ __device__ __forceinline__ void fp8_tile(uint8_t *smem, const uint8_t *w, const 
     // g + 1 - SW + SA (itself needed where SA = SW) and what SW - 2 turns issued.
     auto turn = [&](int g) __attribute__((always_inline)) {
         if (g + SA <= nb)
-            wait_vm<(SW - 2) * T::EACH + (SA > SW ? T::A_EACH : 0)>();  // (scales come first)
+            wait_vm<(SW - 2) * (T::EACH - NO_SCALES) + (SA > SW ? T::A_EACH : 0)>();  // (scales come first)
         else
             wait_vm<0>();
         ring_barrier();

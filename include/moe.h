@@ -639,7 +639,8 @@ int moe_fp8_matmul(const void *a, int a_type, int64_t a_stride, const float *a_s
  * MOE_FP8 in its descriptor.
  * MOE_E_ARG for T < 0, NULL pointers, or x, shared_slab, y, out or workspace not 16-byte
  * aligned; MOE_E_NOMEM for a workspace below moe_fp8_expert_ffn_workspace_bytes (which
- * never falls as T grows); T = 0 is a no-op.  The combine call needs every routed expert's slab and has no mask. */
+ * never falls as T grows); T = 0 is a no-op.  The combine call needs every routed expert's
+ * slab and has no mask. */
 size_t moe_expert_bytes_fp8(int hidden, int inter);
 size_t moe_fp8_expert_ffn_workspace_bytes(int T, int H, int I, int E, int k, int has_shared);
 int moe_fp8_expert_ffn(const uint16_t *x, int T, int H, int I, int E, const int32_t *topk_idx, int k,

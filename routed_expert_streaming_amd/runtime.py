@@ -317,6 +317,8 @@ def pack_fp8_expert(w1, w3, w2, slab: torch.Tensor | None = None,
             _check_codes(w, "pack_fp8_expert")
         if _values_of(w).device != device:
             raise ValueError(f"pack_fp8_expert: matrices on {device} and {_values_of(w).device}")
+    if scale_rule not in (L.MOE_FP8_SCALE_AMAX, L.MOE_FP8_SCALE_POW2):
+        raise ValueError(f"pack_fp8_expert: scale_rule {scale_rule}")
     given = [tuple(_values_of(w).shape) for w in (w1, w3, w2)]
     I, H = given[0]
     if given != [(I, H), (I, H), (H, I)]:

@@ -65,4 +65,6 @@ def test_experts_of_a_checkpoint():
                 (codes.cpu(), scales.cpu()), (codes[:, :96], scales[:, :1]), good[0]):
         with pytest.raises(ValueError):
             pack_fp8_expert(good[0], good[1], bad, slab=slab)
+    with pytest.raises((ValueError, L.MoEError)):  # a rule that only the last matrix would need
+        pack_fp8_expert(good[0], good[1], matrix(2, H, I), slab=slab, scale_rule=2)
     assert (slab == 7).all()
